@@ -166,6 +166,67 @@ witcert_status witcert_write_ragged(witcert_cache* cache, int layer, const void*
                                     const void* K_hat, const void* V_hat, const int32_t* n_tok,
                                     void* stream);
 
+/* Rotary positions (Su et al., "RoFormer", 2021).  Pair p of a head's first rotary_dim channels,
+ * channels (p, p + rotary_dim/2) or, interleaved, (2p, 2p + 1), turns by position x freq[p] radians
+ * and is multiplied by scale; later channels pass unchanged (and unscaled).  Scaled frequencies for
+ * long contexts are the caller's freq (the Python binding's Rope fills it).  Angles are exact to the
+ * rounding of freq at any 64-bit position. */
+typedef struct {
+  int rotary_dim;            /* a multiple of 8, at most the head dimension */
+  int interleaved;
+  double scale;
+  double freq[128];          /* the first rotary_dim / 2 are used; finite */
+} witcert_rope_config;
+
+/* A tensor [n_tok][n_heads][head_dim] and where its rotation goes: strides in elements, channels
+ * adjacent.  y may be x itself (with its strides); other overlaps are undefined. */
+typedef struct {
+  const void* x;
+  void* y;
+  int n_heads;
+  long long x_token_stride, x_head_stride, y_token_stride, y_head_stride;
+} witcert_rope_tensor;
+
+/* Rotate q and, unless k is NULL, k by the tokens' positions (device int64 [n_tok], any values) in
+ * one launch.  dtype is that of both; head_dim is even, at most 256.  inverse turns the other way
+ * (times the same scale): the gradient with respect to x of the rotation, given that of y.
+ * Asynchronous on `stream`; no cache is involved.  EINVAL on bad arguments. */
+witcert_status witcert_rope(const witcert_rope_config* rope, witcert_dtype dtype, int head_dim, int n_tok,
+                            const int64_t* positions, const witcert_rope_tensor* q, const witcert_rope_tensor* k,
+                            int inverse, void* stream);
+
+/* witcert_write and witcert_write_hat for keys without positions: the token at position t of a
+ * sequence has its key (and K_hat) turned by pos_offset + t and rounded to kv_dtype on the way; the
+ * cache then holds what writing that rotated key would have stored, bit for bit (codes, witness,
+ * exact copies).  V is stored as given.  K_hat and V_hat are NULL unless the cache is a black-box
+ * one.  Exact keys of a gated cache reach the pinned backing store by the writers' stores.  EINVAL
+ * as for the plain writes and for a bad rope. */
+witcert_status witcert_write_rope(witcert_cache* cache, int layer, const void* K, const void* V, const void* K_hat,
+                                  const void* V_hat, int n_tok, const witcert_rope_config* rope, void* stream);
+
+/* Ragged append with rotation: witcert_write_ragged (packed rows, host counts) with every key
+ * turned by its own sequence's position, as for witcert_write_rope. */
+witcert_status witcert_write_rope_ragged(witcert_cache* cache, int layer, const void* K, const void* V,
+                                         const void* K_hat, const void* V_hat, const int32_t* n_tok,
+                                         const witcert_rope_config* rope, void* stream);
+
+/* Drop tokens from the end (drafted tokens that were not accepted): sequence i of `layer`, or of
+ * every layer if layer is -1, keeps its first lengths[i] tokens (host [batch], >= 0; a sequence that
+ * is not longer stays as it is).  The next append takes the freed positions.  Pages stay with the
+ * sequence until it is reset; repairs of its blocks stay.  Block risks become stale (witcert_gate
+ * needs a new decode).  EINVAL for a KIVI2 cache where a finished 16-token block would reopen: its
+ * exact keys are gone.  Asynchronous on `stream`. */
+witcert_status witcert_truncate(witcert_cache* cache, int layer, const int32_t* lengths, void* stream);
+
+/* The keys and values the cache stands for: tokens t0[i] .. t0[i] + n_tok[i] - 1 of every sequence
+ * (host [batch]; t0 NULL: each sequence's last n_tok[i]) as rows of kv_dtype, packed sequence by
+ * sequence into device K, V [sum n_tok][n_kv_heads][128].  Exact keys where the cache holds them
+ * (repaired blocks, KIVI2's unfinished block); otherwise the decoded values (the dithered scheme's
+ * with the dither taken off), formed in fp32 and rounded once.  EINVAL for rows past a sequence's
+ * length.  Asynchronous on `stream`, after a pending gate of the layer. */
+witcert_status witcert_read(witcert_cache* cache, int layer, const int32_t* t0, const int32_t* n_tok, void* K,
+                            void* V, void* stream);
+
 /* Empty sequence `seq` in every layer so the slot can serve a new request (continuous
  * batching).  Its repairs are dropped too (their slots in the exact-key pool are not
  * reused), a paged cache returns its pages to the pool, and its value witnesses are zeroed

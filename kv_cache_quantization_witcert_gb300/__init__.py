@@ -7,6 +7,7 @@ the C ABI (include/witcert.h): witcert_create / write / decode / gate / ...
 from __future__ import annotations
 
 import ctypes
+import math
 
 import torch
 
@@ -14,7 +15,7 @@ from . import _lib
 from ._lib import (BF16, BLACKBOX, EINVAL, ENOMEM, EPAGEIN, ESTATE, ETIMEDOUT, F32, FP8_E4M3, INT8_DITHER,  # noqa: F401
                    INT8_RTN, KIVI2, SCHEMES, WitcertError, check, load)
 
-__all__ = ["Cache", "witcert_dither", "witcert_merge_partials", "witcert_gate_select", "WitcertError", "load", "SCHEMES", "PART_STRIDE"]
+__all__ = ["Cache", "Rope", "witcert_rope", "witcert_dither", "witcert_merge_partials", "witcert_gate_select", "WitcertError", "load", "SCHEMES", "PART_STRIDE"]
 
 _TORCH_DT = {F32: torch.float32, BF16: torch.bfloat16}
 
@@ -58,6 +59,102 @@ def _need(*specs):
     for name, t in given:
         if not t.is_cuda:
             raise ValueError(f"{name} must be a CUDA tensor")
+
+
+class Rope:
+    """Rotary positions: the first `rotary_dim` channels of a head, pairs (p, p + rotary_dim/2) or,
+    interleaved, (2p, 2p + 1), pair p turning base^(-2p / rotary_dim) radians a position.
+
+    scaling None: as above.  "linear": every frequency / factor (position interpolation, Chen et
+    al., 2023).  "by_parts" (Peng et al., "YaRN", 2023): pairs that turn more than `fast` times in
+    the original_tokens the model was trained on keep their frequency, those under `slow` turns take
+    frequency / factor, a linear ramp between; the vectors are scaled by 0.1 ln(factor) + 1.
+    freq (rotary_dim / 2 radians per position) and scale override what these give."""
+
+    def __init__(self, rotary_dim=128, base=10000.0, interleaved=False, scaling=None, factor=1.0,
+                 original_tokens=4096, fast=32.0, slow=1.0, freq=None, scale=None):
+        rotary_dim = int(rotary_dim)
+        if rotary_dim < 8 or rotary_dim % 8 or rotary_dim > 256:
+            raise ValueError(f"rotary_dim must be a multiple of 8 in [8, 256], got {rotary_dim}")
+        if scaling not in (None, "linear", "by_parts"):
+            raise ValueError(f'scaling must be None, "linear" or "by_parts", got {scaling!r}')
+        if not (base > 0 and math.isfinite(base) and factor > 0 and math.isfinite(factor)):
+            raise ValueError("base and factor must be positive and finite")
+        gain = 1.0
+        if freq is None:
+            freq = [base ** (-2.0 * p / rotary_dim) for p in range(rotary_dim // 2)]
+            if scaling == "linear":
+                freq = [f / factor for f in freq]
+            elif scaling == "by_parts":
+                if not (fast > slow >= 0 and original_tokens > 0):
+                    raise ValueError("by_parts needs fast > slow >= 0 and original_tokens > 0")
+                keep = [min(max((original_tokens * f / (2 * math.pi) - slow) / (fast - slow), 0.0), 1.0) for f in freq]
+                freq = [f * (k + (1 - k) / factor) for f, k in zip(freq, keep)]
+                gain = 0.1 * math.log(factor) + 1.0
+        elif len(freq) != rotary_dim // 2:
+            raise ValueError(f"freq needs one entry per pair ({rotary_dim // 2}), got {len(freq)}")
+        self.freq = tuple(float(f) for f in freq)
+        self.scale = gain if scale is None else float(scale)
+        if not (math.isfinite(self.scale) and all(math.isfinite(f) for f in self.freq)):
+            raise ValueError("freq and scale must be finite")
+        self.rotary_dim, self.interleaved = rotary_dim, bool(interleaved)
+        self._cfg = _lib.witcert_rope_config(rotary_dim, int(self.interleaved), self.scale,
+                                             (ctypes.c_double * 128)(*self.freq))
+        self._ref = ctypes.addressof(self._cfg)
+
+
+def _need_rope(rope, head_dim):
+    if not isinstance(rope, Rope):
+        raise ValueError(f"rope must be a Rope, got {type(rope).__name__}")
+    if rope.rotary_dim > head_dim:
+        raise ValueError(f"rope turns {rope.rotary_dim} channels of a head of {head_dim}")
+
+
+def _rope_tensor(name, x, y, n_tok, like):
+    """A tensor [n_tok, heads, head_dim] with adjacent channels and its output, for witcert_rope."""
+    for nm, t in ((name, x), (name + "_out", y)):
+        if not isinstance(t, torch.Tensor):
+            raise ValueError(f"{nm} must be a torch.Tensor, got {type(t).__name__}")
+        if t.dim() != 3 or t.shape[0] != n_tok or t.shape[2] != like.shape[2] or t.shape[1] != x.shape[1]:
+            raise ValueError(f"{nm} must have shape ({n_tok}, {x.shape[1] if x.dim() == 3 else '*'}, {like.shape[2]}), "
+                             f"got {tuple(t.shape)}")
+        if t.dtype != like.dtype:
+            raise ValueError(f"{nm} must be {like.dtype}, got {t.dtype}")
+        if t.stride(2) != 1:
+            raise ValueError(f"{nm} must have adjacent channels (stride 1), got stride {t.stride(2)}")
+    for nm, t in ((name, x), (name + "_out", y)):
+        if not t.is_cuda:
+            raise ValueError(f"{nm} must be a CUDA tensor")
+    return _lib.witcert_rope_tensor(x.data_ptr(), y.data_ptr(), x.shape[1], x.stride(0), x.stride(1), y.stride(0),
+                                    y.stride(1))
+
+
+def witcert_rope(rope, positions, q, k=None, q_out=None, k_out=None, inverse=False, stream=None):
+    """Rotate q [n_tok, heads, head_dim] and, if given, k [n_tok, kv_heads, head_dim] (bf16 or fp32, any
+    token and head strides) by int64 positions [n_tok], in one launch.  Returns q_out, or (q_out, k_out);
+    outputs are new contiguous tensors unless given (the input itself rotates in place).  inverse turns
+    back: the gradient of the inputs from that of the outputs.  See witcert_rope in include/witcert.h."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be a torch.Tensor [n_tok, heads, head_dim]")
+    if q.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"q must be torch.bfloat16 or torch.float32, got {q.dtype}")
+    n_tok, _, head_dim = q.shape
+    _need_rope(rope, head_dim)
+    _need(("positions", positions, torch.int64, (n_tok,)))
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    tq = _rope_tensor("q", q, q_out, n_tok, q)
+    tk = None
+    if k is not None:
+        if k_out is None:
+            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        tk = _rope_tensor("k", k, k_out, n_tok, q)
+    elif k_out is not None:
+        raise ValueError("k_out needs k")
+    check(load().witcert_rope(rope._ref, BF16 if q.dtype == torch.bfloat16 else F32, head_dim, n_tok,
+                              _ptr(positions), ctypes.addressof(tq), None if tk is None else ctypes.addressof(tk),
+                              int(bool(inverse)), _stream_ptr(stream)), "witcert_rope")
+    return q_out if k is None else (q_out, k_out)
 
 
 class Cache:
@@ -104,16 +201,55 @@ class Cache:
         check(load().witcert_write_hat(self._h, layer, _ptr(K), _ptr(V), _ptr(K_hat), _ptr(V_hat), n_tok,
                                        _stream_ptr(stream)), "witcert_write_hat")
 
-    def witcert_write_ragged(self, layer, K, V, n_tok, K_hat=None, V_hat=None, stream=None):
-        """Ragged append: n_tok[i] tokens to sequence i; K, V (and K_hat, V_hat for black-box
-        caches) packed sequence by sequence, [sum(n_tok), Hkv, 128]."""
-        counts = [int(x) for x in n_tok]
+    def _counts(self, name, values):
+        """One host integer per sequence, as the library takes them."""
+        counts = [int(x) for x in values]
         if len(counts) != self.cfg.batch:
-            raise ValueError(f"n_tok needs one count per sequence ({self.cfg.batch}), got {len(counts)}")
+            raise ValueError(f"{name} needs one count per sequence ({self.cfg.batch}), got {len(counts)}")
+        return counts, (ctypes.c_int32 * len(counts))(*counts)
+
+    def witcert_write_rope(self, layer, K, V, rope, K_hat=None, V_hat=None, stream=None):
+        """witcert_write (witcert_write_hat with K_hat, V_hat) of keys without positions: each is turned by
+        its position in the sequence on the way into the cache."""
+        n_tok = _extent(K, 1)
+        _need_rope(rope, 128)
+        shape = self._kv_shape(n_tok)
+        _need(("K", K, self.dtype, shape), ("V", V, self.dtype, shape), ("K_hat", K_hat, self.dtype, shape, True),
+              ("V_hat", V_hat, self.dtype, shape, True))
+        check(load().witcert_write_rope(self._h, layer, _ptr(K), _ptr(V), _ptr(K_hat), _ptr(V_hat), n_tok, rope._ref,
+                                        _stream_ptr(stream)), "witcert_write_rope")
+
+    def witcert_write_rope_ragged(self, layer, K, V, n_tok, rope, K_hat=None, V_hat=None, stream=None):
+        """witcert_write_ragged of keys without positions (see witcert_write_rope)."""
+        counts, arr = self._counts("n_tok", n_tok)
+        _need_rope(rope, 128)
         shape = (sum(counts), self.cfg.n_kv_heads, 128)
         _need(("K", K, self.dtype, shape), ("V", V, self.dtype, shape), ("K_hat", K_hat, self.dtype, shape, True),
               ("V_hat", V_hat, self.dtype, shape, True))
-        arr = (ctypes.c_int32 * len(counts))(*counts)
+        check(load().witcert_write_rope_ragged(self._h, layer, _ptr(K), _ptr(V), _ptr(K_hat), _ptr(V_hat), arr,
+                                               rope._ref, _stream_ptr(stream)), "witcert_write_rope_ragged")
+
+    def witcert_truncate(self, layer, lengths, stream=None):
+        """Keep the first lengths[i] tokens of sequence i in `layer` (-1: every layer)."""
+        _, arr = self._counts("lengths", lengths)
+        check(load().witcert_truncate(self._h, layer, arr, _stream_ptr(stream)), "witcert_truncate")
+
+    def witcert_read(self, layer, t0, n_tok, K, V, stream=None):
+        """Tokens t0[i] .. t0[i] + n_tok[i] - 1 of every sequence (t0 None: the last n_tok[i]) as rows
+        K, V [sum(n_tok), Hkv, 128] of the cache's dtype."""
+        counts, arr = self._counts("n_tok", n_tok)
+        start = None if t0 is None else self._counts("t0", t0)[1]
+        shape = (sum(counts), self.cfg.n_kv_heads, 128)
+        _need(("K", K, self.dtype, shape), ("V", V, self.dtype, shape))
+        check(load().witcert_read(self._h, layer, start, arr, _ptr(K), _ptr(V), _stream_ptr(stream)), "witcert_read")
+
+    def witcert_write_ragged(self, layer, K, V, n_tok, K_hat=None, V_hat=None, stream=None):
+        """Ragged append: n_tok[i] tokens to sequence i; K, V (and K_hat, V_hat for black-box
+        caches) packed sequence by sequence, [sum(n_tok), Hkv, 128]."""
+        counts, arr = self._counts("n_tok", n_tok)
+        shape = (sum(counts), self.cfg.n_kv_heads, 128)
+        _need(("K", K, self.dtype, shape), ("V", V, self.dtype, shape), ("K_hat", K_hat, self.dtype, shape, True),
+              ("V_hat", V_hat, self.dtype, shape, True))
         check(load().witcert_write_ragged(self._h, layer, _ptr(K), _ptr(V), _ptr(K_hat), _ptr(V_hat), arr,
                                           _stream_ptr(stream)), "witcert_write_ragged")
 
@@ -208,6 +344,14 @@ class Cache:
         if self.v_witness:
             meters["meter_v"] = m[4]
         return out, meters
+
+    def read(self, layer, n_tok, t0=None, stream=None):
+        """Keys and values the cache stands for, packed [sum(n_tok), Hkv, 128] (see witcert_read)."""
+        rows = sum(max(int(x), 0) for x in n_tok)
+        dev = torch.device("cuda", torch.cuda.current_device())
+        K, V = torch.empty((2, rows, self.cfg.n_kv_heads, 128), dtype=self.dtype, device=dev)
+        self.witcert_read(layer, t0, n_tok, K, V, stream=stream)
+        return K, V
 
     def export(self, layer, what, stream=None):
         B, Hkv, Hq = self.cfg.batch, self.cfg.n_kv_heads, self.cfg.n_q_heads

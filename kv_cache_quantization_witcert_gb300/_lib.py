@@ -41,6 +41,17 @@ class witcert_stats_t(ctypes.Structure):
                 ("last_n_splits", ctypes.c_int), ("pages_used", ctypes.c_uint64)]
 
 
+class witcert_rope_config(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int), ("interleaved", ctypes.c_int), ("scale", ctypes.c_double),
+                ("freq", ctypes.c_double * 128)]
+
+
+class witcert_rope_tensor(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("n_heads", ctypes.c_int),
+                ("x_token_stride", ctypes.c_longlong), ("x_head_stride", ctypes.c_longlong),
+                ("y_token_stride", ctypes.c_longlong), ("y_head_stride", ctypes.c_longlong)]
+
+
 _vp, _int, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
 _fp = ctypes.POINTER(ctypes.c_float)
 
@@ -51,6 +62,11 @@ SIGNATURES = {
     "witcert_write_hat": [_vp, _int, _vp, _vp, _vp, _vp, _int, _vp],
     "witcert_write_ragged": [_vp, _int, _vp, _vp, _vp, _vp, ctypes.POINTER(ctypes.c_int32), _vp],
     "witcert_reset_sequence": [_vp, _int, _vp],
+    "witcert_rope": [_vp, _int, _int, _int, _vp, _vp, _vp, _int, _vp],
+    "witcert_write_rope": [_vp, _int, _vp, _vp, _vp, _vp, _int, _vp, _vp],
+    "witcert_write_rope_ragged": [_vp, _int, _vp, _vp, _vp, _vp, ctypes.POINTER(ctypes.c_int32), _vp, _vp],
+    "witcert_truncate": [_vp, _int, ctypes.POINTER(ctypes.c_int32), _vp],
+    "witcert_read": [_vp, _int, ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(ctypes.c_int32), _vp, _vp, _vp],
     "witcert_seq_length": [_vp, _int, _int, ctypes.POINTER(_int)],
     "witcert_decode": [_vp, _int, _vp, ctypes.c_double, _vp, _vp, _vp, _vp, _vp, _vp, _vp],
     "witcert_decode_noalloc": [_vp, _int, _vp, ctypes.c_double, _vp, _vp, _vp, _vp, _vp, _vp, _vp],

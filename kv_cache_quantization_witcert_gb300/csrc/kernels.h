@@ -11,6 +11,15 @@ namespace witcert {
 constexpr int kPartStride = 136;
 constexpr int kPartAcc = 8;
 
+// Rotary positions (rope.cuh): turns per position of each channel pair, as fractions of a turn in
+// units of 2^-64; the factor on the turned channels; how many channels are turned, and how paired.
+struct RopeArgs {
+  uint64_t turn[64];
+  float gain;
+  int rot;                   // a multiple of 8, at most 128
+  int interleaved;           // pairs (2p, 2p + 1), or (p, p + rot / 2)
+};
+
 struct WriteArgs {
   uint8_t* blocks;           // layer base: [B][Hkv][nblk_max][block_bytes], or the layer's page pool
   const int32_t* table;      // paged store: [B][nblk_max] page of each block (shared by layers), or null
@@ -87,6 +96,11 @@ struct LengthArgs {
 cudaError_t launch_write(int scheme, const WriteArgs& a, cudaStream_t st, bool pdl);
 // Ragged appends of the sequences in g (KIVI: values and the key backing store only).
 cudaError_t launch_write_ragged(int scheme, const WriteArgs& a, const RaggedArgs& g, cudaStream_t st, bool pdl);
+// The same writers for keys without positions: each key is turned by its position first.
+cudaError_t launch_write_rope(int scheme, const WriteArgs& a, const RopeArgs& rp, cudaStream_t st, bool pdl);
+cudaError_t launch_write_ragged_rope(int scheme, const WriteArgs& a, const RopeArgs& rp, const RaggedArgs& g,
+                                     cudaStream_t st, bool pdl);
+cudaError_t launch_kivi_keys_rope(const WriteArgs& a, const RopeArgs& rp, cudaStream_t st, bool pdl);
 cudaError_t launch_set_lengths(const LengthArgs& u, cudaStream_t st, bool pdl);
 // KIVI key blocks a (uniform) write completes, then its unfinished block's exact tail.
 cudaError_t launch_kivi_keys(const WriteArgs& a, cudaStream_t st, bool pdl);
@@ -136,6 +150,46 @@ cudaError_t launch_gate(const GateArgs& a, cudaStream_t st);
 cudaError_t launch_gate_select(const GateArgs& a, cudaStream_t st);
 int gate_max_blocks();
 void fixed_limbs(double d, uint32_t (&w)[kBigLimbs]);
+
+// Standalone rotation of up to two tensors [n_tok][heads][head_dim] (strides in elements, the
+// channels adjacent), each into its own output (which may be the input itself).
+constexpr int kRopeMaxPairs = 128;
+struct RopeTensor {
+  const void* x;
+  void* y;
+  long long x_tok, x_head, y_tok, y_head;
+  int heads;
+};
+struct RopeLaunch {
+  RopeTensor t[2];           // heads = 0: absent
+  const int64_t* pos;        // [n_tok]
+  uint64_t turn[kRopeMaxPairs];
+  float gain;
+  int n_tok, head_dim, rot, interleaved, is_bf16;
+};
+cudaError_t launch_rope(const RopeLaunch& a, int sm_count, cudaStream_t st);
+
+// A layer's store as the kernels that expand it to values read it (dequant.cuh).
+struct StoreArgs {
+  const uint8_t* blocks;     // layer base (contiguous store or page pool)
+  const int32_t* table;      // paged store: [B][nblk_max] pages, or null
+  int nblk_max, Hkv, layer, pos0, is_bf16;
+  const int32_t* slots;      // layer base, or null
+  const void* pool;
+  const float* kivi_tail;    // layer base (KIVI)
+  uint32_t rk0[10], rk1[10]; // Philox round keys of the dither
+};
+// Sequences of one read launch, passed by value: tokens t0[k] .. t0[k] + n[k] - 1 of sequence
+// seq[k] (len[k] tokens long) go to output rows row0[k], ...; blk_off counts their blocks.
+struct ReadArgs {
+  StoreArgs s;
+  void *K, *V;               // [rows][Hkv][128] of the cache's dtype
+  int n_seq;
+  int seq[kRaggedPerLaunch], t0[kRaggedPerLaunch], n[kRaggedPerLaunch], len[kRaggedPerLaunch];
+  int blk_off[kRaggedPerLaunch + 1];
+  long long row0[kRaggedPerLaunch];
+};
+cudaError_t launch_read(int scheme, const ReadArgs& a, cudaStream_t st);
 
 struct ExportArgs {
   const uint8_t* blocks;

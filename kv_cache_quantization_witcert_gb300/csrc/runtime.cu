@@ -2,6 +2,8 @@
 // pools, the pinned backing store, the side stream of the gate and the events
 // that order it against writes and decodes; validates every argument and maps
 // failures to status codes with a thread-local message.
+#include <algorithm>
+#include <atomic>
 #include <chrono>
 #include <climits>
 #include <cmath>
@@ -128,6 +130,33 @@ bool order_after_gate(witcert_cache* c, int layer, cudaStream_t st) {
   if (!c->gate_pending[layer]) return false;
   cudaStreamWaitEvent(st, c->gate_done[layer], 0);
   return true;
+}
+
+// Checks a rotation and converts its frequencies to turns (see rope.cuh).
+witcert_status rope_turns(const witcert_rope_config* rope, int head_dim, uint64_t* turn, float* gain) {
+  if (!rope) return fail(WITCERT_EINVAL, "rope must not be NULL");
+  if (rope->rotary_dim < 8 || rope->rotary_dim % 8 || rope->rotary_dim > head_dim)
+    return fail(WITCERT_EINVAL, "rotary_dim must be a multiple of 8 in [8, %d] (got %d)", head_dim, rope->rotary_dim);
+  if (!std::isfinite(rope->scale)) return fail(WITCERT_EINVAL, "the rotation's scale must be finite");
+  for (int p = 0; p < rope->rotary_dim / 2; ++p) {
+    const double f = rope->freq[p];
+    if (!std::isfinite(f)) return fail(WITCERT_EINVAL, "frequency %d of the rotation is not finite", p);
+    const double t = f * 0.15915494309189535;                // turns per position: f / (2 pi)
+    turn[p] = (uint64_t)std::ldexp(t - std::floor(t), 64);   // the fraction is below 1: no overflow
+  }
+  *gain = (float)rope->scale;
+  return WITCERT_OK;
+}
+
+// SM count of the current device (asked once per device).
+int sm_count_now() {
+  static std::atomic<int> known[64];
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return 1;
+  if (dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) return 1;
+  if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
+  return n;
 }
 
 void collect_profile(witcert_cache* c) {
@@ -365,9 +394,16 @@ static cudaError_t backing_copy(witcert_cache* c, int layer, const void* K, int 
 // inputs are packed sequence-major.  Equal appends to equal lengths take the batched writers;
 // anything else marks the cache ragged and writes each sequence at its own position.
 static witcert_status write_impl(witcert_cache* c, int layer, const void* K, const void* V, const void* Kh,
-                                 const void* Vh, const int32_t* counts, int n_uniform, void* stream) {
+                                 const void* Vh, const int32_t* counts, int n_uniform,
+                                 const witcert_rope_config* rope, void* stream) {
   if (witcert_status s = check_layer(c, layer)) return s;
   const int B = c->cfg.batch;
+  RopeArgs rp{};
+  if (rope) {
+    if (witcert_status s = rope_turns(rope, kD, rp.turn, &rp.gain)) return s;
+    rp.rot = rope->rotary_dim;
+    rp.interleaved = rope->interleaved != 0;
+  }
   std::vector<int> n(B, n_uniform);
   long long total = 0;
   for (int i = 0; i < B; ++i) {
@@ -395,8 +431,11 @@ static witcert_status write_impl(witcert_cache* c, int layer, const void* K, con
     const int n_tok = n[0], t0 = c->len[layer];
     WriteArgs a = layer_write_args(c, layer, K, V, Kh, Vh, n_tok, t0);
     // a page-table update launched just before must be complete before the writers read it
-    a.late_wait = pages.empty();
-    if (c->backing_host && n_tok >= kBulkBackingTokens) {
+    // (and a write right after another one waits for it first: a decode that follows takes only
+    // the last write's blocks for unfinished, and a truncation between them makes their rows meet)
+    a.late_wait = pages.empty() && c->last_write_layer < 0;
+    // rotated keys exist only in the writers' registers: the writers store their exact copies
+    if (c->backing_host && n_tok >= kBulkBackingTokens && !rope) {
       // bulk writes copy their exact keys to the pinned backing store with the copy engines
       // instead of the kernels' stores over C2C
       for (int i = 0; i < B && e == cudaSuccess; ++i) e = backing_copy(c, layer, K, i, (size_t)i * n_tok, n_tok, t0, st);
@@ -407,7 +446,7 @@ static witcert_status write_impl(witcert_cache* c, int layer, const void* K, con
       a.backing = nullptr;
       pdl = false;                     // the copies sit between this write and its predecessor
     }
-    e = launch_write(c->scheme, a, st, pdl);
+    e = rope ? launch_write_rope(c->scheme, a, rp, st, pdl) : launch_write(c->scheme, a, st, pdl);
     if (e != cudaSuccess) return cuda_fail(e, "write launch");
     first_blk = t0 / kBlk;
   } else {
@@ -422,11 +461,13 @@ static witcert_status write_impl(witcert_cache* c, int layer, const void* K, con
     RaggedArgs g{};
     auto flush = [&]() -> cudaError_t {
       if (g.n_seq == 0) return cudaSuccess;
-      cudaError_t r = launch_write_ragged(c->scheme, all, g, st, pdl);
+      cudaError_t r = rope ? launch_write_ragged_rope(c->scheme, all, rp, g, st, pdl)
+                           : launch_write_ragged(c->scheme, all, g, st, pdl);
       // KIVI keys close per 16-token block: each sequence's blocks by its own launch
-      for (int k = 0; k < g.n_seq && r == cudaSuccess && c->scheme == kKivi; ++k)
-        r = launch_kivi_keys(seq_write_args(c, all, g.seq[k], (size_t)g.row0[k], g.off[k + 1] - g.off[k], g.t0[k]),
-                             st, pdl);
+      for (int k = 0; k < g.n_seq && r == cudaSuccess && c->scheme == kKivi; ++k) {
+        const WriteArgs ka = seq_write_args(c, all, g.seq[k], (size_t)g.row0[k], g.off[k + 1] - g.off[k], g.t0[k]);
+        r = rope ? launch_kivi_keys_rope(ka, rp, st, pdl) : launch_kivi_keys(ka, st, pdl);
+      }
       g = RaggedArgs{};
       return r;
     };
@@ -437,7 +478,7 @@ static witcert_status write_impl(witcert_cache* c, int layer, const void* K, con
       first_blk = t0 / kBlk < first_blk ? t0 / kBlk : first_blk;
       if (n[i] >= kBlk) {
         WriteArgs a = seq_write_args(c, all, i, row, n[i], t0);
-        if (c->backing_host && n[i] >= kBulkBackingTokens) {
+        if (c->backing_host && n[i] >= kBulkBackingTokens && !rope) {
           e = backing_copy(c, layer, K, i, row, n[i], t0, st);
           if (e != cudaSuccess) {
             c->backing_lost[layer] = 1;
@@ -446,7 +487,7 @@ static witcert_status write_impl(witcert_cache* c, int layer, const void* K, con
           a.backing = nullptr;
           pdl = false;
         }
-        e = launch_write(c->scheme, a, st, pdl);
+        e = rope ? launch_write_rope(c->scheme, a, rp, st, pdl) : launch_write(c->scheme, a, st, pdl);
       } else {
         g.seq[g.n_seq] = i;
         g.t0[g.n_seq] = t0;
@@ -475,21 +516,68 @@ static witcert_status write_impl(witcert_cache* c, int layer, const void* K, con
 witcert_status witcert_write(witcert_cache* c, int layer, const void* K, const void* V, int n_tok, void* stream) {
   if (c && c->scheme == kBbox) return fail(WITCERT_EINVAL, "a black-box cache is written with witcert_write_hat");
   if (n_tok < 0) return fail(WITCERT_EINVAL, "n_tok must be >= 0");
-  return write_impl(c, layer, K, V, nullptr, nullptr, nullptr, n_tok, stream);
+  return write_impl(c, layer, K, V, nullptr, nullptr, nullptr, n_tok, nullptr, stream);
 }
 
 witcert_status witcert_write_hat(witcert_cache* c, int layer, const void* K, const void* V, const void* K_hat,
                                  const void* V_hat, int n_tok, void* stream) {
   if (c && c->scheme != kBbox) return fail(WITCERT_EINVAL, "witcert_write_hat needs a WITCERT_BLACKBOX cache");
   if (n_tok < 0) return fail(WITCERT_EINVAL, "n_tok must be >= 0");
-  return write_impl(c, layer, K, V, K_hat, V_hat, nullptr, n_tok, stream);
+  return write_impl(c, layer, K, V, K_hat, V_hat, nullptr, n_tok, nullptr, stream);
 }
 
 witcert_status witcert_write_ragged(witcert_cache* c, int layer, const void* K, const void* V, const void* K_hat,
                                     const void* V_hat, const int32_t* n_tok, void* stream) {
   if (!c || !n_tok) return fail(WITCERT_EINVAL, "cache and n_tok must not be NULL");
   if (c->scheme != kBbox && (K_hat || V_hat)) return fail(WITCERT_EINVAL, "K_hat and V_hat belong to black-box caches");
-  return write_impl(c, layer, K, V, K_hat, V_hat, n_tok, 0, stream);
+  return write_impl(c, layer, K, V, K_hat, V_hat, n_tok, 0, nullptr, stream);
+}
+
+witcert_status witcert_write_rope(witcert_cache* c, int layer, const void* K, const void* V, const void* K_hat,
+                                  const void* V_hat, int n_tok, const witcert_rope_config* rope, void* stream) {
+  if (!c || !rope) return fail(WITCERT_EINVAL, "cache and rope must not be NULL");
+  if (n_tok < 0) return fail(WITCERT_EINVAL, "n_tok must be >= 0");
+  if (c->scheme != kBbox && (K_hat || V_hat)) return fail(WITCERT_EINVAL, "K_hat and V_hat belong to black-box caches");
+  return write_impl(c, layer, K, V, K_hat, V_hat, nullptr, n_tok, rope, stream);
+}
+
+witcert_status witcert_write_rope_ragged(witcert_cache* c, int layer, const void* K, const void* V, const void* K_hat,
+                                         const void* V_hat, const int32_t* n_tok, const witcert_rope_config* rope,
+                                         void* stream) {
+  if (!c || !n_tok || !rope) return fail(WITCERT_EINVAL, "cache, n_tok and rope must not be NULL");
+  if (c->scheme != kBbox && (K_hat || V_hat)) return fail(WITCERT_EINVAL, "K_hat and V_hat belong to black-box caches");
+  return write_impl(c, layer, K, V, K_hat, V_hat, n_tok, 0, rope, stream);
+}
+
+witcert_status witcert_rope(const witcert_rope_config* rope, witcert_dtype dtype, int head_dim, int n_tok,
+                            const int64_t* positions, const witcert_rope_tensor* q, const witcert_rope_tensor* k,
+                            int inverse, void* stream) {
+  if (dtype != WITCERT_F32 && dtype != WITCERT_BF16) return fail(WITCERT_EINVAL, "unknown dtype %d", (int)dtype);
+  if (head_dim < 8 || head_dim % 2 || head_dim > 2 * kRopeMaxPairs)
+    return fail(WITCERT_EINVAL, "head_dim must be even and in [8, %d] (got %d)", 2 * kRopeMaxPairs, head_dim);
+  if (n_tok < 0) return fail(WITCERT_EINVAL, "n_tok must be >= 0");
+  RopeLaunch a{};
+  if (witcert_status s = rope_turns(rope, head_dim, a.turn, &a.gain)) return s;
+  if (!q) return fail(WITCERT_EINVAL, "q must not be NULL");
+  const witcert_rope_tensor* in[2] = {q, k};
+  for (int i = 0; i < 2; ++i) {
+    if (!in[i]) continue;
+    const witcert_rope_tensor& t = *in[i];
+    if (t.n_heads < 1 || t.n_heads > 65535) return fail(WITCERT_EINVAL, "n_heads must be in [1, 65535]");
+    if (n_tok > 0 && (!t.x || !t.y)) return fail(WITCERT_EINVAL, "x and y must not be NULL");
+    a.t[i] = RopeTensor{t.x, t.y, t.x_token_stride, t.x_head_stride, t.y_token_stride, t.y_head_stride, t.n_heads};
+  }
+  if (n_tok == 0) { ok(); return WITCERT_OK; }
+  if (!positions) return fail(WITCERT_EINVAL, "positions must not be NULL");
+  a.pos = positions;
+  a.n_tok = n_tok; a.head_dim = head_dim; a.rot = rope->rotary_dim; a.interleaved = rope->interleaved != 0;
+  a.is_bf16 = dtype == WITCERT_BF16;
+  if (inverse)
+    for (uint64_t& t : a.turn) t = 0 - t;
+  cudaError_t e = launch_rope(a, sm_count_now(), static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "rope launch");
+  ok();
+  return WITCERT_OK;
 }
 
 witcert_status witcert_reset_sequence(witcert_cache* c, int seq, void* stream) {
@@ -532,6 +620,114 @@ witcert_status witcert_reset_sequence(witcert_cache* c, int seq, void* stream) {
   }
   c->last_write_layer = -1;
   c->lengths_last = true;
+  ok();
+  return WITCERT_OK;
+}
+
+witcert_status witcert_truncate(witcert_cache* c, int layer, const int32_t* lengths, void* stream) {
+  if (!c || !lengths) return fail(WITCERT_EINVAL, "cache and lengths must not be NULL");
+  if (layer != -1)
+    if (witcert_status s = check_layer(c, layer)) return s;
+  const int l0 = layer < 0 ? 0 : layer, l1 = layer < 0 ? c->cfg.n_layers : layer + 1, B = c->cfg.batch;
+  bool any = false;
+  for (int l = l0; l < l1; ++l)
+    for (int i = 0; i < B; ++i) {
+      const int now = c->slen[l][i], to = lengths[i];
+      if (to < 0) return fail(WITCERT_EINVAL, "lengths must be >= 0 (sequence %d: %d)", i, to);
+      if (to >= now) continue;
+      any = true;
+      if (c->scheme == kKivi && to % kBlk && to / kBlk < now / kBlk)
+        return fail(WITCERT_EINVAL, "layer %d sequence %d: the exact keys of a finished KIVI block are gone; truncate "
+                    "to a multiple of %d or within the unfinished block (at %d)", l, i, kBlk, now / kBlk * kBlk);
+    }
+  if (!any) { ok(); return WITCERT_OK; }
+  auto st = static_cast<cudaStream_t>(stream);
+  bool waited = false;
+  for (int l = l0; l < l1; ++l) waited |= order_after_gate(c, l, st);
+  bool pdl = c->overlap && !waited;
+  // lengths that stay equal need no copy on the device
+  bool uniform = !c->ragged;
+  for (int l = l0; l < l1 && uniform; ++l)
+    for (int i = 1; i < B && uniform; ++i)
+      uniform = std::min(c->slen[l][i], (int)lengths[i]) == std::min(c->slen[l][0], (int)lengths[0]);
+  cudaError_t e = cudaSuccess;
+  if (!uniform) {
+    e = enter_ragged(c, st, pdl);
+    std::vector<std::pair<int, int>> upd;
+    for (int l = l0; l < l1; ++l)
+      for (int i = 0; i < B; ++i)
+        if (lengths[i] < c->slen[l][i]) upd.emplace_back(l * B + i, lengths[i]);
+    if (e == cudaSuccess) e = push_lengths(c, upd, st, pdl);
+    if (e != cudaSuccess) return cuda_fail(e, "sequence lengths");
+    c->lengths_last = true;
+  }
+  for (int l = l0; l < l1; ++l) {
+    int mx = 0;
+    bool moved = false;
+    for (int i = 0; i < B; ++i) {
+      if (lengths[i] < c->slen[l][i]) { c->slen[l][i] = lengths[i]; moved = true; }
+      mx = std::max(mx, c->slen[l][i]);
+    }
+    c->len[l] = mx;
+    if (moved) ++c->write_gen[l];          // block risks of the longer sequence are stale
+  }
+  ok();
+  return WITCERT_OK;
+}
+
+// The layer's store as the kernels that expand it read it.
+static StoreArgs store_args(const witcert_cache* c, int layer) {
+  StoreArgs s{};
+  s.blocks = c->blocks + layer * c->layer_blocks;
+  s.table = c->table;
+  s.nblk_max = c->nblk_max; s.Hkv = c->cfg.n_kv_heads; s.layer = layer; s.pos0 = c->cfg.pos_offset;
+  s.is_bf16 = c->cfg.kv_dtype == WITCERT_BF16;
+  if (c->slots) s.slots = c->slots + layer * layer_rows(c) * c->nblk_max;
+  s.pool = c->pool;
+  if (c->kivi_tail) s.kivi_tail = c->kivi_tail + layer * layer_rows(c) * kBlk * kD;
+  philox_round_keys(c->cfg.seed, s.rk0, s.rk1);
+  return s;
+}
+
+witcert_status witcert_read(witcert_cache* c, int layer, const int32_t* t0, const int32_t* n_tok, void* K, void* V,
+                            void* stream) {
+  if (witcert_status s = check_layer(c, layer)) return s;
+  if (!n_tok) return fail(WITCERT_EINVAL, "n_tok must not be NULL");
+  const int B = c->cfg.batch;
+  long long total = 0;
+  for (int i = 0; i < B; ++i) {
+    const long long from = t0 ? t0[i] : (long long)c->slen[layer][i] - n_tok[i];
+    if (n_tok[i] < 0 || from < 0 || from + n_tok[i] > c->slen[layer][i])
+      return fail(WITCERT_EINVAL, "layer %d sequence %d holds %d tokens; cannot read %d from %lld", layer, i,
+                  c->slen[layer][i], n_tok[i], from);
+    total += n_tok[i];
+  }
+  if (total == 0) { ok(); return WITCERT_OK; }
+  if (!K || !V) return fail(WITCERT_EINVAL, "K and V must not be NULL");
+  auto st = static_cast<cudaStream_t>(stream);
+  order_after_gate(c, layer, st);
+  ReadArgs a{};
+  a.s = store_args(c, layer);
+  a.K = K; a.V = V;
+  long long row = 0;
+  cudaError_t e = cudaSuccess;
+  for (int i = 0; i < B && e == cudaSuccess; ++i) {
+    const int n = n_tok[i];
+    if (n > 0) {
+      const int k = a.n_seq++, from = t0 ? t0[i] : c->slen[layer][i] - n;
+      a.seq[k] = i; a.t0[k] = from; a.n[k] = n; a.len[k] = c->slen[layer][i];
+      a.row0[k] = row;
+      a.blk_off[k + 1] = a.blk_off[k] + (from + n - 1) / kBlk - from / kBlk + 1;
+      row += n;
+    }
+    if (a.n_seq == kRaggedPerLaunch || (i + 1 == B && a.n_seq)) {
+      e = launch_read(c->scheme, a, st);
+      a.n_seq = 0;
+    }
+  }
+  if (e != cudaSuccess) return cuda_fail(e, "read launch");
+  c->last_write_layer = -1;
+  c->lengths_last = false;
   ok();
   return WITCERT_OK;
 }
