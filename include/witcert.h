@@ -227,6 +227,28 @@ witcert_status witcert_truncate(witcert_cache* cache, int layer, const int32_t* 
 witcert_status witcert_read(witcert_cache* cache, int layer, const int32_t* t0, const int32_t* n_tok, void* K,
                             void* V, void* stream);
 
+/* Chunk attention: causal attention of several new tokens a sequence over the compressed cache (a
+ * prompt chunk, drafted tokens to check).  The queries are the last n_tok[i] tokens of sequence i,
+ * already written (host [batch], 0 <= n_tok[i] <= length): q, device [sum n_tok][n_q_heads][128]
+ * bf16, post-RoPE, packed sequence by sequence in position order.  The query at position p attends
+ * to positions 0 .. p of its sequence as the cache stores them, with weights softmax(q.k / sqrt d);
+ * query head j reads KV head j / (Hq/Hkv).  out: device, q's shape, bf16.  Row by row this is what
+ * witcert_decode gives at that length (KIVI2: with the blocks finished since then quantized), to
+ * bf16; no meters are formed.  Products run on the tensor cores: decoded keys and values and the
+ * softmax weights are rounded to fp16 (keys and values beyond 65504 saturate), for a black-box
+ * cache to bf16, with fp32 sums.  Keys a query does not see have weight 0; values among the same
+ * 128 tokens must be finite for that to hold.  bf16 caches only.  workspace: device, 16-byte aligned, at
+ * least what witcert_attend_workspace says for the same n_tok; nothing in it is kept between calls.
+ * EINVAL on bad arguments.  Asynchronous on `stream`, after a pending gate of the layer.  A device
+ * wait that runs out (2 s) leaves the rows it concerns unwritten and counts in witcert_stats'
+ * device_errors. */
+witcert_status witcert_attend(witcert_cache* cache, int layer, const void* q, const int32_t* n_tok, void* out,
+                              void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of device workspace that witcert_attend needs for these counts at the layer's present
+ * lengths (host, no device work). */
+witcert_status witcert_attend_workspace(const witcert_cache* cache, int layer, const int32_t* n_tok, size_t* bytes);
+
 /* Empty sequence `seq` in every layer so the slot can serve a new request (continuous
  * batching).  Its repairs are dropped too (their slots in the exact-key pool are not
  * reused), a paged cache returns its pages to the pool, and its value witnesses are zeroed

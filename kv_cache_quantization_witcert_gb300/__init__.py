@@ -243,6 +243,33 @@ class Cache:
         _need(("K", K, self.dtype, shape), ("V", V, self.dtype, shape))
         check(load().witcert_read(self._h, layer, start, arr, _ptr(K), _ptr(V), _stream_ptr(stream)), "witcert_read")
 
+    def witcert_attend_workspace(self, layer, n_tok):
+        """Bytes of workspace that witcert_attend needs for these counts."""
+        _, arr = self._counts("n_tok", n_tok)
+        n = ctypes.c_size_t()
+        check(load().witcert_attend_workspace(self._h, layer, arr, ctypes.byref(n)), "witcert_attend_workspace")
+        return n.value
+
+    def witcert_attend(self, layer, q, n_tok, out, workspace, stream=None):
+        """Causal attention of each sequence's last n_tok[i] tokens, q [sum(n_tok), Hq, 128] bf16, over the
+        cache, into out (q's shape, bf16)."""
+        counts, arr = self._counts("n_tok", n_tok)
+        shape = (sum(counts), self.cfg.n_q_heads, 128)
+        _need(("q", q, torch.bfloat16, shape), ("out", out, torch.bfloat16, shape),
+              ("workspace", workspace, torch.uint8, (None,)))
+        check(load().witcert_attend(self._h, layer, _ptr(q), arr, _ptr(out), _ptr(workspace), workspace.numel(),
+                                    _stream_ptr(stream)), "witcert_attend")
+
+    def attend(self, layer, q, n_tok, stream=None):
+        """Chunk attention with a fresh output and workspace (see witcert_attend)."""
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        workspace = torch.empty(self.witcert_attend_workspace(layer, n_tok), dtype=torch.uint8, device=q.device)
+        self.witcert_attend(layer, q, n_tok, out, workspace, stream=stream)
+        if stream is not None:
+            workspace.record_stream(stream)
+            out.record_stream(stream)
+        return out
+
     def witcert_write_ragged(self, layer, K, V, n_tok, K_hat=None, V_hat=None, stream=None):
         """Ragged append: n_tok[i] tokens to sequence i; K, V (and K_hat, V_hat for black-box
         caches) packed sequence by sequence, [sum(n_tok), Hkv, 128]."""

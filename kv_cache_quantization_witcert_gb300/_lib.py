@@ -66,6 +66,8 @@ SIGNATURES = {
     "witcert_write_rope": [_vp, _int, _vp, _vp, _vp, _vp, _int, _vp, _vp],
     "witcert_write_rope_ragged": [_vp, _int, _vp, _vp, _vp, _vp, ctypes.POINTER(ctypes.c_int32), _vp, _vp],
     "witcert_truncate": [_vp, _int, ctypes.POINTER(ctypes.c_int32), _vp],
+    "witcert_attend": [_vp, _int, _vp, ctypes.POINTER(ctypes.c_int32), _vp, _vp, _sz, _vp],
+    "witcert_attend_workspace": [_vp, _int, ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(_sz)],
     "witcert_read": [_vp, _int, ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(ctypes.c_int32), _vp, _vp, _vp],
     "witcert_seq_length": [_vp, _int, _int, ctypes.POINTER(_int)],
     "witcert_decode": [_vp, _int, _vp, ctypes.c_double, _vp, _vp, _vp, _vp, _vp, _vp, _vp],

@@ -191,6 +191,35 @@ struct ReadArgs {
 };
 cudaError_t launch_read(int scheme, const ReadArgs& a, cudaStream_t st);
 
+// Chunk attention (attend.cu, expand.cu).  Sequences of one launch, passed by value: the n[k]
+// newest tokens of sequence seq[k] (len[k] tokens long) are the queries, packed from token row
+// row0[k] on.  A query row of a KV head is (token, head of the group), token-major: rows_k = n grp.
+constexpr int kAttendSeqs = 64;
+constexpr int kTileTok = 128;                    // tokens of a key / value tile
+constexpr int kTileBytes = kTileTok * 128 * 2;   // one operand image: 128 x 128 two-byte elements
+constexpr int kTileRows = 128;                   // query rows of one tensor-core tile
+constexpr int kRecStride = 132;                  // split record: m (log2), l, two unused, 128 sums
+struct AttendArgs {
+  StoreArgs s;
+  const void* q;             // [rows][Hq][128] bf16
+  void* out;                 // [rows][Hq][128] bf16
+  uint8_t* images;           // [tiles][Hkv][keys, values] operand images
+  float* rec;                // split records
+  int* err;                  // device error word (waits that ran out)
+  int Hq, grp, n_seq;
+  float scale_log2;          // log2(e) / sqrt(d)
+  int seq[kAttendSeqs], n[kAttendSeqs], len[kAttendSeqs], row0[kAttendSeqs];
+  int splits[kAttendSeqs];   // runs of key tiles a query tile is split into
+  int tile_off[kAttendSeqs + 1];       // image tiles before sequence k
+  int unit_off[kAttendSeqs + 1];       // CTAs before sequence k
+  long long rec_off[kAttendSeqs + 1];  // records before sequence k (none where there is one part)
+};
+cudaError_t launch_expand(int scheme, const AttendArgs& a, cudaStream_t st);
+// pair: one 128-row query tile a CTA, whose two softmax groups take alternate key tiles; otherwise
+// two query tiles a CTA.
+cudaError_t launch_attend(int scheme, const AttendArgs& a, bool pair, cudaStream_t st);
+cudaError_t launch_attend_merge(const AttendArgs& a, bool pair, cudaStream_t st);
+
 struct ExportArgs {
   const uint8_t* blocks;
   const int32_t* table;      // paged store, or null

@@ -732,6 +732,148 @@ witcert_status witcert_read(witcert_cache* c, int layer, const int32_t* t0, cons
   return WITCERT_OK;
 }
 
+// ------------------------------------------------------------------ chunk attention
+// One group of sequences: expanded, attended and merged by one launch each.
+struct AttendGroup {
+  AttendArgs a;
+  bool pair;
+};
+// Operand images of a group (64 KB per 128 tokens and KV head) stay below this, unless a single
+// sequence needs more.
+constexpr size_t kImageCap = size_t(2) << 30;
+
+// Splits of the key tiles: CTAs run one an SM, so with U row tiles of up to T key tiles each the
+// launch takes ceil(U s / SMs) rounds of ceil(T / s) tile steps and a fixed part (staging queries,
+// the pipeline's ends: about four steps); more than one part adds the merge (about three).
+static void attend_splits(AttendArgs& a, bool pair, int sm_count) {
+  const int rows_cta = pair ? kTileRows : 2 * kTileRows;
+  int most = 1;
+  for (int k = 0; k < a.n_seq; ++k) most = std::max(most, (a.len[k] + kTileTok - 1) / kTileTok);
+  int best = most;
+  double best_cost = 1e300;
+  for (int s = 1; s <= 64 && s <= most; ++s) {
+    const int per = (most + s - 1) / s;
+    long long units = 0;
+    for (int k = 0; k < a.n_seq; ++k) {
+      const int tiles = (a.len[k] + kTileTok - 1) / kTileTok;
+      units += (long long)a.s.Hkv * ((a.n[k] * a.grp + rows_cta - 1) / rows_cta) * ((tiles + per - 1) / per);
+    }
+    const double rounds = (double)((units + sm_count - 1) / sm_count);
+    const double cost = rounds * (per + 4.0) + (s > 1 && !pair ? 3.0 : 0.0);
+    if (cost < best_cost * 0.999) { best_cost = cost; best = per; }
+  }
+  for (int k = 0; k < a.n_seq; ++k) a.splits[k] = ((a.len[k] + kTileTok - 1) / kTileTok + best - 1) / best;
+}
+
+// Groups of an attend call; bytes of the images and of the records the largest of them needs.
+static void plan_attend(const witcert_cache* c, int layer, const int32_t* n_tok, std::vector<AttendGroup>& groups,
+                        size_t& image_bytes, size_t& rec_bytes) {
+  const int B = c->cfg.batch, Hkv = c->cfg.n_kv_heads, grp = c->cfg.n_q_heads / Hkv;
+  const size_t tile = (size_t)Hkv * 2 * kTileBytes;
+  image_bytes = rec_bytes = 0;
+  for (int pass = 0; pass < 2; ++pass) {
+    const bool pair = pass == 0;               // sequences of at most one row tile
+    int row0 = 0;
+    bool open = false;
+    for (int i = 0; i < B; ++i) {
+      const int n = n_tok[i], len = c->slen[layer][i];
+      const int at = row0;
+      row0 += n;
+      if (n == 0 || (n * (long long)grp <= kTileRows) != pair) continue;
+      const int tiles = (len + kTileTok - 1) / kTileTok;
+      if (open) {
+        const AttendArgs& g = groups.back().a;
+        if (g.n_seq == kAttendSeqs || (g.tile_off[g.n_seq] + (size_t)tiles) * tile > kImageCap) open = false;
+      }
+      if (!open) {
+        groups.emplace_back();
+        AttendGroup& g = groups.back();
+        memset(&g, 0, sizeof g);
+        g.pair = pair;
+        g.a.s = store_args(c, layer);
+        g.a.Hq = c->cfg.n_q_heads; g.a.grp = grp;
+        g.a.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)kD));
+        g.a.err = c->err;
+        open = true;
+      }
+      AttendArgs& a = groups.back().a;
+      const int k = a.n_seq++;
+      a.seq[k] = i; a.n[k] = n; a.len[k] = len; a.row0[k] = at;
+      a.tile_off[k + 1] = a.tile_off[k] + tiles;
+    }
+  }
+  for (AttendGroup& g : groups) {
+    AttendArgs& a = g.a;
+    attend_splits(a, g.pair, c->sm_count);
+    const int rows_cta = g.pair ? kTileRows : 2 * kTileRows;
+    for (int k = 0; k < a.n_seq; ++k) {
+      const long long rows = (long long)a.n[k] * grp;
+      const int parts = a.splits[k] * (g.pair ? 2 : 1);
+      a.unit_off[k + 1] = a.unit_off[k] + (int)((rows + rows_cta - 1) / rows_cta) * a.splits[k] * Hkv;
+      a.rec_off[k + 1] = a.rec_off[k] + (parts > 1 ? rows * Hkv * parts : 0);
+    }
+    image_bytes = std::max(image_bytes, a.tile_off[a.n_seq] * tile);
+    rec_bytes = std::max(rec_bytes, (size_t)a.rec_off[a.n_seq] * kRecStride * sizeof(float));
+  }
+}
+
+static witcert_status check_attend(const witcert_cache* c, int layer, const int32_t* n_tok, long long& rows) {
+  if (witcert_status s = check_layer(c, layer)) return s;
+  if (!n_tok) return fail(WITCERT_EINVAL, "n_tok must not be NULL");
+  if (c->cfg.kv_dtype != WITCERT_BF16) return fail(WITCERT_EINVAL, "chunk attention needs a bf16 cache");
+  rows = 0;
+  for (int i = 0; i < c->cfg.batch; ++i) {
+    if (n_tok[i] < 0 || n_tok[i] > c->slen[layer][i])
+      return fail(WITCERT_EINVAL, "layer %d sequence %d holds %d tokens; %d queries do not fit", layer, i,
+                  c->slen[layer][i], n_tok[i]);
+    rows += n_tok[i];
+  }
+  if (rows * c->cfg.n_q_heads > INT_MAX) return fail(WITCERT_EINVAL, "too many query rows (%lld)", rows);
+  return WITCERT_OK;
+}
+
+witcert_status witcert_attend_workspace(const witcert_cache* c, int layer, const int32_t* n_tok, size_t* bytes) {
+  long long rows = 0;
+  if (witcert_status s = check_attend(c, layer, n_tok, rows)) return s;
+  if (!bytes) return fail(WITCERT_EINVAL, "bytes must not be NULL");
+  std::vector<AttendGroup> groups;
+  size_t image = 0, rec = 0;
+  plan_attend(c, layer, n_tok, groups, image, rec);
+  *bytes = image + rec;
+  ok();
+  return WITCERT_OK;
+}
+
+witcert_status witcert_attend(witcert_cache* c, int layer, const void* q, const int32_t* n_tok, void* out,
+                              void* workspace, size_t workspace_bytes, void* stream) {
+  long long rows = 0;
+  if (witcert_status s = check_attend(c, layer, n_tok, rows)) return s;
+  if (rows == 0) { ok(); return WITCERT_OK; }
+  if (!q || !out) return fail(WITCERT_EINVAL, "q and out must not be NULL");
+  if (((uintptr_t)q | (uintptr_t)out | (uintptr_t)workspace) % 16)
+    return fail(WITCERT_EINVAL, "q, out and workspace must be 16-byte aligned");
+  std::vector<AttendGroup> groups;
+  size_t image = 0, rec = 0;
+  plan_attend(c, layer, n_tok, groups, image, rec);
+  if (image + rec > workspace_bytes || !workspace)
+    return fail(WITCERT_EINVAL, "the workspace needs %zu bytes, got %zu", image + rec, workspace ? workspace_bytes : 0);
+  auto st = static_cast<cudaStream_t>(stream);
+  order_after_gate(c, layer, st);
+  for (AttendGroup& g : groups) {
+    g.a.q = q; g.a.out = out;
+    g.a.images = static_cast<uint8_t*>(workspace);
+    g.a.rec = reinterpret_cast<float*>(g.a.images + image);
+    cudaError_t e = launch_expand(c->scheme, g.a, st);
+    if (e == cudaSuccess) e = launch_attend(c->scheme, g.a, g.pair, st);
+    if (e == cudaSuccess) e = launch_attend_merge(g.a, g.pair, st);
+    if (e != cudaSuccess) return cuda_fail(e, "attend launch");
+  }
+  c->last_write_layer = -1;
+  c->lengths_last = false;
+  ok();
+  return WITCERT_OK;
+}
+
 // Automatic split count for a decode of nblk blocks: sized by how many split-kernel CTAs of
 // this configuration fit on an SM, and never above the scratch sized at create time.
 static int auto_splits(const witcert_cache* c, int nblk, bool meter, int cap) {
