@@ -1,0 +1,300 @@
+// What the chunk attention kernels share: the walk over a CTA's work, the staging of query rows and
+// the softmax of one key tile.
+//
+// A query row is handled by two threads of two warps that can reach the same tensor-memory lanes,
+// each with half of the tile's columns: half the registers, and two warps instead of one to hide
+// the latency of a tile's chain (tensor memory, maximum, exponentials, tensor memory), which is
+// what bounds a step.  They agree on the row's maximum through shared memory and a named barrier.
+//
+// Softmax: weights 2^(s c - m + kOff) with the row's reference m in log2 units.  m follows the
+// running maximum only when that has grown by more than kGrow, so O and the sum l are rescaled
+// rarely, by the softmax threads themselves.  kOff keeps the small weights of fp16 normal: weights
+// reach 2^15 at most, and those below 2^-22 of the reference (2^-32 before they vanish) lose bits.
+#pragma once
+#include "kernels.h"
+#include "tcgen05.cuh"
+
+namespace witcert {
+
+constexpr float kOff = 8.0f, kGrow = 7.0f;
+constexpr uint64_t kAttendWaitNs = 2000000000ull;          // 2 s per barrier wait
+
+// One stretch of key tiles of one unit.
+struct Segment {
+  int k, h, r0, rows;        // sequence, KV head, first query row of the unit, rows of the sequence
+  int j0, nk;                // key tiles j0 .. j0 + nk - 1
+  bool whole;                // all of the unit's key tiles: the output is final
+  int slot;                  // otherwise: where its records go
+};
+// Rows of unit u and its key tiles.
+__device__ __forceinline__ int unit_place(const AttendArgs& a, int u, Segment& x) {
+  int lo = 0, hi = a.n_seq - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (a.unit_off[mid] <= u) lo = mid; else hi = mid - 1;
+  }
+  u -= a.unit_off[lo];
+  x.k = lo;
+  x.rows = a.n[lo] * a.grp;
+  const int tiles = (x.rows + a.unit_rows - 1) / a.unit_rows;
+  x.h = u % a.s.Hkv;
+  x.r0 = (tiles - 1 - u / a.s.Hkv) * a.unit_rows;          // last rows, which see most keys, first
+  const int last = min(x.rows, x.r0 + a.unit_rows) - 1;
+  return (a.len[lo] - a.n[lo] + last / a.grp) / kTileTok + 1;
+}
+// The segments of CTA c in order: f(segment) until it returns false.
+template <typename F>
+__device__ __forceinline__ void walk(const AttendArgs& a, int c, F f) {
+  AttendStart at = a.start[c];
+  const AttendStart end = a.start[c + 1];
+  while (at.unit < end.unit || (at.unit == end.unit && at.j < end.j)) {
+    Segment x;
+    const int nt = unit_place(a, at.unit, x);
+    const int to = at.unit == end.unit ? end.j : nt;
+    x.j0 = at.j;
+    x.nk = to - at.j;
+    x.whole = at.j == 0 && to == nt;
+    x.slot = 2 * c + (at.j == 0 ? 1 : 0);
+    if (!f(x)) return;
+    at.unit += to == nt;
+    at.j = to == nt ? 0 : to;
+  }
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  return BF16 ? bf2_bits(__floats2bfloat162_rn(a, b)) : h2_bits(__floats2half2_rn(a, b));
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// One arrival for a warp whose lanes have all come here (their earlier writes included).
+__device__ __forceinline__ void warp_arrive(uint32_t bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+// A wait of a whole warp: its lanes give up together (tensor-memory accesses need all of them).
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
+  return !__any_sync(0xffffffffu, !mbar_wait(bar, parity, kAttendWaitNs));
+}
+
+// A row's two threads: shared words mine and other, and the barrier of their two warps (an mbarrier
+// of two arrivals, so that the wait has a limit).
+struct RowPair {
+  volatile float *mine, *other;
+  uint32_t bar, phase;
+  bool ok;
+  __device__ __forceinline__ void sync() {
+    warp_arrive(bar);
+    ok = ok && warp_wait(bar, phase++ & 1);
+  }
+  __device__ __forceinline__ float swap(float v) {
+    *mine = v;
+    sync();
+    return *other;
+  }
+};
+
+// This thread's half (channels 64 hf ..) of query row `row` of a segment into the swizzled operand
+// tile, as row r; rows past the sequence's are zero.  Returns log2(e)/sqrt(d) times the power of
+// two that the row was divided by: fp16 rows are scaled to a largest element in [1, 2).
+template <bool BF16>
+__device__ __forceinline__ float stage_query(const AttendArgs& a, const Segment& u, int row, int r, int hf,
+                                             uint8_t* tile, RowPair& pair) {
+  uint4 v[8];
+#pragma unroll
+  for (int c = 0; c < 8; ++c) v[c] = make_uint4(0, 0, 0, 0);
+  if (row < u.rows) {
+    const uint4* src = reinterpret_cast<const uint4*>(
+        static_cast<const __nv_bfloat16*>(a.q) +
+        ((size_t)(a.row0[u.k] + row / a.grp) * a.Hq + u.h * a.grp + row % a.grp) * kD + 64 * hf);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) v[c] = src[c];
+  }
+  float scale = a.scale_log2;
+  if (!BF16) {
+    uint32_t top = 0;                                     // largest magnitude's bits, two lanes of bf16
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) top = __vmaxu2(top, w[e] & 0x7FFF7FFFu);
+    }
+    const int mine = (int)max(top & 0xFFFFu, top >> 16);
+    const int both = max(mine, __float_as_int(pair.swap(__int_as_float(mine))));
+    // biased exponent of the row's largest element, kept where 2^-e and 2^e are normal numbers
+    const int e = min(max(both >> 7, 16), 238) - 127;
+    const float down = __int_as_float((127 - e) << 23);
+    scale *= __int_as_float((127 + e) << 23);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      uint32_t* w = &v[c].x;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        w[k] = pack2<false>(__uint_as_float(w[k] << 16) * down, __uint_as_float(w[k] & 0xFFFF0000u) * down);
+    }
+    pair.sync();                                          // both have read before the words are used again
+  }
+#pragma unroll
+  for (int c = 0; c < 8; ++c)
+    *reinterpret_cast<uint4*>(tile + hf * (kTileRows * 128) + r * 128 + ((c ^ (r & 7)) << 4)) = v[c];
+  return scale;
+}
+
+// One key tile's softmax for half a row: logits at ts (64 columns), weights to tp (32 columns, over
+// the logits), O at to (64 columns).  rel: the last place-order token of the tile this row sees (127 or
+// more: all, negative: none).  The weights of the half's first 32 and last 32 places are announced
+// on p_bar and p_bar + 8.
+template <bool BF16>
+__device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t tp, uint32_t to, int hf, int rel, bool first,
+                                             float scale, float& m, float& l, RowPair& pair, uint32_t p_bar) {
+  uint32_t v[2][32];
+  tmem_ld32(ts, v[0]);
+  tmem_ld32(ts + 32, v[1]);
+  tmem_wait_ld();
+  if (__any_sync(0xffffffffu, rel < kTileTok - 1)) {
+    const int lim = rel - 64 * hf;
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int e = 0; e < 32; ++e) {
+        // token of place e (see expand.cu)
+        const int p = e & 15, tok = 32 * c + (e & 16) + 2 * (p >> 2) + (p & 1) + 8 * ((p >> 1) & 1);
+        if (tok > lim) v[c][e] = 0xFF800000u;
+      }
+  }
+  float mx[4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const uint32_t* x = &v[c >> 1][16 * (c & 1)];
+    mx[c] = __uint_as_float(x[0]);
+#pragma unroll
+    for (int e = 1; e < 15; e += 2) mx[c] = max3(mx[c], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+    mx[c] = fmaxf(mx[c], __uint_as_float(x[15]));
+  }
+  float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
+  // the other half's logits have left tensor memory when this returns: weights may overwrite them
+  top = fmaxf(top, pair.swap(top));
+  const bool grow = (top - m) * scale > kGrow;             // also from -inf; false while nothing is visible
+  if (__any_sync(0xffffffffu, grow)) {
+    const float mn = grow ? top : m, f = grow ? ex2((m - mn) * scale) : 1.0f;
+    l *= f;
+    m = mn;
+    if (!first) {
+#pragma unroll 1
+      for (int c = 0; c < 64; c += 16) {
+        uint32_t o[16];
+        tmem_ld16(to + c, o);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+        tmem_st16(to + c, o);
+      }
+    }
+  }
+  const float bias = kOff - (m == -INFINITY ? 0.f : m * scale);
+  const float2 sc2 = make_float2(scale, scale), b2 = make_float2(bias, bias);
+  float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    uint32_t pk[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const float2 x = __ffma2_rn(make_float2(__uint_as_float(v[c][2 * e]), __uint_as_float(v[c][2 * e + 1])), sc2, b2);
+      const float2 p = make_float2(ex2(x.x), ex2(x.y));
+      sum[e & 1] = __fadd2_rn(sum[e & 1], p);
+      pk[e] = pack2<BF16>(p.x, p.y);
+    }
+    tmem_st16(tp + 16 * c, pk);
+    tmem_wait_st();
+    tc_fence_before();
+    warp_arrive(p_bar + 8 * c);
+  }
+  l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+}
+
+// O += P V for one tile: A in tensor memory, the value image at descriptor vd; the first and last 32
+// places of each half as they are announced.  False if a wait ran out.
+__device__ __forceinline__ bool issue_pv(uint32_t to, uint32_t tp, uint64_t vd, uint32_t idesc, bool first,
+                                         uint32_t p_bar, uint32_t parity) {
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    if (!warp_wait(p_bar + 8 * c, parity)) return false;
+    tc_fence_after();
+    if (elect_one()) {
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {                        // 16 places a step, 64 a panel
+        const int x = 4 * (y >> 1) + 2 * c + (y & 1);
+        mma_ts(to, tp + x * 8, vd + (uint64_t)(x >> 2) * (kD * 128 >> 4) + (x & 3) * 2, idesc, !first || c > 0 || y > 0);
+      }
+    }
+    __syncwarp();
+  }
+  return true;
+}
+// S = Q K^T for one tile; done is told when it (and all before it) is complete.
+__device__ __forceinline__ void issue_qk(uint32_t ts, uint64_t qd, uint64_t kd, uint32_t idesc, uint32_t done) {
+  if (elect_one()) {
+#pragma unroll
+    for (int x = 0; x < 8; ++x) {                          // 16 channels a step, 64 a panel
+      const uint64_t o = (uint64_t)(x >> 2) * (kTileRows * 128 >> 4) + (x & 3) * 2;
+      mma_ss(ts, qd + o, kd + o, idesc, x > 0);
+    }
+    mma_commit(done);
+  }
+  __syncwarp();
+}
+__device__ __forceinline__ void warp_commit(uint32_t bar) {
+  if (elect_one()) mma_commit(bar);
+  __syncwarp();
+}
+// A place in a ring of N stages and the parity of the visit.
+template <int N> struct RingAt {
+  uint32_t st = 0, ph = 0;
+  __device__ __forceinline__ void next() {
+    if (++st == N) { st = 0; ph ^= 1; }
+  }
+};
+
+// Half a row of a finished segment: the output itself, or its record.
+__device__ __forceinline__ void store_row(const AttendArgs& a, const Segment& u, int row, int hf, uint32_t to, float m,
+                                          float l, float scale, bool ok) {
+  const bool store = ok && row < u.rows;
+  float* rec = nullptr;
+  __nv_bfloat16* out = nullptr;
+  if (u.whole) {
+    out = static_cast<__nv_bfloat16*>(a.out) +
+          ((size_t)(a.row0[u.k] + row / a.grp) * a.Hq + u.h * a.grp + row % a.grp) * kD + 64 * hf;
+  } else {
+    rec = a.rec + ((size_t)u.slot * a.unit_rows + (row - u.r0)) * kRecStride;
+    if (store && hf == 0) *reinterpret_cast<float2*>(rec) = make_float2(m == -INFINITY ? m : m * scale, l);
+    rec += 4 + 64 * hf;
+  }
+  const float inv = 1.0f / l;                              // a whole unit's row sees at least one key
+#pragma unroll 1
+  for (int c = 0; c < 64; c += 16) {
+    uint32_t o[16];
+    tmem_ld16(to + c, o);
+    tmem_wait_ld();
+    if (store && !u.whole) {
+#pragma unroll
+      for (int e = 0; e < 16; e += 4)
+        *reinterpret_cast<uint4*>(rec + c + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+    } else if (store) {
+#pragma unroll
+      for (int e = 0; e < 16; e += 8) {
+        uint32_t b[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          b[x] = pack2<true>(__uint_as_float(o[e + 2 * x]) * inv, __uint_as_float(o[e + 2 * x + 1]) * inv);
+        *reinterpret_cast<uint4*>(out + c + e) = make_uint4(b[0], b[1], b[2], b[3]);
+      }
+    }
+    __syncwarp();
+  }
+}
+
+}  // namespace witcert

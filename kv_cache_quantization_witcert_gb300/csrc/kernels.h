@@ -191,34 +191,36 @@ struct ReadArgs {
 };
 cudaError_t launch_read(int scheme, const ReadArgs& a, cudaStream_t st);
 
-// Chunk attention (attend.cu, expand.cu).  Sequences of one launch, passed by value: the n[k]
-// newest tokens of sequence seq[k] (len[k] tokens long) are the queries, packed from token row
-// row0[k] on.  A query row of a KV head is (token, head of the group), token-major: rows_k = n grp.
+// Chunk attention (attend.cuh).  Sequences of one launch, passed by value: the n[k] newest tokens
+// of sequence seq[k] (len[k] tokens long) are the queries, packed from token row row0[k] on.  A
+// query row of a KV head is (token, head of the group), token-major: rows_k = n grp.  A unit is a
+// row tile of one KV head; CTA c takes the key tiles from start[c] up to start[c + 1] in (unit, key
+// tile) order, so every CTA has the same number of them, and a unit that crosses CTAs leaves one
+// record per row and part.
 constexpr int kAttendSeqs = 64;
+constexpr int kAttendCtas = 192;
 constexpr int kTileTok = 128;                    // tokens of a key / value tile
 constexpr int kTileBytes = kTileTok * 128 * 2;   // one operand image: 128 x 128 two-byte elements
 constexpr int kTileRows = 128;                   // query rows of one tensor-core tile
 constexpr int kRecStride = 132;                  // split record: m (log2), l, two unused, 128 sums
+struct AttendStart { int unit, j; };
 struct AttendArgs {
   StoreArgs s;
   const void* q;             // [rows][Hq][128] bf16
   void* out;                 // [rows][Hq][128] bf16
   uint8_t* images;           // [tiles][Hkv][keys, values] operand images
-  float* rec;                // split records
+  float* rec;                // [2 n_ctas][rows of a unit] records: CTA c's unit from before, its unit carried on
   int* err;                  // device error word (waits that ran out)
-  int Hq, grp, n_seq;
+  int Hq, grp, n_seq, n_ctas, unit_rows;
   float scale_log2;          // log2(e) / sqrt(d)
   int seq[kAttendSeqs], n[kAttendSeqs], len[kAttendSeqs], row0[kAttendSeqs];
-  int splits[kAttendSeqs];   // runs of key tiles a query tile is split into
   int tile_off[kAttendSeqs + 1];       // image tiles before sequence k
-  int unit_off[kAttendSeqs + 1];       // CTAs before sequence k
-  long long rec_off[kAttendSeqs + 1];  // records before sequence k (none where there is one part)
+  int unit_off[kAttendSeqs + 1];       // units before sequence k
+  AttendStart start[kAttendCtas + 1];
 };
 cudaError_t launch_expand(int scheme, const AttendArgs& a, cudaStream_t st);
-// pair: one 128-row query tile a CTA, whose two softmax groups take alternate key tiles; otherwise
-// two query tiles a CTA.
-cudaError_t launch_attend(int scheme, const AttendArgs& a, bool pair, cudaStream_t st);
-cudaError_t launch_attend_merge(const AttendArgs& a, bool pair, cudaStream_t st);
+cudaError_t launch_attend(int scheme, const AttendArgs& a, cudaStream_t st);
+cudaError_t launch_attend_merge(const AttendArgs& a, cudaStream_t st);
 
 struct ExportArgs {
   const uint8_t* blocks;

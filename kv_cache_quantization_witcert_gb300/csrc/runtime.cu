@@ -734,86 +734,91 @@ witcert_status witcert_read(witcert_cache* c, int layer, const int32_t* t0, cons
 
 // ------------------------------------------------------------------ chunk attention
 // One group of sequences: expanded, attended and merged by one launch each.
-struct AttendGroup {
-  AttendArgs a;
-  bool pair;
-};
-// Operand images of a group (64 KB per 128 tokens and KV head) stay below this, unless a single
+// Operand images of a group (64 KB per 128 tokens and KV head) stay below kImageCap, unless a single
 // sequence needs more.
 constexpr size_t kImageCap = size_t(2) << 30;
 
-// Splits of the key tiles: CTAs run one an SM, so with U row tiles of up to T key tiles each the
-// launch takes ceil(U s / SMs) rounds of ceil(T / s) tile steps and a fixed part (staging queries,
-// the pipeline's ends: about four steps); more than one part adds the merge (about three).
-static void attend_splits(AttendArgs& a, bool pair, int sm_count) {
-  const int rows_cta = pair ? kTileRows : 2 * kTileRows;
-  int most = 1;
-  for (int k = 0; k < a.n_seq; ++k) most = std::max(most, (a.len[k] + kTileTok - 1) / kTileTok);
-  int best = most;
-  double best_cost = 1e300;
-  for (int s = 1; s <= 64 && s <= most; ++s) {
-    const int per = (most + s - 1) / s;
-    long long units = 0;
-    for (int k = 0; k < a.n_seq; ++k) {
-      const int tiles = (a.len[k] + kTileTok - 1) / kTileTok;
-      units += (long long)a.s.Hkv * ((a.n[k] * a.grp + rows_cta - 1) / rows_cta) * ((tiles + per - 1) / per);
+// Row tiles of sequence k, and key tiles of its row tile number rt in unit order (last rows first).
+static int attend_row_tiles(const AttendArgs& a, int k) { return (int)(((long long)a.n[k] * a.grp + a.unit_rows - 1) / a.unit_rows); }
+static int attend_key_tiles(const AttendArgs& a, int k, int rt) {
+  const long long rows = (long long)a.n[k] * a.grp, r0 = (long long)(attend_row_tiles(a, k) - 1 - rt) * a.unit_rows;
+  const long long last = std::min(rows, r0 + a.unit_rows) - 1;
+  return (int)((a.len[k] - a.n[k] + last / a.grp) / kTileTok) + 1;
+}
+
+// Shares the units' key tiles out to CTAs, one an SM: the same number to each, units cut where that
+// falls, unless whole units do as well.  A cut costs the records' merge and a second start of the
+// pipeline, about kCutTiles key tiles' time, and shares below kMinShare tiles are not worth it.
+static void share_units(AttendArgs& a, int sm_count) {
+  constexpr int kCutTiles = 6, kMinShare = 4;
+  const int Hkv = a.s.Hkv, sms = std::min(sm_count, kAttendCtas);
+  long long total = 0;
+  int units = 0, most = 1;
+  for (int k = 0; k < a.n_seq; ++k) {
+    const int rts = attend_row_tiles(a, k);
+    a.unit_off[k] = units;
+    units += rts * Hkv;
+    for (int rt = 0; rt < rts; ++rt) {
+      const int nt = attend_key_tiles(a, k, rt);
+      total += (long long)nt * Hkv;
+      most = std::max(most, nt);
     }
-    const double rounds = (double)((units + sm_count - 1) / sm_count);
-    const double cost = rounds * (per + 4.0) + (s > 1 && !pair ? 3.0 : 0.0);
-    if (cost < best_cost * 0.999) { best_cost = cost; best = per; }
   }
-  for (int k = 0; k < a.n_seq; ++k) a.splits[k] = ((a.len[k] + kTileTok - 1) / kTileTok + best - 1) / best;
+  a.unit_off[a.n_seq] = units;
+  const int per_cta = (units + sms - 1) / sms;
+  const long long share = std::max<long long>((total + sms - 1) / sms, std::min(kMinShare, most));
+  if ((long long)per_cta * most <= share + kCutTiles) {      // whole units
+    a.n_ctas = (units + per_cta - 1) / per_cta;
+    for (int c = 0; c <= a.n_ctas; ++c) a.start[c] = {std::min(units, c * per_cta), 0};
+    return;
+  }
+  a.n_ctas = (int)((total + share - 1) / share);
+  int c = 0;
+  long long at = 0;                                          // tiles before the present row tile's units
+  for (int k = 0; k < a.n_seq; ++k)
+    for (int rt = 0, rts = attend_row_tiles(a, k); rt < rts; ++rt) {
+      const int nt = attend_key_tiles(a, k, rt);
+      for (; c < a.n_ctas && c * share < at + (long long)nt * Hkv; ++c) {
+        const long long in = c * share - at;
+        a.start[c] = {a.unit_off[k] + rt * Hkv + (int)(in / nt), (int)(in % nt)};
+      }
+      at += (long long)nt * Hkv;
+    }
+  a.start[a.n_ctas] = {units, 0};
 }
 
 // Groups of an attend call; bytes of the images and of the records the largest of them needs.
-static void plan_attend(const witcert_cache* c, int layer, const int32_t* n_tok, std::vector<AttendGroup>& groups,
+static void plan_attend(const witcert_cache* c, int layer, const int32_t* n_tok, std::vector<AttendArgs>& groups,
                         size_t& image_bytes, size_t& rec_bytes) {
   const int B = c->cfg.batch, Hkv = c->cfg.n_kv_heads, grp = c->cfg.n_q_heads / Hkv;
   const size_t tile = (size_t)Hkv * 2 * kTileBytes;
   image_bytes = rec_bytes = 0;
-  for (int pass = 0; pass < 2; ++pass) {
-    const bool pair = pass == 0;               // sequences of at most one row tile
-    int row0 = 0;
-    bool open = false;
-    for (int i = 0; i < B; ++i) {
-      const int n = n_tok[i], len = c->slen[layer][i];
-      const int at = row0;
-      row0 += n;
-      if (n == 0 || (n * (long long)grp <= kTileRows) != pair) continue;
-      const int tiles = (len + kTileTok - 1) / kTileTok;
-      if (open) {
-        const AttendArgs& g = groups.back().a;
-        if (g.n_seq == kAttendSeqs || (g.tile_off[g.n_seq] + (size_t)tiles) * tile > kImageCap) open = false;
-      }
-      if (!open) {
-        groups.emplace_back();
-        AttendGroup& g = groups.back();
-        memset(&g, 0, sizeof g);
-        g.pair = pair;
-        g.a.s = store_args(c, layer);
-        g.a.Hq = c->cfg.n_q_heads; g.a.grp = grp;
-        g.a.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)kD));
-        g.a.err = c->err;
-        open = true;
-      }
-      AttendArgs& a = groups.back().a;
-      const int k = a.n_seq++;
-      a.seq[k] = i; a.n[k] = n; a.len[k] = len; a.row0[k] = at;
-      a.tile_off[k + 1] = a.tile_off[k] + tiles;
+  int row0 = 0;
+  for (int i = 0; i < B; ++i) {
+    const int n = n_tok[i], len = c->slen[layer][i];
+    if (n == 0) continue;
+    const int tiles = (len + kTileTok - 1) / kTileTok;
+    if (groups.empty() || groups.back().n_seq == kAttendSeqs ||
+        (groups.back().tile_off[groups.back().n_seq] + (size_t)tiles) * tile > kImageCap) {
+      groups.emplace_back();
+      AttendArgs& g = groups.back();
+      memset(&g, 0, sizeof g);
+      g.s = store_args(c, layer);
+      g.Hq = c->cfg.n_q_heads; g.grp = grp;
+      g.unit_rows = 2 * kTileRows;
+      g.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)kD));
+      g.err = c->err;
     }
+    AttendArgs& a = groups.back();
+    const int k = a.n_seq++;
+    a.seq[k] = i; a.n[k] = n; a.len[k] = len; a.row0[k] = row0;
+    a.tile_off[k + 1] = a.tile_off[k] + tiles;
+    row0 += n;
   }
-  for (AttendGroup& g : groups) {
-    AttendArgs& a = g.a;
-    attend_splits(a, g.pair, c->sm_count);
-    const int rows_cta = g.pair ? kTileRows : 2 * kTileRows;
-    for (int k = 0; k < a.n_seq; ++k) {
-      const long long rows = (long long)a.n[k] * grp;
-      const int parts = a.splits[k] * (g.pair ? 2 : 1);
-      a.unit_off[k + 1] = a.unit_off[k] + (int)((rows + rows_cta - 1) / rows_cta) * a.splits[k] * Hkv;
-      a.rec_off[k + 1] = a.rec_off[k] + (parts > 1 ? rows * Hkv * parts : 0);
-    }
+  for (AttendArgs& a : groups) {
+    share_units(a, c->sm_count);
     image_bytes = std::max(image_bytes, a.tile_off[a.n_seq] * tile);
-    rec_bytes = std::max(rec_bytes, (size_t)a.rec_off[a.n_seq] * kRecStride * sizeof(float));
+    rec_bytes = std::max(rec_bytes, (size_t)2 * a.n_ctas * a.unit_rows * kRecStride * sizeof(float));
   }
 }
 
@@ -836,7 +841,7 @@ witcert_status witcert_attend_workspace(const witcert_cache* c, int layer, const
   long long rows = 0;
   if (witcert_status s = check_attend(c, layer, n_tok, rows)) return s;
   if (!bytes) return fail(WITCERT_EINVAL, "bytes must not be NULL");
-  std::vector<AttendGroup> groups;
+  std::vector<AttendArgs> groups;
   size_t image = 0, rec = 0;
   plan_attend(c, layer, n_tok, groups, image, rec);
   *bytes = image + rec;
@@ -852,20 +857,20 @@ witcert_status witcert_attend(witcert_cache* c, int layer, const void* q, const 
   if (!q || !out) return fail(WITCERT_EINVAL, "q and out must not be NULL");
   if (((uintptr_t)q | (uintptr_t)out | (uintptr_t)workspace) % 16)
     return fail(WITCERT_EINVAL, "q, out and workspace must be 16-byte aligned");
-  std::vector<AttendGroup> groups;
+  std::vector<AttendArgs> groups;
   size_t image = 0, rec = 0;
   plan_attend(c, layer, n_tok, groups, image, rec);
   if (image + rec > workspace_bytes || !workspace)
     return fail(WITCERT_EINVAL, "the workspace needs %zu bytes, got %zu", image + rec, workspace ? workspace_bytes : 0);
   auto st = static_cast<cudaStream_t>(stream);
   order_after_gate(c, layer, st);
-  for (AttendGroup& g : groups) {
-    g.a.q = q; g.a.out = out;
-    g.a.images = static_cast<uint8_t*>(workspace);
-    g.a.rec = reinterpret_cast<float*>(g.a.images + image);
-    cudaError_t e = launch_expand(c->scheme, g.a, st);
-    if (e == cudaSuccess) e = launch_attend(c->scheme, g.a, g.pair, st);
-    if (e == cudaSuccess) e = launch_attend_merge(g.a, g.pair, st);
+  for (AttendArgs& a : groups) {
+    a.q = q; a.out = out;
+    a.images = static_cast<uint8_t*>(workspace);
+    a.rec = reinterpret_cast<float*>(a.images + image);
+    cudaError_t e = launch_expand(c->scheme, a, st);
+    if (e == cudaSuccess) e = launch_attend(c->scheme, a, st);
+    if (e == cudaSuccess) e = launch_attend_merge(a, st);
     if (e != cudaSuccess) return cuda_fail(e, "attend launch");
   }
   c->last_write_layer = -1;
