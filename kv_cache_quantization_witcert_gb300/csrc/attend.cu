@@ -150,7 +150,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       const int row = u.r0 + w * kTileRows + r;
       float scale = 0.f;
       if (mine) {
-        scale = stage_query<BF16>(a, u, row, r, hf, sm + kSmemQ + w * kTileBytes, pair);
+        uint32_t qw[32];
+        scale = query_words<BF16>(a, u, row, hf, qw, pair);
+        uint8_t* q = sm + kSmemQ + w * kTileBytes + hf * (kTileRows * 128) + r * 128;
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          *reinterpret_cast<uint4*>(q + ((c ^ (r & 7)) << 4)) = make_uint4(qw[4 * c], qw[4 * c + 1], qw[4 * c + 2], qw[4 * c + 3]);
         fence_proxy_async();
       }
       warp_arrive(q_full);
@@ -166,7 +171,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       for (int s = 0; s < u.nk; ++s) {
         if (!pair.ok || !warp_wait(s_full + 8 * w, step++ & 1)) { dead = true; return false; }
         tc_fence_after();
-        softmax_tile<BF16>(ts, tp, to, hf, limit - (u.j0 + s) * kTileTok, s == 0, scale, m, l, pair, p_full + 16 * w);
+        softmax_tile<BF16>(ts, tp, to, hf, limit - (u.j0 + s) * kTileTok, s == 0, scale, m, l, pair, p_full + 16 * w,
+                           [] {});                         // S_w(s) is complete, so O_w += P_w V(s - 1) is
       }
       if (!warp_wait(o_full + 8 * w, done++ & 1)) { dead = true; return false; }
       tc_fence_after();

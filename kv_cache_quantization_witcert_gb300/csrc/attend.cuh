@@ -98,12 +98,12 @@ struct RowPair {
   }
 };
 
-// This thread's half (channels 64 hf ..) of query row `row` of a segment into the swizzled operand
-// tile, as row r; rows past the sequence's are zero.  Returns log2(e)/sqrt(d) times the power of
-// two that the row was divided by: fp16 rows are scaled to a largest element in [1, 2).
+// This thread's half (channels 64 hf ..) of query row `row` of a segment as operand words in the key
+// images' channel order; zero for rows past the sequence's.  Returns log2(e)/sqrt(d) times the power
+// of two that the row was divided by: fp16 rows are scaled to a largest element in [1, 2).
 template <bool BF16>
-__device__ __forceinline__ float stage_query(const AttendArgs& a, const Segment& u, int row, int r, int hf,
-                                             uint8_t* tile, RowPair& pair) {
+__device__ __forceinline__ float query_words(const AttendArgs& a, const Segment& u, int row, int hf, uint32_t (&w)[32],
+                                             RowPair& pair) {
   uint4 v[8];
 #pragma unroll
   for (int c = 0; c < 8; ++c) v[c] = make_uint4(0, 0, 0, 0);
@@ -114,15 +114,22 @@ __device__ __forceinline__ float stage_query(const AttendArgs& a, const Segment&
 #pragma unroll
     for (int c = 0; c < 8; ++c) v[c] = src[c];
   }
+  // 16-byte piece 4 jj + t: channels 32 jj + 4t .. + 3 and 32 jj + 16 + 4t .. + 3
+#pragma unroll
+  for (int jj = 0; jj < 2; ++jj)
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        const uint4& x = v[4 * jj + 2 * m + (t >> 1)];
+        w[16 * jj + 4 * t + 2 * m] = t & 1 ? x.z : x.x;
+        w[16 * jj + 4 * t + 2 * m + 1] = t & 1 ? x.w : x.y;
+      }
   float scale = a.scale_log2;
   if (!BF16) {
     uint32_t top = 0;                                     // largest magnitude's bits, two lanes of bf16
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) top = __vmaxu2(top, w[e] & 0x7FFF7FFFu);
-    }
+    for (int c = 0; c < 32; ++c) top = __vmaxu2(top, w[c] & 0x7FFF7FFFu);
     const int mine = (int)max(top & 0xFFFFu, top >> 16);
     const int both = max(mine, __float_as_int(pair.swap(__int_as_float(mine))));
     // biased exponent of the row's largest element, kept where 2^-e and 2^e are normal numbers
@@ -130,27 +137,20 @@ __device__ __forceinline__ float stage_query(const AttendArgs& a, const Segment&
     const float down = __int_as_float((127 - e) << 23);
     scale *= __int_as_float((127 + e) << 23);
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      uint32_t* w = &v[c].x;
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        w[k] = pack2<false>(__uint_as_float(w[k] << 16) * down, __uint_as_float(w[k] & 0xFFFF0000u) * down);
-    }
+    for (int c = 0; c < 32; ++c)
+      w[c] = pack2<false>(__uint_as_float(w[c] << 16) * down, __uint_as_float(w[c] & 0xFFFF0000u) * down);
     pair.sync();                                          // both have read before the words are used again
   }
-#pragma unroll
-  for (int c = 0; c < 8; ++c)
-    *reinterpret_cast<uint4*>(tile + hf * (kTileRows * 128) + r * 128 + ((c ^ (r & 7)) << 4)) = v[c];
   return scale;
 }
 
 // One key tile's softmax for half a row: logits at ts (64 columns), weights to tp (32 columns, over
-// the logits), O at to (64 columns).  rel: the last place-order token of the tile this row sees (127 or
-// more: all, negative: none).  The weights of the half's first 32 and last 32 places are announced
+// the logits), O at to (64 columns).  rel: the last token of the tile this row sees (127 or more: all,
+// negative: none).  o_wait(): O holds all earlier tiles' products (asked before O is rescaled).  The weights of the half's first 32 and last 32 places are announced
 // on p_bar and p_bar + 8.
-template <bool BF16>
+template <bool BF16, typename W>
 __device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t tp, uint32_t to, int hf, int rel, bool first,
-                                             float scale, float& m, float& l, RowPair& pair, uint32_t p_bar) {
+                                             float scale, float& m, float& l, RowPair& pair, uint32_t p_bar, W o_wait) {
   uint32_t v[2][32];
   tmem_ld32(ts, v[0]);
   tmem_ld32(ts + 32, v[1]);
@@ -161,8 +161,8 @@ __device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t tp, uint32_t 
     for (int c = 0; c < 2; ++c)
 #pragma unroll
       for (int e = 0; e < 32; ++e) {
-        // token of place e (see expand.cu)
-        const int p = e & 15, tok = 32 * c + (e & 16) + 2 * (p >> 2) + (p & 1) + 8 * ((p >> 1) & 1);
+        // token of place e (see expand.cuh)
+        const int tok = 32 * c + 16 * (e & 1) + 2 * (e >> 3) + ((e >> 2) & 1) + 8 * ((e >> 1) & 1);
         if (tok > lim) v[c][e] = 0xFF800000u;
       }
   }
@@ -184,6 +184,7 @@ __device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t tp, uint32_t 
     l *= f;
     m = mn;
     if (!first) {
+      o_wait();
 #pragma unroll 1
       for (int c = 0; c < 64; c += 16) {
         uint32_t o[16];
@@ -259,7 +260,8 @@ template <int N> struct RingAt {
   }
 };
 
-// Half a row of a finished segment: the output itself, or its record.
+// Half a row of a finished segment: the output itself, or its record.  O's columns are in the value
+// images' channel order.
 __device__ __forceinline__ void store_row(const AttendArgs& a, const Segment& u, int row, int hf, uint32_t to, float m,
                                           float l, float scale, bool ok) {
   const bool store = ok && row < u.rows;
@@ -279,17 +281,18 @@ __device__ __forceinline__ void store_row(const AttendArgs& a, const Segment& u,
     uint32_t o[16];
     tmem_ld16(to + c, o);
     tmem_wait_ld();
+    float x[16];                                           // by channel
+#pragma unroll
+    for (int e = 0; e < 16; ++e) x[e] = __uint_as_float(o[(e & 8) + 4 * (e & 1) + ((e & 7) >> 1)]);
     if (store && !u.whole) {
 #pragma unroll
-      for (int e = 0; e < 16; e += 4)
-        *reinterpret_cast<uint4*>(rec + c + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+      for (int e = 0; e < 16; e += 4) *reinterpret_cast<float4*>(rec + c + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
     } else if (store) {
 #pragma unroll
       for (int e = 0; e < 16; e += 8) {
         uint32_t b[4];
 #pragma unroll
-        for (int x = 0; x < 4; ++x)
-          b[x] = pack2<true>(__uint_as_float(o[e + 2 * x]) * inv, __uint_as_float(o[e + 2 * x + 1]) * inv);
+        for (int y = 0; y < 4; ++y) b[y] = pack2<true>(x[e + 2 * y] * inv, x[e + 2 * y + 1] * inv);
         *reinterpret_cast<uint4*>(out + c + e) = make_uint4(b[0], b[1], b[2], b[3]);
       }
     }
