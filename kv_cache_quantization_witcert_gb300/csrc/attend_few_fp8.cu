@@ -1,0 +1,7 @@
+#include "attend_few.cuh"
+
+namespace witcert {
+
+template cudaError_t launch_attend_few<kFp8>(const AttendArgs&, cudaStream_t);
+
+}  // namespace witcert

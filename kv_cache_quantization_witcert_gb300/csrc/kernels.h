@@ -221,6 +221,8 @@ struct AttendArgs {
 cudaError_t launch_expand(int scheme, const AttendArgs& a, cudaStream_t st);
 cudaError_t launch_attend(int scheme, const AttendArgs& a, cudaStream_t st);
 cudaError_t launch_attend_merge(const AttendArgs& a, cudaStream_t st);
+// Straight from the store, without images (units of 128 rows).
+template <int SCH> cudaError_t launch_attend_few(const AttendArgs& a, cudaStream_t st);
 
 struct ExportArgs {
   const uint8_t* blocks;

@@ -787,39 +787,65 @@ static void share_units(AttendArgs& a, int sm_count) {
   a.start[a.n_ctas] = {units, 0};
 }
 
+// Sequences of at most this many query rows a KV head are attended straight from the store, each
+// row tile of 128 reading the codes itself; longer ones share operand images.
+constexpr int kFewRows = kTileRows;
+
 // Groups of an attend call; bytes of the images and of the records the largest of them needs.
 static void plan_attend(const witcert_cache* c, int layer, const int32_t* n_tok, std::vector<AttendArgs>& groups,
                         size_t& image_bytes, size_t& rec_bytes) {
   const int B = c->cfg.batch, Hkv = c->cfg.n_kv_heads, grp = c->cfg.n_q_heads / Hkv;
   const size_t tile = (size_t)Hkv * 2 * kTileBytes;
   image_bytes = rec_bytes = 0;
-  int row0 = 0;
-  for (int i = 0; i < B; ++i) {
-    const int n = n_tok[i], len = c->slen[layer][i];
-    if (n == 0) continue;
-    const int tiles = (len + kTileTok - 1) / kTileTok;
-    if (groups.empty() || groups.back().n_seq == kAttendSeqs ||
-        (groups.back().tile_off[groups.back().n_seq] + (size_t)tiles) * tile > kImageCap) {
-      groups.emplace_back();
-      AttendArgs& g = groups.back();
-      memset(&g, 0, sizeof g);
-      g.s = store_args(c, layer);
-      g.Hq = c->cfg.n_q_heads; g.grp = grp;
-      g.unit_rows = 2 * kTileRows;
-      g.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)kD));
-      g.err = c->err;
+  for (int pass = 0; pass < 2; ++pass) {
+    const bool few = pass == 0;
+    bool open = false;
+    int row0 = 0;
+    for (int i = 0; i < B; ++i) {
+      const int n = n_tok[i], len = c->slen[layer][i], at = row0;
+      row0 += n;
+      if (n == 0 || ((long long)n * grp <= kFewRows) != few) continue;
+      const int tiles = (len + kTileTok - 1) / kTileTok;
+      if (!open || groups.back().n_seq == kAttendSeqs ||
+          (!few && (groups.back().tile_off[groups.back().n_seq] + (size_t)tiles) * tile > kImageCap)) {
+        groups.emplace_back();
+        AttendArgs& g = groups.back();
+        memset(&g, 0, sizeof g);
+        g.s = store_args(c, layer);
+        g.Hq = c->cfg.n_q_heads; g.grp = grp;
+        g.unit_rows = few ? kTileRows : 2 * kTileRows;
+        g.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)kD));
+        g.err = c->err;
+        open = true;
+      }
+      AttendArgs& a = groups.back();
+      const int k = a.n_seq++;
+      a.seq[k] = i; a.n[k] = n; a.len[k] = len; a.row0[k] = at;
+      a.tile_off[k + 1] = a.tile_off[k] + tiles;
     }
-    AttendArgs& a = groups.back();
-    const int k = a.n_seq++;
-    a.seq[k] = i; a.n[k] = n; a.len[k] = len; a.row0[k] = row0;
-    a.tile_off[k + 1] = a.tile_off[k] + tiles;
-    row0 += n;
   }
   for (AttendArgs& a : groups) {
     share_units(a, c->sm_count);
-    image_bytes = std::max(image_bytes, a.tile_off[a.n_seq] * tile);
+    if (a.unit_rows != kTileRows) image_bytes = std::max(image_bytes, a.tile_off[a.n_seq] * tile);
     rec_bytes = std::max(rec_bytes, (size_t)2 * a.n_ctas * a.unit_rows * kRecStride * sizeof(float));
   }
+}
+
+static cudaError_t attend_group(int scheme, const AttendArgs& a, cudaStream_t st) {
+  cudaError_t e;
+  if (a.unit_rows == kTileRows) {
+    switch (scheme) {
+      case kInt8: e = launch_attend_few<kInt8>(a, st); break;
+      case kRtn: e = launch_attend_few<kRtn>(a, st); break;
+      case kFp8: e = launch_attend_few<kFp8>(a, st); break;
+      case kKivi: e = launch_attend_few<kKivi>(a, st); break;
+      default: e = launch_attend_few<kBbox>(a, st); break;
+    }
+  } else {
+    e = launch_expand(scheme, a, st);
+    if (e == cudaSuccess) e = launch_attend(scheme, a, st);
+  }
+  return e == cudaSuccess ? launch_attend_merge(a, st) : e;
 }
 
 static witcert_status check_attend(const witcert_cache* c, int layer, const int32_t* n_tok, long long& rows) {
@@ -868,9 +894,7 @@ witcert_status witcert_attend(witcert_cache* c, int layer, const void* q, const 
     a.q = q; a.out = out;
     a.images = static_cast<uint8_t*>(workspace);
     a.rec = reinterpret_cast<float*>(a.images + image);
-    cudaError_t e = launch_expand(c->scheme, a, st);
-    if (e == cudaSuccess) e = launch_attend(c->scheme, a, st);
-    if (e == cudaSuccess) e = launch_attend_merge(a, st);
+    cudaError_t e = attend_group(c->scheme, a, st);
     if (e != cudaSuccess) return cuda_fail(e, "attend launch");
   }
   c->last_write_layer = -1;
