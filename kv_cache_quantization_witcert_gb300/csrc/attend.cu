@@ -10,7 +10,8 @@
 //   warps 4..11, 12..19   softmax of row tile w (attend.cuh)
 // While one group turns S_w into P_w, the tensor cores run the other tile's products.  S_w(j + 1) is
 // issued after O_w += P_w V(j), so a softmax group that holds S_w(j + 1) may rescale O_w, and a
-// group that holds its last S_w may overwrite Q_w.
+// group that holds its last S_w may overwrite Q_w; and every softmax thread's P_w(j) was announced,
+// so its partner has read what they swapped for tile j.
 //
 // The operands are fp16 for the quantized stores (2^-12 rounding of the decoded values; query rows
 // are scaled by powers of two) and bf16 for the black-box store, whose values bf16 holds exactly;
@@ -68,7 +69,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         // keys and values of a tile in turn
         for (int t = 0; t < 2 * u.nk && !dead; ++t, ++idx) {
           const int st = idx % kStages;
-          if (idx >= kStages && !mbar_wait(empty + 8 * st, (idx / kStages - 1) & 1, kAttendWaitNs)) { dead = true; break; }
+          if (idx >= kStages && !bar_wait(empty + 8 * st, (idx / kStages - 1) & 1)) { dead = true; break; }
           mbar_expect_tx(full + 8 * st, kTileBytes);
           bulk_g2s(skv + st * kTileBytes, img + (size_t)(t >> 1) * stride + (t & 1) * kTileBytes, kTileBytes, full + 8 * st);
         }
@@ -76,7 +77,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       });
       // giving up: the copies in flight still land in this CTA's shared memory
       if (dead)
-        for (int i = max(0, idx - kStages); i < idx; ++i) mbar_wait(full + 8 * (i % kStages), (i / kStages) & 1, kAttendWaitNs);
+        for (int i = max(0, idx - kStages); i < idx; ++i) bar_wait(full + 8 * (i % kStages), (i / kStages) & 1);
     }
   } else if (warp == 1) {
     if (!dead) {
@@ -99,7 +100,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         issue_qk(tm + w * 128, sw128_desc(sq + w * kTileBytes), sw128_desc(skv + st * kTileBytes), idesc, s_full + 8 * w);
       };
       auto pv = [&](int w, uint32_t st, bool first) {
-        return issue_pv(tm + 256 + w * 128, tm + w * 128, sw128_desc(skv + st * kTileBytes), idesc, first,
+        return issue_pv<2>(tm + 256 + w * 128, tm + w * 128, sw128_desc(skv + st * kTileBytes), idesc, first,
                         p_full + 16 * w, steps[w]++ & 1);
       };
       walk(a, cta, [&](const Segment& u) {
@@ -135,13 +136,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       });
       if (dead) {                                          // the MMAs in flight still use this CTA's memories
         warp_commit(drain);
-        mbar_wait(drain, 0, kAttendWaitNs);
+        bar_wait(drain, 0);
       }
     }
   } else if (warp >= 4 && !dead) {
     const int w = (warp - 4) >> 3, hf = ((warp - 4) >> 2) & 1, r = (warp & 3) * 32 + lane;
-    float* swap = reinterpret_cast<float*>(sm + kSmemSwap) + w * 2 * kTileRows;
-    RowPair pair{swap + hf * kTileRows + r, swap + (1 - hf) * kTileRows + r, pairs + 8 * (w * 4 + (warp & 3)), 0, true};
+    RowGroup<2> pair{reinterpret_cast<float*>(sm + kSmemSwap) + w * 2 * kTileRows + r, hf, 0,
+                     pairs + 8 * (w * 4 + (warp & 3)), 0, true};
     const uint32_t lanes = tm + ((uint32_t)(warp & 3) << 21) + w * 128;
     const uint32_t ts = lanes + 64 * hf, tp = lanes + 32 * hf, to = lanes + 256 + 64 * hf;
     uint32_t seg = 0, step = 0, done = 0;
@@ -151,7 +152,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       float scale = 0.f;
       if (mine) {
         uint32_t qw[32];
-        scale = query_words<BF16>(a, u, row, hf, qw, pair);
+        scale = query_words<BF16, 2>(a, u, row, qw, pair);
         uint8_t* q = sm + kSmemQ + w * kTileBytes + hf * (kTileRows * 128) + r * 128;
 #pragma unroll
         for (int c = 0; c < 8; ++c)
@@ -171,13 +172,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       for (int s = 0; s < u.nk; ++s) {
         if (!pair.ok || !warp_wait(s_full + 8 * w, step++ & 1)) { dead = true; return false; }
         tc_fence_after();
-        softmax_tile<BF16>(ts, tp, to, hf, limit - (u.j0 + s) * kTileTok, s == 0, scale, m, l, pair, p_full + 16 * w,
+        softmax_tile<BF16, 2>(ts, tp, to, limit - (u.j0 + s) * kTileTok, s == 0, scale, m, l, pair, p_full + 16 * w,
                            [] {});                         // S_w(s) is complete, so O_w += P_w V(s - 1) is
       }
       if (!warp_wait(o_full + 8 * w, done++ & 1)) { dead = true; return false; }
       tc_fence_after();
-      l += pair.swap(l);
-      store_row(a, u, row, hf, to, m, l, scale, pair.ok);
+      l = pair.sum(l);
+      store_row<2>(a, u, row, hf, to, m, l, scale, pair.ok);
       pair.sync();                                         // the partner has read l
       dead = !pair.ok;
       return !dead;
@@ -194,7 +195,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
 
 // Records of the units that cross CTAs joined: out = sum 2^(m - M) O / sum 2^(m - M) l.  Block row
 // blockIdx.y takes the unit that CTA c = blockIdx.y starts without finishing (its slot 2c + 1, then
-// the slots 2c' of the CTAs that go on); one warp a row.
+// the slots 2c' of the CTAs that go on); one warp a row.  Lane p holds part p's m and l, so the loads
+// of a row's parts do not wait for one another.
 __global__ void __launch_bounds__(256) attend_merge_kernel(const __grid_constant__ AttendArgs a) {
   const int c0 = blockIdx.y, lane = threadIdx.x & 31;
   const AttendStart next = a.start[c0 + 1];
@@ -204,22 +206,36 @@ __global__ void __launch_bounds__(256) attend_merge_kernel(const __grid_constant
   unit_place(a, next.unit, u);
   const int row = u.r0 + blockIdx.x * 8 + (threadIdx.x >> 5);
   if (row >= u.rows || row >= u.r0 + a.unit_rows) return;
+  const float* first = a.rec + ((size_t)2 * c0 * a.unit_rows + (row - u.r0)) * kRecStride;
+  const size_t step = (size_t)2 * a.unit_rows * kRecStride;          // to the next CTA's slot
+  auto part = [&](int p) { return first + p * step + (p == 0 ? step / 2 : 0); };
   float top = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int pass = 0; pass < 2; ++pass) {
-    for (int c = c0; c < a.n_ctas; ++c) {
-      if (c > c0 && !(a.start[c].unit == next.unit && a.start[c].j > 0)) break;
-      const float* r = a.rec + ((size_t)(2 * c + (c == c0 ? 1 : 0)) * a.unit_rows + (row - u.r0)) * kRecStride;
-      const float2 ml = *reinterpret_cast<const float2*>(r);
-      if (pass == 0) {
-        top = fmaxf(top, ml.x);
-        continue;
-      }
-      const float4 v = *reinterpret_cast<const float4*>(r + 4 + 4 * lane);
-      const float f = ex2(ml.x - top);                     // some part sees a key: top is finite (or NaN's row)
-      l = fmaf(f, ml.y, l);
-      o[0] = fmaf(f, v.x, o[0]); o[1] = fmaf(f, v.y, o[1]); o[2] = fmaf(f, v.z, o[2]); o[3] = fmaf(f, v.w, o[3]);
+  for (int p0 = 0; ; p0 += 32) {
+    const int c = c0 + p0 + lane;
+    const bool mine = c < a.n_ctas && (c == c0 || (a.start[c].unit == next.unit && a.start[c].j > 0));
+    const int n = __popc(__ballot_sync(0xffffffffu, mine));          // parts of a unit are consecutive CTAs'
+    const float2 ml = mine ? *reinterpret_cast<const float2*>(part(p0 + lane)) : make_float2(-INFINITY, 0.f);
+    float t = ml.x;
+#pragma unroll
+    for (int x = 16; x; x >>= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, x));
+    t = fmaxf(t, top);
+    const float keep = top == t ? 1.0f : ex2(top - t);               // of what is joined so far
+    const float f = t == -INFINITY ? 0.f : ex2(ml.x - t);            // a part may see no key
+    top = t;
+    l *= keep;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) o[x] *= keep;
+    float s = mine ? f * ml.y : 0.f;
+#pragma unroll
+    for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
+    l += s;
+#pragma unroll 8
+    for (int p = 0; p < n; ++p) {
+      const float4 v = *reinterpret_cast<const float4*>(part(p0 + p) + 4 + 4 * lane);
+      const float w = __shfl_sync(0xffffffffu, f, p);
+      o[0] = fmaf(w, v.x, o[0]); o[1] = fmaf(w, v.y, o[1]); o[2] = fmaf(w, v.z, o[2]); o[3] = fmaf(w, v.w, o[3]);
     }
-    if (top == -INFINITY) top = 0.f;
+    if (n < 32) break;
   }
   const float inv = 1.0f / l;
   *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) +

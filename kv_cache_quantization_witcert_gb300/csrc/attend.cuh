@@ -1,10 +1,10 @@
 // What the chunk attention kernels share: the walk over a CTA's work, the staging of query rows and
 // the softmax of one key tile.
 //
-// A query row is handled by two threads of two warps that can reach the same tensor-memory lanes,
-// each with half of the tile's columns: half the registers, and two warps instead of one to hide
-// the latency of a tile's chain (tensor memory, maximum, exponentials, tensor memory), which is
-// what bounds a step.  They agree on the row's maximum through shared memory and a named barrier.
+// A query row is handled by N threads (two, or four where only few rows are there) of N warps that
+// can reach the same tensor-memory lanes, each with 128 / N of the tile's columns: fewer registers,
+// and more warps to hide the latency of a tile's chain (tensor memory, maximum, exponentials, tensor
+// memory), which is what bounds a step.  They agree on the row's maximum through shared memory.
 //
 // Softmax: weights 2^(s c - m + kOff) with the row's reference m in log2 units.  m follows the
 // running maximum only when that has grown by more than kGrow, so O and the sum l are rescaled
@@ -71,6 +71,23 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
+// Bounded barrier wait.  Each attempt lets the hardware suspend the thread for up to a millisecond
+// (it wakes when the phase completes), so waiting warps take no issue slots from working ones.
+__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000000;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity) {
+  if (bar_try(bar, parity)) return true;
+  const uint64_t t0 = global_ns();
+  while (!bar_try(bar, parity))
+    if (global_ns() - t0 > kAttendWaitNs) return false;
+  return true;
+}
 // One arrival for a warp whose lanes have all come here (their earlier writes included).
 __device__ __forceinline__ void warp_arrive(uint32_t bar) {
   __syncwarp();
@@ -78,45 +95,56 @@ __device__ __forceinline__ void warp_arrive(uint32_t bar) {
 }
 // A wait of a whole warp: its lanes give up together (tensor-memory accesses need all of them).
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
-  return !__any_sync(0xffffffffu, !mbar_wait(bar, parity, kAttendWaitNs));
+  if (__all_sync(0xffffffffu, bar_try(bar, parity))) return true;      // the usual case, 70 cycles
+  return !__any_sync(0xffffffffu, !bar_wait(bar, parity));
 }
 
-// A row's two threads: shared words mine and other, and the barrier of their two warps (an mbarrier
-// of two arrivals, so that the wait has a limit).
-struct RowPair {
-  volatile float *mine, *other;
+// A row's N threads: one shared word each, 128 rows a part, and the barrier of their warps (an
+// mbarrier of N arrivals, so that the wait has a limit).  A combination may overwrite the words of
+// the one before it only when the partners have read them: either something between the two says so
+// (stride 0), or combinations alternate between words `stride` apart, whose last use lies before the
+// combination in between.
+template <int N>
+struct RowGroup {
+  volatile float* words;       // of this row: part p at words[128 p]
+  int part, stride;
   uint32_t bar, phase;
   bool ok;
   __device__ __forceinline__ void sync() {
     warp_arrive(bar);
     ok = ok && warp_wait(bar, phase++ & 1);
   }
-  __device__ __forceinline__ float swap(float v) {
-    *mine = v;
+  template <typename F> __device__ __forceinline__ float all(float v, F f) {
+    volatile float* w = words + (phase & 1 ? stride : 0);
+    w[128 * part] = v;
     sync();
-    return *other;
+#pragma unroll
+    for (int p = 1; p < N; ++p) v = f(v, w[128 * ((part + p) % N)]);
+    return v;
   }
+  __device__ __forceinline__ float top(float v) { return all(v, [](float a, float b) { return fmaxf(a, b); }); }
+  __device__ __forceinline__ float sum(float v) { return all(v, [](float a, float b) { return a + b; }); }
 };
 
-// This thread's half (channels 64 hf ..) of query row `row` of a segment as operand words in the key
-// images' channel order; zero for rows past the sequence's.  Returns log2(e)/sqrt(d) times the power
-// of two that the row was divided by: fp16 rows are scaled to a largest element in [1, 2).
-template <bool BF16>
-__device__ __forceinline__ float query_words(const AttendArgs& a, const Segment& u, int row, int hf, uint32_t (&w)[32],
-                                             RowPair& pair) {
-  uint4 v[8];
+// This thread's 128 / N channels of query row `row` of a segment as operand words in the key images'
+// channel order; zero for rows past the sequence's.  Returns log2(e)/sqrt(d) times the power of two
+// that the row was divided by: fp16 rows are scaled to a largest element in [1, 2).
+template <bool BF16, int N>
+__device__ __forceinline__ float query_words(const AttendArgs& a, const Segment& u, int row, uint32_t (&w)[64 / N],
+                                             RowGroup<N>& grp) {
+  uint4 v[16 / N];
 #pragma unroll
-  for (int c = 0; c < 8; ++c) v[c] = make_uint4(0, 0, 0, 0);
+  for (int c = 0; c < 16 / N; ++c) v[c] = make_uint4(0, 0, 0, 0);
   if (row < u.rows) {
     const uint4* src = reinterpret_cast<const uint4*>(
         static_cast<const __nv_bfloat16*>(a.q) +
-        ((size_t)(a.row0[u.k] + row / a.grp) * a.Hq + u.h * a.grp + row % a.grp) * kD + 64 * hf);
+        ((size_t)(a.row0[u.k] + row / a.grp) * a.Hq + u.h * a.grp + row % a.grp) * kD + (128 / N) * grp.part);
 #pragma unroll
-    for (int c = 0; c < 8; ++c) v[c] = src[c];
+    for (int c = 0; c < 16 / N; ++c) v[c] = src[c];
   }
   // 16-byte piece 4 jj + t: channels 32 jj + 4t .. + 3 and 32 jj + 16 + 4t .. + 3
 #pragma unroll
-  for (int jj = 0; jj < 2; ++jj)
+  for (int jj = 0; jj < 4 / N; ++jj)
 #pragma unroll
     for (int t = 0; t < 4; ++t)
 #pragma unroll
@@ -129,36 +157,38 @@ __device__ __forceinline__ float query_words(const AttendArgs& a, const Segment&
   if (!BF16) {
     uint32_t top = 0;                                     // largest magnitude's bits, two lanes of bf16
 #pragma unroll
-    for (int c = 0; c < 32; ++c) top = __vmaxu2(top, w[c] & 0x7FFF7FFFu);
-    const int mine = (int)max(top & 0xFFFFu, top >> 16);
-    const int both = max(mine, __float_as_int(pair.swap(__int_as_float(mine))));
+    for (int c = 0; c < 64 / N; ++c) top = __vmaxu2(top, w[c] & 0x7FFF7FFFu);
+    // as a bf16 value, which orders like its bits; a NaN or infinity counts as the largest exponent
+    const float mine = __uint_as_float(min(max(top & 0xFFFFu, top >> 16), 0x7F7Fu) << 16);
     // biased exponent of the row's largest element, kept where 2^-e and 2^e are normal numbers
-    const int e = min(max(both >> 7, 16), 238) - 127;
+    const int e = min(max((int)(__float_as_uint(grp.top(mine)) >> 23), 16), 238) - 127;
     const float down = __int_as_float((127 - e) << 23);
     scale *= __int_as_float((127 + e) << 23);
 #pragma unroll
-    for (int c = 0; c < 32; ++c)
+    for (int c = 0; c < 64 / N; ++c)
       w[c] = pack2<false>(__uint_as_float(w[c] << 16) * down, __uint_as_float(w[c] & 0xFFFF0000u) * down);
-    pair.sync();                                          // both have read before the words are used again
+    grp.sync();                                           // all have read before the words are used again
   }
   return scale;
 }
 
-// One key tile's softmax for half a row: logits at ts (64 columns), weights to tp (32 columns, over
-// the logits), O at to (64 columns).  rel: the last token of the tile this row sees (127 or more: all,
-// negative: none).  o_wait(): O holds all earlier tiles' products (asked before O is rescaled).  The weights of the half's first 32 and last 32 places are announced
-// on p_bar and p_bar + 8.
-template <bool BF16, typename W>
-__device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t tp, uint32_t to, int hf, int rel, bool first,
-                                             float scale, float& m, float& l, RowPair& pair, uint32_t p_bar, W o_wait) {
-  uint32_t v[2][32];
-  tmem_ld32(ts, v[0]);
-  tmem_ld32(ts + 32, v[1]);
+// One key tile's softmax for this thread's 128 / N columns of a row: logits at ts, weights to tp (half
+// as many columns, over the logits), O at to.  rel: the last token of the tile this row sees (127 or
+// more: all, negative: none).  o_wait(): O holds all earlier tiles' products (asked before O is
+// rescaled).  The weights of each thread's first and last half of places are announced on p_bar and
+// p_bar + 8.
+template <bool BF16, int N, typename W>
+__device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t tp, uint32_t to, int rel, bool first, float scale,
+                                             float& m, float& l, RowGroup<N>& grp, uint32_t p_bar, W o_wait) {
+  constexpr int kCols = 128 / N;
+  uint32_t v[kCols / 32][32];
+#pragma unroll
+  for (int c = 0; c < kCols / 32; ++c) tmem_ld32(ts + 32 * c, v[c]);
   tmem_wait_ld();
   if (__any_sync(0xffffffffu, rel < kTileTok - 1)) {
-    const int lim = rel - 64 * hf;
+    const int lim = rel - kCols * grp.part;
 #pragma unroll
-    for (int c = 0; c < 2; ++c)
+    for (int c = 0; c < kCols / 32; ++c)
 #pragma unroll
       for (int e = 0; e < 32; ++e) {
         // token of place e (see expand.cuh)
@@ -169,15 +199,15 @@ __device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t tp, uint32_t 
   float mx[4];
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
-    const uint32_t* x = &v[c >> 1][16 * (c & 1)];
+    constexpr int kRun = kCols / 4;
+    const uint32_t* x = &v[c * kRun / 32][c * kRun % 32];
     mx[c] = __uint_as_float(x[0]);
 #pragma unroll
-    for (int e = 1; e < 15; e += 2) mx[c] = max3(mx[c], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
-    mx[c] = fmaxf(mx[c], __uint_as_float(x[15]));
+    for (int e = 1; e + 1 < kRun; e += 2) mx[c] = max3(mx[c], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+    mx[c] = fmaxf(mx[c], __uint_as_float(x[kRun - 1]));
   }
-  float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
-  // the other half's logits have left tensor memory when this returns: weights may overwrite them
-  top = fmaxf(top, pair.swap(top));
+  // the partners' logits have left tensor memory when this returns: weights may overwrite them
+  const float top = grp.top(fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]));
   const bool grow = (top - m) * scale > kGrow;             // also from -inf; false while nothing is visible
   if (__any_sync(0xffffffffu, grow)) {
     const float mn = grow ? top : m, f = grow ? ex2((m - mn) * scale) : 1.0f;
@@ -186,7 +216,7 @@ __device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t tp, uint32_t 
     if (!first) {
       o_wait();
 #pragma unroll 1
-      for (int c = 0; c < 64; c += 16) {
+      for (int c = 0; c < kCols; c += 16) {
         uint32_t o[16];
         tmem_ld16(to + c, o);
         tmem_wait_ld();
@@ -201,15 +231,17 @@ __device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t tp, uint32_t 
   float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
-    uint32_t pk[16];
+    constexpr int kPairs = kCols / 4;                      // weight pairs of half the columns
+    uint32_t pk[kPairs];
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      const float2 x = __ffma2_rn(make_float2(__uint_as_float(v[c][2 * e]), __uint_as_float(v[c][2 * e + 1])), sc2, b2);
+    for (int e = 0; e < kPairs; ++e) {
+      const uint32_t* y = &v[(c * 2 * kPairs + 2 * e) / 32][(c * 2 * kPairs + 2 * e) % 32];
+      const float2 x = __ffma2_rn(make_float2(__uint_as_float(y[0]), __uint_as_float(y[1])), sc2, b2);
       const float2 p = make_float2(ex2(x.x), ex2(x.y));
       sum[e & 1] = __fadd2_rn(sum[e & 1], p);
       pk[e] = pack2<BF16>(p.x, p.y);
     }
-    tmem_st16(tp + 16 * c, pk);
+    tmem_st(tp + kPairs * c, pk);
     tmem_wait_st();
     tc_fence_before();
     warp_arrive(p_bar + 8 * c);
@@ -217,8 +249,9 @@ __device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t tp, uint32_t 
   l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
 }
 
-// O += P V for one tile: A in tensor memory, the value image at descriptor vd; the first and last 32
-// places of each half as they are announced.  False if a wait ran out.
+// O += P V for one tile: A in tensor memory, the value image at descriptor vd; the first and last half
+// of each of the N threads' places as they are announced.  False if a wait ran out.
+template <int N>
 __device__ __forceinline__ bool issue_pv(uint32_t to, uint32_t tp, uint64_t vd, uint32_t idesc, bool first,
                                          uint32_t p_bar, uint32_t parity) {
 #pragma unroll
@@ -228,7 +261,7 @@ __device__ __forceinline__ bool issue_pv(uint32_t to, uint32_t tp, uint64_t vd, 
     if (elect_one()) {
 #pragma unroll
       for (int y = 0; y < 4; ++y) {                        // 16 places a step, 64 a panel
-        const int x = 4 * (y >> 1) + 2 * c + (y & 1);
+        const int x = N == 2 ? 4 * (y >> 1) + 2 * c + (y & 1) : 2 * y + c;
         mma_ts(to, tp + x * 8, vd + (uint64_t)(x >> 2) * (kD * 128 >> 4) + (x & 3) * 2, idesc, !first || c > 0 || y > 0);
       }
     }
@@ -260,24 +293,26 @@ template <int N> struct RingAt {
   }
 };
 
-// Half a row of a finished segment: the output itself, or its record.  O's columns are in the value
-// images' channel order.
-__device__ __forceinline__ void store_row(const AttendArgs& a, const Segment& u, int row, int hf, uint32_t to, float m,
+// This thread's 128 / N columns of a row of a finished segment: the output itself, or its record.  O's
+// columns are in the value images' channel order.
+template <int N>
+__device__ __forceinline__ void store_row(const AttendArgs& a, const Segment& u, int row, int part, uint32_t to, float m,
                                           float l, float scale, bool ok) {
+  constexpr int kCols = 128 / N;
   const bool store = ok && row < u.rows;
   float* rec = nullptr;
   __nv_bfloat16* out = nullptr;
   if (u.whole) {
     out = static_cast<__nv_bfloat16*>(a.out) +
-          ((size_t)(a.row0[u.k] + row / a.grp) * a.Hq + u.h * a.grp + row % a.grp) * kD + 64 * hf;
+          ((size_t)(a.row0[u.k] + row / a.grp) * a.Hq + u.h * a.grp + row % a.grp) * kD + kCols * part;
   } else {
     rec = a.rec + ((size_t)u.slot * a.unit_rows + (row - u.r0)) * kRecStride;
-    if (store && hf == 0) *reinterpret_cast<float2*>(rec) = make_float2(m == -INFINITY ? m : m * scale, l);
-    rec += 4 + 64 * hf;
+    if (store && part == 0) *reinterpret_cast<float2*>(rec) = make_float2(m == -INFINITY ? m : m * scale, l);
+    rec += 4 + kCols * part;
   }
   const float inv = 1.0f / l;                              // a whole unit's row sees at least one key
 #pragma unroll 1
-  for (int c = 0; c < 64; c += 16) {
+  for (int c = 0; c < kCols; c += 16) {
     uint32_t o[16];
     tmem_ld16(to + c, o);
     tmem_wait_ld();

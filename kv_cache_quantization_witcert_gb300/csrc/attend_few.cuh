@@ -2,19 +2,28 @@
 // are made in shared memory, read once and never stored.  Templates; each scheme instantiates them
 // in its own translation unit (attend_few_<scheme>.cu), so the build compiles them in parallel.
 //
-// A unit is 128 query rows of one KV head; the CTAs' shares and records are those of attend.cuh.
-// Bound by HBM: the codes of every tile are read once per row tile, so the stages around the MMAs
-// only have to keep up with about 37 KB a tile (830 ns at an SM's share of HBM).  Twenty warps:
-//   warp 0       one bulk copy per 16-token block into a ring of half tiles (codes as they lie)
-//   warp 1       MMAs: S = Q K^T with Q in tensor memory, O += P V with P in tensor memory: only
-//                the images are read from shared memory
-//   warp 2       tensor memory: S twice (even and odd tiles), O, Q
-//   warps 4..11  softmax, two threads a row (attend.cuh); warps whose rows are all past the end only
-//                keep the barriers going
-//   warps 12..19 images: warp e takes blocks 2 (e / 2), + 1 and half of their channels (expand.cuh)
+// A unit is 128 query rows of one KV head, or 32 where no sequence has more (TINY); the CTAs' shares
+// and records are those of attend.cuh.  Bound by HBM as far as the stages around the MMAs keep up:
+// the codes of a tile, about 37 KB, arrive in 830 ns at an SM's share of HBM.
+//   warp 0    one bulk copy per 16-token block into a ring of half tiles (codes as they lie)
+//   warp 1    MMAs: S = Q K^T with Q in tensor memory, O += P V with P in tensor memory: only the
+//             images are read from shared memory
+//   warp 2    tensor memory: S twice (even and odd tiles), O, Q
+//   softmax   (attend.cuh) general: warps 4..11, two threads a row, warps whose rows are all past the
+//             end only keep the barriers going; TINY: warps 4, 8, 12, 16, four threads a row
+//   images    sixteen warps, eight for the keys and eight for the values, each with two of a tile's
+//             blocks and half of their channels (expand.cuh).  General: warps 12..27; TINY: the other
+//             warps of 5..23
+// The rows of TINY lie in the first 32 lanes of tensor memory, which only warps 0 mod 4 reach: all
+// its softmax runs on one scheduler of the SM, whose other warps would slow its chain down (general
+// kernel with 32 rows: 3100 cycles a tile, all of them the softmax's), so the images are made on
+// the other three (one warp but).  The general softmax needs more registers than an even split gives, and its
+// warpgroups trade them: launched with 72 a thread, 504 a lane of the seven groups; 40 + 2 x 96 +
+// 4 x 64 = 488.
 // Two S buffers let S(j + 1) be formed while P(j) is; O += P V(j) follows S(j + 1), so a softmax warp
-// that must rescale O waits for it.  Images live in a ring of four 32 KB stages, keys and values of a
-// tile in turn.
+// that must rescale O waits for it, and a row's threads swap through alternate words (S(j + 1) says
+// nothing about the partners' P(j)).  Images live in a ring of four 32 KB stages, keys and values of
+// a tile in turn.
 #pragma once
 #include "attend.cuh"
 #include "expand.cuh"
@@ -23,46 +32,51 @@ namespace witcert {
 
 namespace {
 
-constexpr int kFewThreads = 640;
 constexpr int kFewImages = 4;
 constexpr int kHalfBlocks = kTileTok / kBlk / 2;           // blocks of a half tile
-template <int SCH> struct FewSmem {
+template <int SCH, bool TINY> struct FewSmem {
+  static constexpr int kThreads = TINY ? 768 : 896;
+  static constexpr int kN = TINY ? 4 : 2;                  // threads a row
+  static constexpr int kSoftWarps = TINY ? 4 : 8;
   static constexpr int kHalf = kHalfBlocks * block_bytes(SCH);
   // half tiles of codes in flight: what fits beside the images, at most eight
-  static constexpr int kScratch = SCH == kInt8 ? 8 * kXsFloats * 4 : 0;
-  static constexpr int kRoom = 232448 - kFewImages * kTileBytes - kScratch - 2 * kTileRows * 4 - 512;
-  static constexpr int kRing = kRoom / kHalf < 8 ? kRoom / kHalf : 8;
+  static constexpr int kScratch = SCH == kInt8 ? 8 * kXwWords * 4 : 0;
+  static constexpr int kRoom = 232448 - kFewImages * kTileBytes - kScratch - 2 * kN * kTileRows * 4 - 512;
+  // (an even number, so that a stage always holds the same half and the same warps see its every use)
+  static constexpr int kRing = kRoom / kHalf < 8 ? kRoom / kHalf / 2 * 2 : 8;
   static constexpr int kRaw = kFewImages * kTileBytes;
   static constexpr int kXs = kRaw + kRing * kHalf;
   static constexpr int kSwap = kXs + kScratch;
-  static constexpr int kBar = kSwap + 2 * kTileRows * 4;
+  static constexpr int kBar = kSwap + 2 * kN * kTileRows * 4;
   static constexpr int kBytes = kBar + 512;
   static_assert(kRing >= 2 && kHalf % 16 == 0, "two half tiles at least");
 };
 
-template <int SCH>
-__global__ void __launch_bounds__(kFewThreads, 1) attend_few_kernel(const __grid_constant__ AttendArgs a) {
-  using L = FewSmem<SCH>;
+template <int SCH, bool TINY>
+__global__ void __launch_bounds__(FewSmem<SCH, TINY>::kThreads, 1) attend_few_kernel(const __grid_constant__ AttendArgs a) {
+  using L = FewSmem<SCH, TINY>;
+  constexpr int N = L::kN;
   constexpr bool BF16 = SCH == kBbox;
   constexpr int kRing = L::kRing;
   extern __shared__ __align__(1024) uint8_t sm[];
   const uint32_t base = smem_addr(sm), bars = base + L::kBar;
   const uint32_t q_full = bars, raw_full = bars + 8, raw_empty = raw_full + 8 * kRing, img_full = raw_empty + 8 * kRing;
   const uint32_t img_empty = img_full + 8 * kFewImages, s_full = img_empty + 8 * kFewImages, p_full = s_full + 16;
-  const uint32_t pv_done = p_full + 32, pairs = pv_done + 8, drain = pairs + 32, slot = drain + 8;
+  const uint32_t pv_done = p_full + 32, o_full = pv_done + 8, pairs = o_full + 8, drain = pairs + 32, slot = drain + 8;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
 
   if (threadIdx.x == 0) {
-    mbar_init(q_full, 8);
-    for (int s = 0; s < kRing; ++s) { mbar_init(raw_full + 8 * s, 1); mbar_init(raw_empty + 8 * s, 4); }
+    mbar_init(q_full, L::kSoftWarps);
+    for (int s = 0; s < kRing; ++s) { mbar_init(raw_full + 8 * s, 1); mbar_init(raw_empty + 8 * s, 8); }
     for (int s = 0; s < kFewImages; ++s) { mbar_init(img_full + 8 * s, 8); mbar_init(img_empty + 8 * s, 1); }
     for (int b = 0; b < 2; ++b) {
       mbar_init(s_full + 8 * b, 1);
-      mbar_init(p_full + 16 * b, 8);
-      mbar_init(p_full + 16 * b + 8, 8);
+      mbar_init(p_full + 16 * b, L::kSoftWarps);
+      mbar_init(p_full + 16 * b + 8, L::kSoftWarps);
     }
     mbar_init(pv_done, 1);
-    for (int x = 0; x < 4; ++x) mbar_init(pairs + 8 * x, 2);
+    mbar_init(o_full, 1);
+    for (int x = 0; x < 4; ++x) mbar_init(pairs + 8 * x, N);
     mbar_init(drain, 1);
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
@@ -74,7 +88,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) attend_few_kernel(const __grid
   const uint32_t tmem_o = tm + 256, tmem_q = tm + 384;
   bool dead = (base & 1023u) != 0;                         // a wait ran out (or no aligned tiles): give up, in order
 
-  if (warp == 0 && !dead) {
+  auto produce = [&]() {
     // lane b < 4 copies block b of the half tile
     RingAt<kRing> at;
     int filled = 0;
@@ -96,8 +110,9 @@ __global__ void __launch_bounds__(kFewThreads, 1) attend_few_kernel(const __grid
     });
     // giving up: the copies in flight still land in this CTA's shared memory
     if (dead)
-      for (int f = max(0, filled - kRing); f < filled; ++f) mbar_wait(raw_full + 8 * (f % kRing), (f / kRing) & 1, kAttendWaitNs);
-  } else if (warp == 1 && !dead) {
+      for (int f = max(0, filled - kRing); f < filled; ++f) bar_wait(raw_full + 8 * (f % kRing), (f / kRing) & 1);
+  };
+  auto multiply = [&]() {
     constexpr uint32_t idesc = mma_idesc(BF16, kTileRows, kTileTok);
     int tiles = 0, done = 0;                               // of this CTA; tiles whose keys were taken
     uint32_t seg = 0;
@@ -130,9 +145,9 @@ __global__ void __launch_bounds__(kFewThreads, 1) attend_few_kernel(const __grid
         const int j = done + s;
         if (s + 1 < u.nk) dead = !qk(j + 1);
         dead = dead || !wait_image(2 * j + 1) ||
-               !issue_pv(tmem_o, tm + (j & 1) * 128, sw128_desc(image(2 * j + 1)), idesc, s == 0, p_full + 16 * (j & 1), (j >> 1) & 1);
+               !issue_pv<N>(tmem_o, tm + (j & 1) * 128, sw128_desc(image(2 * j + 1)), idesc, s == 0, p_full + 16 * (j & 1), (j >> 1) & 1);
         if (dead) return false;
-        warp_commit(pv_done);
+        warp_commit(s + 1 < u.nk ? pv_done : o_full);
         release(2 * j + 1);
       }
       done += u.nk;
@@ -140,23 +155,26 @@ __global__ void __launch_bounds__(kFewThreads, 1) attend_few_kernel(const __grid
     });
     if (dead) {                                            // the MMAs in flight still use this CTA's memories
       warp_commit(drain);
-      mbar_wait(drain, 0, kAttendWaitNs);
+      bar_wait(drain, 0);
     }
-  } else if (warp >= 4 && warp < 12 && !dead) {
-    const int hf = (warp - 4) >> 2, r = (warp & 3) * 32 + lane;
-    float* swap = reinterpret_cast<float*>(sm + L::kSwap);
-    RowPair pair{swap + hf * kTileRows + r, swap + (1 - hf) * kTileRows + r, pairs + 8 * (warp & 3), 0, true};
-    const uint32_t lanes = (uint32_t)(warp & 3) << 21, to = tmem_o + lanes + 64 * hf;
+  };
+  auto softmax = [&](int part) {
+    constexpr int kCols = 128 / N;
+    const int r = (warp & 3) * 32 + lane;
+    RowGroup<N> grp{reinterpret_cast<float*>(sm + L::kSwap) + r, part, N * kTileRows, pairs + 8 * (warp & 3), 0, true};
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21, to = tmem_o + lanes + kCols * part;
     int j = 0;                                             // tiles of this CTA so far
+    uint32_t seg = 0, sums = 0;                            // segments so far; their products that were not the last
     walk(a, cta, [&](const Segment& u) {
       const int row = u.r0 + r;
       const bool busy = u.r0 + (warp & 3) * 32 < u.rows;   // some row of the warp is a query
       float scale = 0.f, m = -INFINITY, l = 0.f;
       if (busy) {
-        uint32_t qw[32];
-        scale = query_words<BF16>(a, u, row, hf, qw, pair);
-        tmem_st16(tmem_q + lanes + 32 * hf, *reinterpret_cast<uint32_t(*)[16]>(qw));
-        tmem_st16(tmem_q + lanes + 32 * hf + 16, *reinterpret_cast<uint32_t(*)[16]>(qw + 16));
+        uint32_t qw[64 / N];
+        scale = query_words<BF16, N>(a, u, row, qw, grp);
+#pragma unroll
+        for (int c = 0; c < 64 / N; c += 16)
+          tmem_st16(tmem_q + lanes + (64 / N) * part + c, *reinterpret_cast<uint32_t(*)[16]>(qw + c));
         tmem_wait_st();
       }
       tc_fence_before();
@@ -165,60 +183,81 @@ __global__ void __launch_bounds__(kFewThreads, 1) attend_few_kernel(const __grid
       const int limit = row < u.rows ? a.len[u.k] - a.n[u.k] + row / a.grp : -1;
       for (int s = 0; s < u.nk; ++s, ++j) {
         const uint32_t ts = tm + (j & 1) * 128 + lanes, pb = p_full + 16 * (j & 1);
-        if (!pair.ok || !warp_wait(s_full + 8 * (j & 1), (j >> 1) & 1)) { dead = true; return false; }
+        if (!grp.ok || !warp_wait(s_full + 8 * (j & 1), (j >> 1) & 1)) { dead = true; return false; }
         tc_fence_after();
         if (busy) {
-          softmax_tile<BF16>(ts + 64 * hf, ts + 32 * hf, to, hf, limit - (u.j0 + s) * kTileTok, s == 0, scale, m, l, pair, pb,
-                             [&] { pair.ok = pair.ok && warp_wait(pv_done, (j - 1) & 1); tc_fence_after(); });
+          softmax_tile<BF16, N>(ts + kCols * part, ts + kCols / 2 * part, to, limit - (u.j0 + s) * kTileTok, s == 0, scale, m, l,
+                                grp, pb, [&] { grp.ok = grp.ok && warp_wait(pv_done, (sums - 1) & 1); tc_fence_after(); });
         } else {
           warp_arrive(pb);
           warp_arrive(pb + 8);
         }
+        sums += s + 1 < u.nk;
       }
-      if (!warp_wait(pv_done, (j - 1) & 1)) { dead = true; return false; }
+      // a barrier of its own: the products before the last may be two phases behind, which a parity
+      // does not tell
+      if (!warp_wait(o_full, seg++ & 1)) { dead = true; return false; }
       tc_fence_after();
       if (busy) {
-        l += pair.swap(l);
-        store_row(a, u, row, hf, to, m, l, scale, pair.ok);
+        l = grp.sum(l);
+        store_row<N>(a, u, row, part, to, m, l, scale, grp.ok);
         tc_fence_before();
-        pair.sync();                                       // the partner has read l
       }
-      dead = !pair.ok;
+      dead = !grp.ok;
       return !dead;
     });
-  } else if (warp >= 12 && !dead) {
+  };
+  // One of the sixteen warps that make images.
+  auto expand = [&](int e) {
+    const int values = e >> 3, half = (e >> 2) & 1, j0 = 2 * (e & 1);
     BlockPair x;
-    x.pr = (warp - 12) >> 1; x.jh = warp & 1; x.lane = lane;
-    float* xs = SCH == kInt8 ? reinterpret_cast<float*>(sm + L::kXs) + (warp - 12) * kXsFloats : nullptr;
-    RingAt<kRing> at;                                      // half tiles: this warp reads every second one
-    if (x.pr >> 1) at.next();
-    RingAt<kFewImages> img;
+    x.lane = lane;
+    x.pr = (e >> 1) & 3;
+    [[maybe_unused]] uint32_t* xs = reinterpret_cast<uint32_t*>(sm + L::kXs) + (e & 7) * kXwWords;
+    RingAt<kRing / 2> at;                                  // the tile's halves: stages 2 at.st and + 1
+    RingAt<kFewImages / 2> img;                            // image x of the CTA in stage x mod 4: keys 0 and 2, values 1 and 3
     int made = 0;
     walk(a, cta, [&](const Segment& u) {
       x.h = u.h;
       x.len = a.len[u.k];
-      for (int j = u.j0; j < u.j0 + u.nk; ++j) {
+      for (int j = u.j0; j < u.j0 + u.nk; ++j, ++made) {
+        const int raw_st = 2 * at.st + half, st = 2 * img.st + values;
         x.tb = j * kTileTok + x.pr * 2 * kBlk;
-        const uint8_t* raw = sm + L::kRaw + at.st * L::kHalf + (x.pr & 1) * 2 * block_bytes(SCH);
-        x.bp[0] = raw;
-        x.bp[1] = raw + block_bytes(SCH);
-        find_exact<SCH>(a.s, a.seq[u.k], x);
-        if (!warp_wait(raw_full + 8 * at.st, at.ph)) { dead = true; return false; }
-        for (int v = 0; v < 2; ++v) {
-          if (made >= kFewImages && !warp_wait(img_empty + 8 * img.st, img.ph ^ 1)) { dead = true; return false; }
-          if (v == 0) expand_keys<SCH>(a.s, x, sm + img.st * kTileBytes);
-          else expand_values<SCH>(a.s, x, xs, sm + img.st * kTileBytes);
-          fence_proxy_async();
-          warp_arrive(img_full + 8 * img.st);
-          img.next();
-          ++made;
+        x.bp[0] = sm + L::kRaw + raw_st * L::kHalf + (x.pr & 1) * 2 * block_bytes(SCH);
+        x.bp[1] = x.bp[0] + block_bytes(SCH);
+        if (!warp_wait(raw_full + 8 * raw_st, at.ph) ||
+            (made >= kFewImages / 2 && !warp_wait(img_empty + 8 * st, img.ph ^ 1))) { dead = true; return false; }
+        if (values) {
+          expand_values<SCH>(a.s, x, j0, xs, sm + st * kTileBytes, [&] { warp_arrive(raw_empty + 8 * raw_st); });
+        } else {
+          find_exact<SCH>(a.s, a.seq[u.k], x);
+          expand_keys<SCH>(a.s, x, j0, sm + st * kTileBytes, [&] { warp_arrive(raw_empty + 8 * raw_st); });
         }
-        warp_arrive(raw_empty + 8 * at.st);
-        at.next();
+        fence_proxy_async();
+        warp_arrive(img_full + 8 * st);
+        img.next();
         at.next();
       }
       return true;
     });
+  };
+
+  if (dead) {
+  } else if (TINY) {
+    if (warp == 0) produce();
+    else if (warp == 1) multiply();
+    else if (warp >= 4 && warp < 20 && (warp & 3) == 0) softmax((warp - 4) >> 2);
+    else if (warp >= 4) expand(warp < 20 ? 3 * ((warp - 4) >> 2) + (warp & 3) - 1 : warp - 8);
+  } else if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;\n");
+    if (warp == 0) produce();
+    else if (warp == 1) multiply();
+  } else if (warp < 12) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 96;\n");
+    softmax((warp - 4) >> 2);
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;\n");
+    expand(warp - 12);
   }
   if (dead) atomicAdd(a.err, 1);
   tc_fence_before();
@@ -231,12 +270,18 @@ __global__ void __launch_bounds__(kFewThreads, 1) attend_few_kernel(const __grid
 
 }  // namespace
 
+template <int SCH, bool TINY>
+cudaError_t launch_few(const AttendArgs& a, cudaStream_t st) {
+  using L = FewSmem<SCH, TINY>;
+  cudaError_t e = cudaFuncSetAttribute(attend_few_kernel<SCH, TINY>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
+  if (e != cudaSuccess) return e;
+  attend_few_kernel<SCH, TINY><<<(unsigned)a.n_ctas, L::kThreads, L::kBytes, st>>>(a);
+  return cudaGetLastError();
+}
+
 template <int SCH>
 cudaError_t launch_attend_few(const AttendArgs& a, cudaStream_t st) {
-  cudaError_t e = cudaFuncSetAttribute(attend_few_kernel<SCH>, cudaFuncAttributeMaxDynamicSharedMemorySize, FewSmem<SCH>::kBytes);
-  if (e != cudaSuccess) return e;
-  attend_few_kernel<SCH><<<(unsigned)a.n_ctas, kFewThreads, FewSmem<SCH>::kBytes, st>>>(a);
-  return cudaGetLastError();
+  return a.unit_rows == kTinyRows ? launch_few<SCH, true>(a, st) : launch_few<SCH, false>(a, st);
 }
 
 }  // namespace witcert

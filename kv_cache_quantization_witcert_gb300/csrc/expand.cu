@@ -12,7 +12,7 @@ namespace {
 
 template <int SCH>
 __global__ void __launch_bounds__(256) expand_kernel(const __grid_constant__ AttendArgs a) {
-  __shared__ float scratch[SCH == kInt8 ? 8 : 1][SCH == kInt8 ? kXsFloats : 1];
+  __shared__ __align__(16) uint32_t scratch[SCH == kInt8 ? 8 : 1][SCH == kInt8 ? kXwWords : 1];
   const int warp = threadIdx.x >> 5;
   const int tile_all = blockIdx.x / a.s.Hkv;
   int k = 0;
@@ -20,7 +20,7 @@ __global__ void __launch_bounds__(256) expand_kernel(const __grid_constant__ Att
   const int i = a.seq[k];
   BlockPair x;
   x.h = blockIdx.x % a.s.Hkv;
-  x.pr = warp >> 1; x.jh = warp & 1; x.lane = threadIdx.x & 31;
+  x.pr = warp >> 1; x.lane = threadIdx.x & 31;
   x.tb = (tile_all - a.tile_off[k]) * kTileTok + x.pr * 2 * kBlk;
   x.len = a.len[k];
   uint8_t* img = a.images + ((size_t)tile_all * a.s.Hkv + x.h) * 2 * kTileBytes;
@@ -31,8 +31,8 @@ __global__ void __launch_bounds__(256) expand_kernel(const __grid_constant__ Att
     x.bp[b] = a.s.blocks + block_index(a.s.table, a.s.Hkv, a.s.nblk_max, i, x.h,
                                        x.tb + b * kBlk < x.len ? x.tb / kBlk + b : first) * block_bytes(SCH);
   find_exact<SCH>(a.s, i, x);
-  expand_keys<SCH>(a.s, x, img);
-  expand_values<SCH>(a.s, x, scratch[SCH == kInt8 ? warp : 0], img + kTileBytes);
+  expand_keys<SCH>(a.s, x, 2 * (warp & 1), img, [] {});
+  expand_values<SCH>(a.s, x, 2 * (warp & 1), scratch[SCH == kInt8 ? warp : 0], img + kTileBytes, [] {});
 }
 
 }  // namespace

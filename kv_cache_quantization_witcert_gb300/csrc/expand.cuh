@@ -29,127 +29,191 @@ template <int SCH> __device__ __forceinline__ uint32_t operand2(float a, float b
   return half2_sat(__floats2half2_rn(a, b));
 }
 
-// Keys of step j of a block as operand pairs: w[m][r][p] = channels 32j + 16m + 4t + 2p, + 1 of token
-// g + 8r.  The undithered stores are decoded in fp16 with a single rounding.
-template <int SCH>
-__device__ __forceinline__ void key_words(const StoreArgs& s, const uint8_t* bp, int h, int tb, int j, int lane,
-                                          uint32_t (&w)[2][2][2]) {
-  const int g = lane >> 2, t = lane & 3;
-  if constexpr (SCH == kFp8) {
-    const uint4 c = *reinterpret_cast<const uint4*>(bp + Fp8Layout::KC + j * 512 + lane * 16);
-#pragma unroll
-    for (int m = 0; m < 2; ++m)
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        w[m][r][0] = e4m3x2_lo(word_of(c, 2 * m + r));
-        w[m][r][1] = e4m3x2_hi(word_of(c, 2 * m + r));
-      }
-  } else if constexpr (SCH == kRtn) {
-    const uint4 c = *reinterpret_cast<const uint4*>(bp + Int8Layout::KC + j * 512 + lane * 16);
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const __half2 sc = __half2half2(*reinterpret_cast<const __half*>(bp + Int8Layout::KS + ((g + 8 * r) * 4 + j) * 2));
-#pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        w[m][r][0] = half2_sat(__hmul2(bits_h2(i8x2_lo(word_of(c, 2 * m + r))), sc));
-        w[m][r][1] = half2_sat(__hmul2(bits_h2(i8x2_hi(word_of(c, 2 * m + r))), sc));
-      }
-    }
-  } else if constexpr (SCH == kKivi) {
-    const uint32_t c = *reinterpret_cast<const uint32_t*>(bp + KiviLayout::KC + lane * 16 + j * 4);
-#pragma unroll
-    for (int m = 0; m < 2; ++m) {
-      const uint8_t* kp = bp + KiviLayout::KP + (t * 32 + (2 * j + m) * 4) * 2;
-      const uint2 sc = *reinterpret_cast<const uint2*>(kp), zr = *reinterpret_cast<const uint2*>(kp + 256);
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        w[m][r][0] = half2_sat(__hfma2(bits_h2(u2x2(c, m * 4 + r)), bits_h2(sc.x), bits_h2(zr.x)));
-        w[m][r][1] = half2_sat(__hfma2(bits_h2(u2x2(c, m * 4 + r + 2)), bits_h2(sc.y), bits_h2(zr.y)));
-      }
-    }
-  } else if constexpr (SCH == kBbox) {
-#pragma unroll
-    for (int m = 0; m < 2; ++m) {
-      const uint4 c = *reinterpret_cast<const uint4*>(bp + BboxLayout::KH + ((2 * j + m) * 32 + lane) * 16);
-      w[m][0][0] = c.x; w[m][0][1] = c.z; w[m][1][0] = c.y; w[m][1][1] = c.w;
-    }
-  } else {
-    float x[2][2][4];
-    block_keys<SCH>(s, bp, h, tb, j, lane, x);
-#pragma unroll
-    for (int m = 0; m < 2; ++m)
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        w[m][r][0] = operand2<SCH>(x[m][r][0], x[m][r][1]);
-        w[m][r][1] = operand2<SCH>(x[m][r][2], x[m][r][3]);
-      }
-  }
+// The dithered store's operand: s (code - xi) = code s + (-xi) s with one rounding of the sum; -xi is
+// 1.5 - (1 + its upper 23 random bits), rounded to fp16 (an error below 2^-12 s), without an
+// integer-to-float conversion.
+__device__ __forceinline__ uint32_t neg_xi2(uint32_t u0, uint32_t u1) {
+  return h2_bits(__floats2half2_rn(1.5f - __uint_as_float(__funnelshift_r(u0, 0x7Fu, 9)),
+                                   1.5f - __uint_as_float(__funnelshift_r(u1, 0x7Fu, 9))));
+}
+__device__ __forceinline__ uint4 dither_words(const StoreArgs& s, int h, int t, int quad, int tensor) {
+  return philox4x32_10_rk(make_uint4((uint32_t)t, (uint32_t)quad | ((uint32_t)tensor << 16),
+                                     (uint32_t)h | ((uint32_t)s.layer << 16), 0u), s.rk0, s.rk1);
+}
+__device__ __forceinline__ uint32_t dithered2(uint32_t code2, uint32_t nxi2, __half2 sc) {
+  return half2_sat(__hfma2(bits_h2(code2), sc, __hmul2(bits_h2(nxi2), sc)));
 }
 
-// Values of step j of a block as operand pairs: w[m][r][p] = tokens 2t + 8p, 2t + 8p + 1 of channel
-// 32j + 16m + 8r + g.
-template <int SCH>
-__device__ __forceinline__ void value_words(const StoreArgs& s, const uint8_t* bp, int h, int tb, int j, int lane,
-                                            float* xs, uint32_t (&w)[2][2][2]) {
-  const int t = lane & 3;
-  if constexpr (SCH == kFp8) {
-    const uint4 c = *reinterpret_cast<const uint4*>(bp + Fp8Layout::VC + j * 512 + lane * 16);
+// Four E4M3 codes as two fp16 pairs (exact).
+__device__ __forceinline__ void e4m3x4_pairs(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.rn.f16x2.e4m3x2 %0, l;\n cvt.rn.f16x2.e4m3x2 %1, h;\n}\n"
+      : "=r"(lo), "=r"(hi) : "r"(w));
+}
+
+// Steps j0 and j0 + 1 of a block's keys as a lane reads them (j0 = 0 or 2): codes and what decodes them.
+// Decoding follows separately, so that the codes' buffer can be given back in between.
+//   words(jj): step j0 + jj as operand pairs, w[m][r][p] = channels 32j + 16m + 4t + 2p, + 1 of token g + 8r
+// The undithered stores are decoded in fp16 with a single rounding.
+template <int SCH> struct KeyCodes {
+  uint4 c[SCH == kBbox ? 4 : 2];         // black box: (step, m)
+  uint32_t sc[2];                        // INT8: the steps' scales of tokens g and g + 8
+  __device__ __forceinline__ void load(const uint8_t* bp, int j0, int lane) {
+    if constexpr (SCH == kBbox) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) c[k] = *reinterpret_cast<const uint4*>(bp + BboxLayout::KH + ((2 * j0 + k) * 32 + lane) * 16);
+    } else {
+      static_assert(Int8Layout::KC == Fp8Layout::KC, "one place for the codes");
+#pragma unroll
+      for (int jj = 0; jj < 2; ++jj) c[jj] = *reinterpret_cast<const uint4*>(bp + Int8Layout::KC + (j0 + jj) * 512 + lane * 16);
+      if constexpr (int8_layout(SCH)) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+          sc[r] = *reinterpret_cast<const uint32_t*>(bp + Int8Layout::KS + (((lane >> 2) + 8 * r) * 4 + j0) * 2);
+      }
+    }
+  }
+  __device__ __forceinline__ void words(const StoreArgs& s, int h, int tb, int j0, int jj, int lane, uint32_t (&w)[2][2][2]) const {
+    const int g = lane >> 2, t = lane & 3;
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        w[m][r][0] = e4m3x2_lo(word_of(c, 2 * m + r));
-        w[m][r][1] = e4m3x2_hi(word_of(c, 2 * m + r));
+        if constexpr (SCH == kBbox) {
+          const uint4& x = c[2 * jj + m];
+          w[m][r][0] = r ? x.y : x.x;
+          w[m][r][1] = r ? x.w : x.z;
+        } else if constexpr (SCH == kFp8) {
+          e4m3x4_pairs(word_of(c[jj], 2 * m + r), w[m][r][0], w[m][r][1]);
+        } else {
+          const uint32_t x = word_of(c[jj], 2 * m + r);
+          const __half2 s2 = bits_h2(__byte_perm(sc[r], 0, jj ? 0x3232 : 0x1010));
+          if constexpr (SCH == kInt8) {
+            const uint4 u = dither_words(s, h, tb + g + 8 * r, 8 * (j0 + jj) + 4 * m + t, 0);
+            w[m][r][0] = dithered2(i8x2_lo(x), neg_xi2(u.x, u.y), s2);
+            w[m][r][1] = dithered2(i8x2_hi(x), neg_xi2(u.z, u.w), s2);
+          } else {
+            w[m][r][0] = half2_sat(__hmul2(bits_h2(i8x2_lo(x)), s2));
+            w[m][r][1] = half2_sat(__hmul2(bits_h2(i8x2_hi(x)), s2));
+          }
+        }
       }
-  } else if constexpr (SCH == kRtn) {
-    const uint4 c = *reinterpret_cast<const uint4*>(bp + Int8Layout::VC + j * 512 + lane * 16);
-    const uint2 sc = *reinterpret_cast<const uint2*>(bp + Int8Layout::VS + (j * 16 + 4 * t) * 2);
+  }
+};
+template <> struct KeyCodes<kKivi> {
+  uint2 c;
+  uint4 sc[2], zr[2];                    // (step, m): four channels' scales and zeros
+  __device__ __forceinline__ void load(const uint8_t* bp, int j0, int lane) {
+    c = *reinterpret_cast<const uint2*>(bp + KiviLayout::KC + lane * 16 + j0 * 4);
+    const uint8_t* kp = bp + KiviLayout::KP + ((lane & 3) * 32 + 2 * j0 * 4) * 2;
+#pragma unroll
+    for (int jj = 0; jj < 2; ++jj) {
+      sc[jj] = *reinterpret_cast<const uint4*>(kp + 16 * jj);
+      zr[jj] = *reinterpret_cast<const uint4*>(kp + 256 + 16 * jj);
+    }
+  }
+  __device__ __forceinline__ void words(const StoreArgs&, int, int, int, int jj, int, uint32_t (&w)[2][2][2]) const {
+    const uint32_t x = jj ? c.y : c.x;
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
+          w[m][r][p] = half2_sat(__hfma2(bits_h2(u2x2(x, m * 4 + r + 2 * p)), bits_h2(word_of(sc[jj], 2 * m + p)),
+                                         bits_h2(word_of(zr[jj], 2 * m + p))));
+  }
+};
+
+constexpr int kXwPitch = 40;                       // words per token pair: a lane's picks fall on distinct banks
+constexpr int kXwWords = 8 * kXwPitch;             // scratch of one warp (dithered store only)
+
+// The same for values: w[m][r][p] = tokens 2t + 8p, 2t + 8p + 1 of channel 32j + 16m + 8r + g.
+template <int SCH> struct ValueCodes {
+  uint4 c[SCH == kBbox ? 4 : 2];
+  uint2 sc[2];                           // INT8: the step's scales of the lane's four tokens
+  __device__ __forceinline__ void load(const uint8_t* bp, int j0, int lane) {
+    if constexpr (SCH == kBbox) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) c[k] = *reinterpret_cast<const uint4*>(bp + BboxLayout::VH + ((2 * j0 + k) * 32 + lane) * 16);
+    } else {
+      static_assert(Int8Layout::VC == Fp8Layout::VC, "one place for the codes");
+#pragma unroll
+      for (int jj = 0; jj < 2; ++jj) {
+        c[jj] = *reinterpret_cast<const uint4*>(bp + Int8Layout::VC + (j0 + jj) * 512 + lane * 16);
+        if constexpr (int8_layout(SCH)) sc[jj] = *reinterpret_cast<const uint2*>(bp + Int8Layout::VS + ((j0 + jj) * 16 + 4 * (lane & 3)) * 2);
+      }
+    }
+  }
+  __device__ __forceinline__ void words(const StoreArgs& s, int h, int tb, int j0, int jj, int lane, uint32_t* xs,
+                                        uint32_t (&w)[2][2][2]) const {
+    const int g = lane >> 2, t = lane & 3;
+    if constexpr (SCH == kInt8) {
+      // the step's 16 tokens x 32 channels of -xi as token pairs: a lane forms two tokens of a channel
+      // quad at a time, and picks out its own channels' pairs
+      __syncwarp();
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int pr = 4 * k + (lane >> 3), q = lane & 7;    // tokens 2 pr, 2 pr + 1
+        const uint4 u = dither_words(s, h, tb + 2 * pr, 8 * (j0 + jj) + q, 1), v = dither_words(s, h, tb + 2 * pr + 1, 8 * (j0 + jj) + q, 1);
+        *reinterpret_cast<uint4*>(xs + pr * kXwPitch + 4 * q) =
+            make_uint4(neg_xi2(u.x, v.x), neg_xi2(u.y, v.y), neg_xi2(u.z, v.z), neg_xi2(u.w, v.w));
+      }
+      __syncwarp();
+    }
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        w[m][r][0] = half2_sat(__hmul2(bits_h2(i8x2_lo(word_of(c, 2 * m + r))), bits_h2(sc.x)));
-        w[m][r][1] = half2_sat(__hmul2(bits_h2(i8x2_hi(word_of(c, 2 * m + r))), bits_h2(sc.y)));
+        if constexpr (SCH == kBbox) {
+          const uint4& x = c[2 * jj + m];
+          w[m][r][0] = r ? x.y : x.x;
+          w[m][r][1] = r ? x.w : x.z;
+        } else if constexpr (SCH == kFp8) {
+          e4m3x4_pairs(word_of(c[jj], 2 * m + r), w[m][r][0], w[m][r][1]);
+        } else {
+          const uint32_t x = word_of(c[jj], 2 * m + r);
+          const __half2 lo = bits_h2(sc[jj].x), hi = bits_h2(sc[jj].y);
+          if constexpr (SCH == kInt8) {
+            const uint32_t* nx = xs + t * kXwPitch + 16 * m + 8 * r + g;
+            w[m][r][0] = dithered2(i8x2_lo(x), nx[0], lo);
+            w[m][r][1] = dithered2(i8x2_hi(x), nx[4 * kXwPitch], hi);
+          } else {
+            w[m][r][0] = half2_sat(__hmul2(bits_h2(i8x2_lo(x)), lo));
+            w[m][r][1] = half2_sat(__hmul2(bits_h2(i8x2_hi(x)), hi));
+          }
+        }
       }
-  } else if constexpr (SCH == kKivi) {
-    const uint32_t c = *reinterpret_cast<const uint32_t*>(bp + KiviLayout::VC + lane * 16 + j * 4);
+  }
+};
+template <> struct ValueCodes<kKivi> {
+  uint2 c, sz[4];                        // tokens 2t, 2t + 1, 2t + 8, 2t + 9: the steps' (scale, zero) pairs
+  __device__ __forceinline__ void load(const uint8_t* bp, int j0, int lane) {
+    c = *reinterpret_cast<const uint2*>(bp + KiviLayout::VC + lane * 16 + j0 * 4);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      sz[e] = *reinterpret_cast<const uint2*>(bp + KiviLayout::VP + ((2 * (lane & 3) + (e & 1) + 8 * (e >> 1)) * 4 + j0) * 4);
+  }
+  __device__ __forceinline__ void words(const StoreArgs&, int, int, int, int jj, int, uint32_t*, uint32_t (&w)[2][2][2]) const {
+    const uint32_t x = jj ? c.y : c.x;
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
-      // (scale, zero) of tokens 2t + 8p and 2t + 8p + 1
-      const __half2 a = *reinterpret_cast<const __half2*>(bp + KiviLayout::VP + ((2 * t + 8 * p) * 4 + j) * 4);
-      const __half2 b = *reinterpret_cast<const __half2*>(bp + KiviLayout::VP + ((2 * t + 8 * p + 1) * 4 + j) * 4);
+      const __half2 a = bits_h2(jj ? sz[2 * p].y : sz[2 * p].x), b = bits_h2(jj ? sz[2 * p + 1].y : sz[2 * p + 1].x);
       const __half2 sc = __lows2half2(a, b), zr = __highs2half2(a, b);
 #pragma unroll
       for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int r = 0; r < 2; ++r) w[m][r][p] = half2_sat(__hfma2(bits_h2(u2x2(c, m * 4 + r + 2 * p)), sc, zr));
+        for (int r = 0; r < 2; ++r) w[m][r][p] = half2_sat(__hfma2(bits_h2(u2x2(x, m * 4 + r + 2 * p)), sc, zr));
     }
-  } else if constexpr (SCH == kBbox) {
-#pragma unroll
-    for (int m = 0; m < 2; ++m) {
-      const uint4 c = *reinterpret_cast<const uint4*>(bp + BboxLayout::VH + ((2 * j + m) * 32 + lane) * 16);
-      w[m][0][0] = c.x; w[m][0][1] = c.z; w[m][1][0] = c.y; w[m][1][1] = c.w;
-    }
-  } else {
-    float x[2][2][4];
-    block_values<SCH>(s, bp, h, tb, j, lane, xs, x);
-#pragma unroll
-    for (int m = 0; m < 2; ++m)
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        w[m][r][0] = operand2<SCH>(x[m][r][0], x[m][r][1]);
-        w[m][r][1] = operand2<SCH>(x[m][r][2], x[m][r][3]);
-      }
   }
-}
+};
 
-// Two blocks of a tile (token group pr = 0..3, first token at position-in-sequence tb), and half of
-// their channels (steps 2 jh, 2 jh + 1), by one warp.  Blocks past the sequence may be anything.
+// Two blocks of a tile (token group pr = 0..3, first token at position-in-sequence tb) for one warp.
+// Blocks past the sequence may be anything.
 struct BlockPair {
   const uint8_t* bp[2];
   const void* exact[2];          // exact key rows instead of the codes, or null
   bool ebf[2];
-  int h, tb, len, pr, jh, lane;
+  int h, tb, len, pr, lane;
 };
 // The blocks' exact rows (see exact_rows), looked up where the sequence i holds the block.
 template <int SCH>
@@ -162,67 +226,93 @@ __device__ __forceinline__ void find_exact(const StoreArgs& s, int i, BlockPair&
       x.exact[b] = exact_rows<SCH>(s, i, x.h, x.tb / kBlk + b, x.len, x.ebf[b]);
   }
 }
-template <int SCH>
-__device__ __forceinline__ void expand_keys(const StoreArgs& s, const BlockPair& x, uint8_t* img) {
+// Steps j0 and j0 + 1 (j0 = 0 or 2: one panel of the key image) of the two blocks into the key image,
+// or the value image.  got() is called when the codes are in registers.  Everything is decoded before
+// anything is stored: loads do not pass stores that might alias them.  (The dithered store, bound by
+// its integer work, takes the steps one by one.)
+template <int SCH, typename F>
+__device__ __forceinline__ void expand_keys(const StoreArgs& s, const BlockPair& x, int j0, uint8_t* img, F got) {
+  constexpr int kSteps = SCH == kInt8 ? 1 : 2;
   const int g = x.lane >> 2, t = x.lane & 3;
   const bool tail = x.tb + 2 * kBlk > x.len;
-#pragma unroll 1
-  for (int j = 2 * x.jh; j < 2 * x.jh + 2; ++j)
+  KeyCodes<SCH> codes[2];
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      uint32_t w[2][2][2];
-      if (x.exact[b]) {
-        float v[2][2][4];
-        exact_keys(s, x.exact[b], x.ebf[b], j, x.lane, v);
+  for (int b = 0; b < 2; ++b) codes[b].load(x.bp[b], j0, x.lane);
+  got();
 #pragma unroll
-        for (int m = 0; m < 2; ++m)
+  for (int ja = 0; ja < 2; ja += kSteps) {
+    uint32_t w[kSteps][2][2][2][2];                          // [jj][b][m][r][p]
 #pragma unroll
-          for (int r = 0; r < 2; ++r)
+    for (int jj = 0; jj < kSteps; ++jj)
 #pragma unroll
-            for (int p = 0; p < 2; ++p) w[m][r][p] = operand2<SCH>(v[m][r][2 * p], v[m][r][2 * p + 1]);
-      } else {
-        key_words<SCH>(s, x.bp[b], x.h, s.pos0 + x.tb + b * kBlk, j, x.lane, w);
-      }
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const int row = 32 * x.pr + 8 * (g >> 1) + 4 * (g & 1) + 2 * r + b;
-        uint4 v = make_uint4(w[0][r][0], w[0][r][1], w[1][r][0], w[1][r][1]);
-        if (tail && x.tb + b * kBlk + g + 8 * r >= x.len) v = make_uint4(0, 0, 0, 0);
-        *reinterpret_cast<uint4*>(img + (j >> 1) * (kTileTok * 128) + row * 128 + (((4 * (j & 1) + t) ^ (row & 7)) << 4)) = v;
-      }
-    }
-}
-template <int SCH>
-__device__ __forceinline__ void expand_values(const StoreArgs& s, const BlockPair& x, float* xs, uint8_t* img) {
-  const int g = x.lane >> 2, t = x.lane & 3;
-  const bool tail = x.tb + 2 * kBlk > x.len;
-#pragma unroll 1
-  for (int j = 2 * x.jh; j < 2 * x.jh + 2; ++j) {
-    uint32_t w[2][2][2][2];                                  // [b][m][r][p]
-#pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      value_words<SCH>(s, x.bp[b], x.h, s.pos0 + x.tb + b * kBlk, j, x.lane, xs, w[b]);
-      if (tail) {
-#pragma unroll
-        for (int p = 0; p < 2; ++p) {
-          const int tok = x.tb + b * kBlk + 2 * t + 8 * p;
-          const uint32_t keep = tok + 1 < x.len ? 0xFFFFFFFFu : tok < x.len ? 0xFFFFu : 0u;
+      for (int b = 0; b < 2; ++b) {
+        if (x.exact[b]) {
+          float v[2][2][4];
+          exact_keys(s, x.exact[b], x.ebf[b], j0 + ja + jj, x.lane, v);
 #pragma unroll
           for (int m = 0; m < 2; ++m)
 #pragma unroll
-            for (int r = 0; r < 2; ++r) w[b][m][r][p] &= keep;
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+              for (int p = 0; p < 2; ++p) w[jj][b][m][r][p] = operand2<SCH>(v[m][r][2 * p], v[m][r][2 * p + 1]);
+        } else {
+          codes[b].words(s, x.h, s.pos0 + x.tb + b * kBlk, j0, ja + jj, x.lane, w[jj][b]);
         }
       }
-    }
 #pragma unroll
-    for (int m = 0; m < 2; ++m)
+    for (int jj = 0; jj < kSteps; ++jj)
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const int row = 32 * j + 16 * m + 8 * r + 4 * (g & 1) + (g >> 1);
-        const uint4 v = make_uint4(__byte_perm(w[0][m][r][0], w[1][m][r][0], 0x5410), __byte_perm(w[0][m][r][1], w[1][m][r][1], 0x5410),
-                                   __byte_perm(w[0][m][r][0], w[1][m][r][0], 0x7632), __byte_perm(w[0][m][r][1], w[1][m][r][1], 0x7632));
-        *reinterpret_cast<uint4*>(img + (x.pr >> 1) * (kD * 128) + row * 128 + (((4 * (x.pr & 1) + t) ^ (row & 7)) << 4)) = v;
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const int row = 32 * x.pr + 8 * (g >> 1) + 4 * (g & 1) + 2 * r + b;
+          uint4 v = make_uint4(w[jj][b][0][r][0], w[jj][b][0][r][1], w[jj][b][1][r][0], w[jj][b][1][r][1]);
+          if (tail && x.tb + b * kBlk + g + 8 * r >= x.len) v = make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4*>(img + (j0 >> 1) * (kTileTok * 128) + row * 128 + (((4 * (ja + jj) + t) ^ (row & 7)) << 4)) = v;
+        }
+  }
+}
+template <int SCH, typename F>
+__device__ __forceinline__ void expand_values(const StoreArgs& s, const BlockPair& x, int j0, uint32_t* xs, uint8_t* img, F got) {
+  constexpr int kSteps = SCH == kInt8 ? 1 : 2;
+  const int g = x.lane >> 2, t = x.lane & 3;
+  const bool tail = x.tb + 2 * kBlk > x.len;
+  ValueCodes<SCH> codes[2];
+#pragma unroll
+  for (int b = 0; b < 2; ++b) codes[b].load(x.bp[b], j0, x.lane);
+  got();
+#pragma unroll
+  for (int ja = 0; ja < 2; ja += kSteps) {
+    uint32_t w[kSteps][2][2][2][2];                          // [jj][b][m][r][p]
+#pragma unroll
+    for (int jj = 0; jj < kSteps; ++jj)
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        codes[b].words(s, x.h, s.pos0 + x.tb + b * kBlk, j0, ja + jj, x.lane, xs, w[jj][b]);
+        if (tail) {
+#pragma unroll
+          for (int p = 0; p < 2; ++p) {
+            const int tok = x.tb + b * kBlk + 2 * t + 8 * p;
+            const uint32_t keep = tok + 1 < x.len ? 0xFFFFFFFFu : tok < x.len ? 0xFFFFu : 0u;
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+              for (int r = 0; r < 2; ++r) w[jj][b][m][r][p] &= keep;
+          }
+        }
       }
+#pragma unroll
+    for (int jj = 0; jj < kSteps; ++jj)
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const uint32_t (&a)[2] = w[jj][0][m][r], (&b)[2] = w[jj][1][m][r];
+          const int row = 32 * (j0 + ja + jj) + 16 * m + 8 * r + 4 * (g & 1) + (g >> 1);
+          *reinterpret_cast<uint4*>(img + (x.pr >> 1) * (kD * 128) + row * 128 + (((4 * (x.pr & 1) + t) ^ (row & 7)) << 4)) =
+              make_uint4(__byte_perm(a[0], b[0], 0x5410), __byte_perm(a[1], b[1], 0x5410), __byte_perm(a[0], b[0], 0x7632),
+                         __byte_perm(a[1], b[1], 0x7632));
+        }
   }
 }
 

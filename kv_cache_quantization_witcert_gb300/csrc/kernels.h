@@ -202,6 +202,7 @@ constexpr int kAttendCtas = 192;
 constexpr int kTileTok = 128;                    // tokens of a key / value tile
 constexpr int kTileBytes = kTileTok * 128 * 2;   // one operand image: 128 x 128 two-byte elements
 constexpr int kTileRows = 128;                   // query rows of one tensor-core tile
+constexpr int kTinyRows = 32;                    // units of sequences with so few rows (one tensor-memory quadrant)
 constexpr int kRecStride = 132;                  // split record: m (log2), l, two unused, 128 sums
 struct AttendStart { int unit, j; };
 struct AttendArgs {
@@ -221,7 +222,7 @@ struct AttendArgs {
 cudaError_t launch_expand(int scheme, const AttendArgs& a, cudaStream_t st);
 cudaError_t launch_attend(int scheme, const AttendArgs& a, cudaStream_t st);
 cudaError_t launch_attend_merge(const AttendArgs& a, cudaStream_t st);
-// Straight from the store, without images (units of 128 rows).
+// Straight from the store, without images (units of kTileRows or kTinyRows rows).
 template <int SCH> cudaError_t launch_attend_few(const AttendArgs& a, cudaStream_t st);
 
 struct ExportArgs {

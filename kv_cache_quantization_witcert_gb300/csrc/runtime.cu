@@ -797,14 +797,15 @@ static void plan_attend(const witcert_cache* c, int layer, const int32_t* n_tok,
   const int B = c->cfg.batch, Hkv = c->cfg.n_kv_heads, grp = c->cfg.n_q_heads / Hkv;
   const size_t tile = (size_t)Hkv * 2 * kTileBytes;
   image_bytes = rec_bytes = 0;
-  for (int pass = 0; pass < 2; ++pass) {
-    const bool few = pass == 0;
+  for (const int unit_rows : {kTinyRows, kTileRows, 2 * kTileRows}) {
+    const bool few = unit_rows <= kTileRows;
     bool open = false;
     int row0 = 0;
     for (int i = 0; i < B; ++i) {
       const int n = n_tok[i], len = c->slen[layer][i], at = row0;
       row0 += n;
-      if (n == 0 || ((long long)n * grp <= kFewRows) != few) continue;
+      const long long rows = (long long)n * grp;
+      if (n == 0 || unit_rows != (rows <= kTinyRows ? kTinyRows : rows <= kFewRows ? kTileRows : 2 * kTileRows)) continue;
       const int tiles = (len + kTileTok - 1) / kTileTok;
       if (!open || groups.back().n_seq == kAttendSeqs ||
           (!few && (groups.back().tile_off[groups.back().n_seq] + (size_t)tiles) * tile > kImageCap)) {
@@ -813,7 +814,7 @@ static void plan_attend(const witcert_cache* c, int layer, const int32_t* n_tok,
         memset(&g, 0, sizeof g);
         g.s = store_args(c, layer);
         g.Hq = c->cfg.n_q_heads; g.grp = grp;
-        g.unit_rows = few ? kTileRows : 2 * kTileRows;
+        g.unit_rows = unit_rows;
         g.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)kD));
         g.err = c->err;
         open = true;
@@ -826,14 +827,14 @@ static void plan_attend(const witcert_cache* c, int layer, const int32_t* n_tok,
   }
   for (AttendArgs& a : groups) {
     share_units(a, c->sm_count);
-    if (a.unit_rows != kTileRows) image_bytes = std::max(image_bytes, a.tile_off[a.n_seq] * tile);
+    if (a.unit_rows > kTileRows) image_bytes = std::max(image_bytes, a.tile_off[a.n_seq] * tile);
     rec_bytes = std::max(rec_bytes, (size_t)2 * a.n_ctas * a.unit_rows * kRecStride * sizeof(float));
   }
 }
 
 static cudaError_t attend_group(int scheme, const AttendArgs& a, cudaStream_t st) {
   cudaError_t e;
-  if (a.unit_rows == kTileRows) {
+  if (a.unit_rows <= kTileRows) {
     switch (scheme) {
       case kInt8: e = launch_attend_few<kInt8>(a, st); break;
       case kRtn: e = launch_attend_few<kRtn>(a, st); break;
