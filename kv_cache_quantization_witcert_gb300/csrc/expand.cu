@@ -35,7 +35,29 @@ __global__ void __launch_bounds__(256) expand_kernel(const __grid_constant__ Att
   expand_values<SCH>(a.s, x, 2 * (warp & 1), scratch[SCH == kInt8 ? warp : 0], img + kTileBytes, [] {});
 }
 
+// The dither of a tile and head in the order the expanding lanes fetch it.
+__global__ void __launch_bounds__(256) dither_kernel(const __grid_constant__ StoreArgs s, uint4* table) {
+  __shared__ __align__(16) uint32_t scratch[8][kXwWords];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int h = blockIdx.x % s.Hkv, tile = blockIdx.x / s.Hkv, pr = warp >> 1, j0 = 2 * (warp & 1);
+#pragma unroll 1
+  for (int k = 0; k < 8; ++k) {
+    const int values = k >> 2, j = j0 + ((k >> 1) & 1), b = k & 1, tb = s.pos0 + tile * kTileTok + (2 * pr + b) * kBlk;
+    uint32_t n[2][2][2];
+    if (values) value_dither(s, h, tb, j, lane, scratch[warp], n);
+    else key_dither(s, h, tb, j, lane, n);
+    uint4* to = table + dither_at(s.Hkv, tile, h, values, pr, j, b, lane);
+    to[0] = make_uint4(n[0][0][0], n[0][0][1], n[0][1][0], n[0][1][1]);
+    to[32] = make_uint4(n[1][0][0], n[1][0][1], n[1][1][0], n[1][1][1]);
+  }
+}
+
 }  // namespace
+
+cudaError_t launch_dither_table(const StoreArgs& s, uint4* table, int tiles, cudaStream_t st) {
+  dither_kernel<<<(unsigned)(tiles * s.Hkv), 256, 0, st>>>(s, table);
+  return cudaGetLastError();
+}
 
 cudaError_t launch_expand(int scheme, const AttendArgs& a, cudaStream_t st) {
   const unsigned grid = (unsigned)(a.tile_off[a.n_seq] * a.s.Hkv);

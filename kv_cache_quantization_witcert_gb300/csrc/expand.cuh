@@ -40,6 +40,51 @@ __device__ __forceinline__ uint4 dither_words(const StoreArgs& s, int h, int t, 
   return philox4x32_10_rk(make_uint4((uint32_t)t, (uint32_t)quad | ((uint32_t)tensor << 16),
                                      (uint32_t)h | ((uint32_t)s.layer << 16), 0u), s.rk0, s.rk1);
 }
+// -xi of step j of a block's keys, n[m][r][p] = channels 32j + 16m + 4t + 2p, + 1 of token g + 8r.
+__device__ __forceinline__ void key_dither(const StoreArgs& s, int h, int tb, int j, int lane, uint32_t (&n)[2][2][2]) {
+#pragma unroll
+  for (int m = 0; m < 2; ++m)
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const uint4 u = dither_words(s, h, tb + (lane >> 2) + 8 * r, 8 * j + 4 * m + (lane & 3), 0);
+      n[m][r][0] = neg_xi2(u.x, u.y);
+      n[m][r][1] = neg_xi2(u.z, u.w);
+    }
+}
+// -xi of step j of its values, n[m][r][p] = tokens 2t + 8p, 2t + 8p + 1 of channel 32j + 16m + 8r + g.  One
+// Philox call gives four channels of a token: a lane forms two tokens of a channel quad at a time in
+// the warp's scratch xs, and picks out its own channels' pairs.
+constexpr int kXwPitch = 40;                       // words per token pair: a lane's picks fall on distinct banks
+constexpr int kXwWords = 8 * kXwPitch;             // scratch of one warp
+__device__ __forceinline__ void value_dither(const StoreArgs& s, int h, int tb, int j, int lane, uint32_t* xs,
+                                             uint32_t (&n)[2][2][2]) {
+  __syncwarp();
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int pr = 4 * k + (lane >> 3), q = lane & 7;      // tokens 2 pr, 2 pr + 1
+    const uint4 u = dither_words(s, h, tb + 2 * pr, 8 * j + q, 1), v = dither_words(s, h, tb + 2 * pr + 1, 8 * j + q, 1);
+    *reinterpret_cast<uint4*>(xs + pr * kXwPitch + 4 * q) =
+        make_uint4(neg_xi2(u.x, v.x), neg_xi2(u.y, v.y), neg_xi2(u.z, v.z), neg_xi2(u.w, v.w));
+  }
+  __syncwarp();
+#pragma unroll
+  for (int m = 0; m < 2; ++m)
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+      for (int p = 0; p < 2; ++p) n[m][r][p] = xs[((lane & 3) + 4 * p) * kXwPitch + 16 * m + 8 * r + (lane >> 2)];
+}
+// The dither depends on position, head and layer, not on the sequence: where several sequences are
+// read, it is formed once, in the lanes' order, and fetched (dither_kernel in expand.cu).  Place of
+// (tile, head, keys or values, token group, step, block) in 16-byte pieces, two a lane.
+__device__ __forceinline__ size_t dither_at(int Hkv, int tile, int h, int values, int pr, int j, int b, int lane) {
+  return (((((((size_t)tile * Hkv + h) * 2 + values) * 4 + pr) * 4 + j) * 2 + b) * 2) * 32 + lane;
+}
+__device__ __forceinline__ void load_dither(const uint4* table, size_t at, uint32_t (&n)[2][2][2]) {
+  const uint4 lo = table[at], hi = table[at + 32];
+  n[0][0][0] = lo.x; n[0][0][1] = lo.y; n[0][1][0] = lo.z; n[0][1][1] = lo.w;
+  n[1][0][0] = hi.x; n[1][0][1] = hi.y; n[1][1][0] = hi.z; n[1][1][1] = hi.w;
+}
 __device__ __forceinline__ uint32_t dithered2(uint32_t code2, uint32_t nxi2, __half2 sc) {
   return half2_sat(__hfma2(bits_h2(code2), sc, __hmul2(bits_h2(nxi2), sc)));
 }
@@ -50,13 +95,18 @@ __device__ __forceinline__ void e4m3x4_pairs(uint32_t w, uint32_t& lo, uint32_t&
       : "=r"(lo), "=r"(hi) : "r"(w));
 }
 
-// Steps j0 and j0 + 1 of a block's keys as a lane reads them (j0 = 0 or 2): codes and what decodes them.
+// kSteps steps of a block's keys from step j0 on as a lane reads them: codes and what decodes them.
 // Decoding follows separately, so that the codes' buffer can be given back in between.
-//   words(jj): step j0 + jj as operand pairs, w[m][r][p] = channels 32j + 16m + 4t + 2p, + 1 of token g + 8r
-// The undithered stores are decoded in fp16 with a single rounding.
+//   words(jj, n): step j0 + jj as operand pairs, w[m][r][p] = channels 32j + 16m + 4t + 2p, + 1 of token g + 8r
+//   (n: its -xi, dithered store)
+// The stores are decoded in fp16, the undithered ones with a single rounding.  The dithered store
+// takes the steps one by one: its integer work, not memory, bounds it.
+template <int SCH> constexpr int kSteps = SCH == kInt8 ? 1 : 2;
+
 template <int SCH> struct KeyCodes {
-  uint4 c[SCH == kBbox ? 4 : 2];         // black box: (step, m)
-  uint32_t sc[2];                        // INT8: the steps' scales of tokens g and g + 8
+  static constexpr int S = kSteps<SCH>;
+  uint4 c[SCH == kBbox ? 4 : S];         // black box: (step, m)
+  __half2 sc[S][2];                      // INT8: the steps' scales of tokens g and g + 8, twice
   __device__ __forceinline__ void load(const uint8_t* bp, int j0, int lane) {
     if constexpr (SCH == kBbox) {
 #pragma unroll
@@ -64,16 +114,17 @@ template <int SCH> struct KeyCodes {
     } else {
       static_assert(Int8Layout::KC == Fp8Layout::KC, "one place for the codes");
 #pragma unroll
-      for (int jj = 0; jj < 2; ++jj) c[jj] = *reinterpret_cast<const uint4*>(bp + Int8Layout::KC + (j0 + jj) * 512 + lane * 16);
-      if constexpr (int8_layout(SCH)) {
+      for (int jj = 0; jj < S; ++jj) {
+        c[jj] = *reinterpret_cast<const uint4*>(bp + Int8Layout::KC + (j0 + jj) * 512 + lane * 16);
+        if constexpr (int8_layout(SCH)) {
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
-          sc[r] = *reinterpret_cast<const uint32_t*>(bp + Int8Layout::KS + (((lane >> 2) + 8 * r) * 4 + j0) * 2);
+          for (int r = 0; r < 2; ++r)
+            sc[jj][r] = __half2half2(*reinterpret_cast<const __half*>(bp + Int8Layout::KS + (((lane >> 2) + 8 * r) * 4 + j0 + jj) * 2));
+        }
       }
     }
   }
-  __device__ __forceinline__ void words(const StoreArgs& s, int h, int tb, int j0, int jj, int lane, uint32_t (&w)[2][2][2]) const {
-    const int g = lane >> 2, t = lane & 3;
+  __device__ __forceinline__ void words(int jj, const uint32_t (&n)[2][2][2], uint32_t (&w)[2][2][2]) const {
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -86,14 +137,12 @@ template <int SCH> struct KeyCodes {
           e4m3x4_pairs(word_of(c[jj], 2 * m + r), w[m][r][0], w[m][r][1]);
         } else {
           const uint32_t x = word_of(c[jj], 2 * m + r);
-          const __half2 s2 = bits_h2(__byte_perm(sc[r], 0, jj ? 0x3232 : 0x1010));
           if constexpr (SCH == kInt8) {
-            const uint4 u = dither_words(s, h, tb + g + 8 * r, 8 * (j0 + jj) + 4 * m + t, 0);
-            w[m][r][0] = dithered2(i8x2_lo(x), neg_xi2(u.x, u.y), s2);
-            w[m][r][1] = dithered2(i8x2_hi(x), neg_xi2(u.z, u.w), s2);
+            w[m][r][0] = dithered2(i8x2_lo(x), n[m][r][0], sc[jj][r]);
+            w[m][r][1] = dithered2(i8x2_hi(x), n[m][r][1], sc[jj][r]);
           } else {
-            w[m][r][0] = half2_sat(__hmul2(bits_h2(i8x2_lo(x)), s2));
-            w[m][r][1] = half2_sat(__hmul2(bits_h2(i8x2_hi(x)), s2));
+            w[m][r][0] = half2_sat(__hmul2(bits_h2(i8x2_lo(x)), sc[jj][r]));
+            w[m][r][1] = half2_sat(__hmul2(bits_h2(i8x2_hi(x)), sc[jj][r]));
           }
         }
       }
@@ -111,7 +160,7 @@ template <> struct KeyCodes<kKivi> {
       zr[jj] = *reinterpret_cast<const uint4*>(kp + 256 + 16 * jj);
     }
   }
-  __device__ __forceinline__ void words(const StoreArgs&, int, int, int, int jj, int, uint32_t (&w)[2][2][2]) const {
+  __device__ __forceinline__ void words(int jj, const uint32_t (&)[2][2][2], uint32_t (&w)[2][2][2]) const {
     const uint32_t x = jj ? c.y : c.x;
 #pragma unroll
     for (int m = 0; m < 2; ++m)
@@ -124,13 +173,11 @@ template <> struct KeyCodes<kKivi> {
   }
 };
 
-constexpr int kXwPitch = 40;                       // words per token pair: a lane's picks fall on distinct banks
-constexpr int kXwWords = 8 * kXwPitch;             // scratch of one warp (dithered store only)
-
 // The same for values: w[m][r][p] = tokens 2t + 8p, 2t + 8p + 1 of channel 32j + 16m + 8r + g.
 template <int SCH> struct ValueCodes {
-  uint4 c[SCH == kBbox ? 4 : 2];
-  uint2 sc[2];                           // INT8: the step's scales of the lane's four tokens
+  static constexpr int S = kSteps<SCH>;
+  uint4 c[SCH == kBbox ? 4 : S];
+  uint2 sc[S];                           // INT8: the step's scales of the lane's four tokens
   __device__ __forceinline__ void load(const uint8_t* bp, int j0, int lane) {
     if constexpr (SCH == kBbox) {
 #pragma unroll
@@ -138,28 +185,13 @@ template <int SCH> struct ValueCodes {
     } else {
       static_assert(Int8Layout::VC == Fp8Layout::VC, "one place for the codes");
 #pragma unroll
-      for (int jj = 0; jj < 2; ++jj) {
+      for (int jj = 0; jj < S; ++jj) {
         c[jj] = *reinterpret_cast<const uint4*>(bp + Int8Layout::VC + (j0 + jj) * 512 + lane * 16);
         if constexpr (int8_layout(SCH)) sc[jj] = *reinterpret_cast<const uint2*>(bp + Int8Layout::VS + ((j0 + jj) * 16 + 4 * (lane & 3)) * 2);
       }
     }
   }
-  __device__ __forceinline__ void words(const StoreArgs& s, int h, int tb, int j0, int jj, int lane, uint32_t* xs,
-                                        uint32_t (&w)[2][2][2]) const {
-    const int g = lane >> 2, t = lane & 3;
-    if constexpr (SCH == kInt8) {
-      // the step's 16 tokens x 32 channels of -xi as token pairs: a lane forms two tokens of a channel
-      // quad at a time, and picks out its own channels' pairs
-      __syncwarp();
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int pr = 4 * k + (lane >> 3), q = lane & 7;    // tokens 2 pr, 2 pr + 1
-        const uint4 u = dither_words(s, h, tb + 2 * pr, 8 * (j0 + jj) + q, 1), v = dither_words(s, h, tb + 2 * pr + 1, 8 * (j0 + jj) + q, 1);
-        *reinterpret_cast<uint4*>(xs + pr * kXwPitch + 4 * q) =
-            make_uint4(neg_xi2(u.x, v.x), neg_xi2(u.y, v.y), neg_xi2(u.z, v.z), neg_xi2(u.w, v.w));
-      }
-      __syncwarp();
-    }
+  __device__ __forceinline__ void words(int jj, const uint32_t (&n)[2][2][2], uint32_t (&w)[2][2][2]) const {
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -174,9 +206,8 @@ template <int SCH> struct ValueCodes {
           const uint32_t x = word_of(c[jj], 2 * m + r);
           const __half2 lo = bits_h2(sc[jj].x), hi = bits_h2(sc[jj].y);
           if constexpr (SCH == kInt8) {
-            const uint32_t* nx = xs + t * kXwPitch + 16 * m + 8 * r + g;
-            w[m][r][0] = dithered2(i8x2_lo(x), nx[0], lo);
-            w[m][r][1] = dithered2(i8x2_hi(x), nx[4 * kXwPitch], hi);
+            w[m][r][0] = dithered2(i8x2_lo(x), n[m][r][0], lo);
+            w[m][r][1] = dithered2(i8x2_hi(x), n[m][r][1], hi);
           } else {
             w[m][r][0] = half2_sat(__hmul2(bits_h2(i8x2_lo(x)), lo));
             w[m][r][1] = half2_sat(__hmul2(bits_h2(i8x2_hi(x)), hi));
@@ -193,7 +224,7 @@ template <> struct ValueCodes<kKivi> {
     for (int e = 0; e < 4; ++e)
       sz[e] = *reinterpret_cast<const uint2*>(bp + KiviLayout::VP + ((2 * (lane & 3) + (e & 1) + 8 * (e >> 1)) * 4 + j0) * 4);
   }
-  __device__ __forceinline__ void words(const StoreArgs&, int, int, int, int jj, int, uint32_t*, uint32_t (&w)[2][2][2]) const {
+  __device__ __forceinline__ void words(int jj, const uint32_t (&)[2][2][2], uint32_t (&w)[2][2][2]) const {
     const uint32_t x = jj ? c.y : c.x;
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
@@ -227,23 +258,29 @@ __device__ __forceinline__ void find_exact(const StoreArgs& s, int i, BlockPair&
   }
 }
 // Steps j0 and j0 + 1 (j0 = 0 or 2: one panel of the key image) of the two blocks into the key image,
-// or the value image.  got() is called when the codes are in registers.  Everything is decoded before
-// anything is stored: loads do not pass stores that might alias them.  (The dithered store, bound by
-// its integer work, takes the steps one by one.)
+// or the value image.  got() is called when the last codes are in registers.  What is decoded together
+// is decoded before any of it is stored: loads do not pass stores that might alias them.
 template <int SCH, typename F>
 __device__ __forceinline__ void expand_keys(const StoreArgs& s, const BlockPair& x, int j0, uint8_t* img, F got) {
-  constexpr int kSteps = SCH == kInt8 ? 1 : 2;
+  constexpr int S = kSteps<SCH>;
   const int g = x.lane >> 2, t = x.lane & 3;
   const bool tail = x.tb + 2 * kBlk > x.len;
-  KeyCodes<SCH> codes[2];
+#pragma unroll 1
+  for (int ja = 0; ja < 2; ja += S) {
+    uint32_t n[2][2][2][2], w[S][2][2][2][2];                // [b][m][r][p]; [jj][b][m][r][p]
+    if constexpr (SCH == kInt8) {
 #pragma unroll
-  for (int b = 0; b < 2; ++b) codes[b].load(x.bp[b], j0, x.lane);
-  got();
+      for (int b = 0; b < 2; ++b) {
+        if (s.dither) load_dither(s.dither, dither_at(s.Hkv, x.tb / kTileTok, x.h, 0, x.pr, j0 + ja, b, x.lane), n[b]);
+        else key_dither(s, x.h, s.pos0 + x.tb + b * kBlk, j0 + ja, x.lane, n[b]);
+      }
+    }
+    KeyCodes<SCH> codes[2];
 #pragma unroll
-  for (int ja = 0; ja < 2; ja += kSteps) {
-    uint32_t w[kSteps][2][2][2][2];                          // [jj][b][m][r][p]
+    for (int b = 0; b < 2; ++b) codes[b].load(x.bp[b], j0 + ja, x.lane);
+    if (ja + S == 2) got();
 #pragma unroll
-    for (int jj = 0; jj < kSteps; ++jj)
+    for (int jj = 0; jj < S; ++jj)
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
         if (x.exact[b]) {
@@ -256,11 +293,11 @@ __device__ __forceinline__ void expand_keys(const StoreArgs& s, const BlockPair&
 #pragma unroll
               for (int p = 0; p < 2; ++p) w[jj][b][m][r][p] = operand2<SCH>(v[m][r][2 * p], v[m][r][2 * p + 1]);
         } else {
-          codes[b].words(s, x.h, s.pos0 + x.tb + b * kBlk, j0, ja + jj, x.lane, w[jj][b]);
+          codes[b].words(jj, n[b], w[jj][b]);
         }
       }
 #pragma unroll
-    for (int jj = 0; jj < kSteps; ++jj)
+    for (int jj = 0; jj < S; ++jj)
 #pragma unroll
       for (int b = 0; b < 2; ++b)
 #pragma unroll
@@ -274,21 +311,28 @@ __device__ __forceinline__ void expand_keys(const StoreArgs& s, const BlockPair&
 }
 template <int SCH, typename F>
 __device__ __forceinline__ void expand_values(const StoreArgs& s, const BlockPair& x, int j0, uint32_t* xs, uint8_t* img, F got) {
-  constexpr int kSteps = SCH == kInt8 ? 1 : 2;
+  constexpr int S = kSteps<SCH>;
   const int g = x.lane >> 2, t = x.lane & 3;
   const bool tail = x.tb + 2 * kBlk > x.len;
-  ValueCodes<SCH> codes[2];
-#pragma unroll
-  for (int b = 0; b < 2; ++b) codes[b].load(x.bp[b], j0, x.lane);
-  got();
-#pragma unroll
-  for (int ja = 0; ja < 2; ja += kSteps) {
-    uint32_t w[kSteps][2][2][2][2];                          // [jj][b][m][r][p]
-#pragma unroll
-    for (int jj = 0; jj < kSteps; ++jj)
+#pragma unroll 1
+  for (int ja = 0; ja < 2; ja += S) {
+    uint32_t n[2][2][2][2], w[S][2][2][2][2];                // [b][m][r][p]; [jj][b][m][r][p]
+    if constexpr (SCH == kInt8) {
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
-        codes[b].words(s, x.h, s.pos0 + x.tb + b * kBlk, j0, ja + jj, x.lane, xs, w[jj][b]);
+        if (s.dither) load_dither(s.dither, dither_at(s.Hkv, x.tb / kTileTok, x.h, 1, x.pr, j0 + ja, b, x.lane), n[b]);
+        else value_dither(s, x.h, s.pos0 + x.tb + b * kBlk, j0 + ja, x.lane, xs, n[b]);
+      }
+    }
+    ValueCodes<SCH> codes[2];
+#pragma unroll
+    for (int b = 0; b < 2; ++b) codes[b].load(x.bp[b], j0 + ja, x.lane);
+    if (ja + S == 2) got();
+#pragma unroll
+    for (int jj = 0; jj < S; ++jj)
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        codes[b].words(jj, n[b], w[jj][b]);
         if (tail) {
 #pragma unroll
           for (int p = 0; p < 2; ++p) {
@@ -302,7 +346,7 @@ __device__ __forceinline__ void expand_values(const StoreArgs& s, const BlockPai
         }
       }
 #pragma unroll
-    for (int jj = 0; jj < kSteps; ++jj)
+    for (int jj = 0; jj < S; ++jj)
 #pragma unroll
       for (int m = 0; m < 2; ++m)
 #pragma unroll

@@ -178,6 +178,7 @@ struct StoreArgs {
   const void* pool;
   const float* kivi_tail;    // layer base (KIVI)
   uint32_t rk0[10], rk1[10]; // Philox round keys of the dither
+  const uint4* dither;       // the dither of tiles 0, 1, ... of every head formed beforehand (expand.cuh), or null
 };
 // Sequences of one read launch, passed by value: tokens t0[k] .. t0[k] + n[k] - 1 of sequence
 // seq[k] (len[k] tokens long) go to output rows row0[k], ...; blk_off counts their blocks.
@@ -219,6 +220,8 @@ struct AttendArgs {
   int unit_off[kAttendSeqs + 1];       // units before sequence k
   AttendStart start[kAttendCtas + 1];
 };
+constexpr size_t kDitherTile = 2 * kTileTok * 128 * 2;   // bytes of a tile and head's dither
+cudaError_t launch_dither_table(const StoreArgs& s, uint4* table, int tiles, cudaStream_t st);
 cudaError_t launch_expand(int scheme, const AttendArgs& a, cudaStream_t st);
 cudaError_t launch_attend(int scheme, const AttendArgs& a, cudaStream_t st);
 cudaError_t launch_attend_merge(const AttendArgs& a, cudaStream_t st);

@@ -791,12 +791,32 @@ static void share_units(AttendArgs& a, int sm_count) {
 // row tile of 128 reading the codes itself; longer ones share operand images.
 constexpr int kFewRows = kTileRows;
 
-// Groups of an attend call; bytes of the images and of the records the largest of them needs.
-static void plan_attend(const witcert_cache* c, int layer, const int32_t* n_tok, std::vector<AttendArgs>& groups,
-                        size_t& image_bytes, size_t& rec_bytes) {
+// What an attend call launches, and the parts of its workspace: the images and the records of the
+// largest group, and the dithered store's dither.
+struct AttendPlan {
+  std::vector<AttendArgs> groups;
+  size_t image_bytes = 0, rec_bytes = 0, dither_bytes = 0;
+  int dither_tiles = 0;
+  size_t bytes() const { return image_bytes + rec_bytes + dither_bytes; }
+};
+// Sequences that share a dither have it formed once when together they read it at least twice
+// (forming it takes a tile's expansion some 4000 cycles of integer work, fetching it 64 KB).
+constexpr int kDitherShare = 2;
+
+static void plan_attend(const witcert_cache* c, int layer, const int32_t* n_tok, AttendPlan& plan) {
+  std::vector<AttendArgs>& groups = plan.groups;
+  size_t &image_bytes = plan.image_bytes, &rec_bytes = plan.rec_bytes;
   const int B = c->cfg.batch, Hkv = c->cfg.n_kv_heads, grp = c->cfg.n_q_heads / Hkv;
   const size_t tile = (size_t)Hkv * 2 * kTileBytes;
-  image_bytes = rec_bytes = 0;
+  long long read_tiles = 0;
+  for (int i = 0; i < B && c->scheme == kInt8; ++i)
+    if (n_tok[i] > 0) {
+      const int tiles = (c->slen[layer][i] + kTileTok - 1) / kTileTok;
+      read_tiles += tiles;
+      plan.dither_tiles = std::max(plan.dither_tiles, tiles);
+    }
+  if (read_tiles < (long long)kDitherShare * plan.dither_tiles) plan.dither_tiles = 0;
+  plan.dither_bytes = plan.dither_tiles * Hkv * kDitherTile;
   for (const int unit_rows : {kTinyRows, kTileRows, 2 * kTileRows}) {
     const bool few = unit_rows <= kTileRows;
     bool open = false;
@@ -868,10 +888,9 @@ witcert_status witcert_attend_workspace(const witcert_cache* c, int layer, const
   long long rows = 0;
   if (witcert_status s = check_attend(c, layer, n_tok, rows)) return s;
   if (!bytes) return fail(WITCERT_EINVAL, "bytes must not be NULL");
-  std::vector<AttendArgs> groups;
-  size_t image = 0, rec = 0;
-  plan_attend(c, layer, n_tok, groups, image, rec);
-  *bytes = image + rec;
+  AttendPlan plan;
+  plan_attend(c, layer, n_tok, plan);
+  *bytes = plan.bytes();
   ok();
   return WITCERT_OK;
 }
@@ -884,17 +903,23 @@ witcert_status witcert_attend(witcert_cache* c, int layer, const void* q, const 
   if (!q || !out) return fail(WITCERT_EINVAL, "q and out must not be NULL");
   if (((uintptr_t)q | (uintptr_t)out | (uintptr_t)workspace) % 16)
     return fail(WITCERT_EINVAL, "q, out and workspace must be 16-byte aligned");
-  std::vector<AttendArgs> groups;
-  size_t image = 0, rec = 0;
-  plan_attend(c, layer, n_tok, groups, image, rec);
-  if (image + rec > workspace_bytes || !workspace)
-    return fail(WITCERT_EINVAL, "the workspace needs %zu bytes, got %zu", image + rec, workspace ? workspace_bytes : 0);
+  AttendPlan plan;
+  plan_attend(c, layer, n_tok, plan);
+  if (plan.bytes() > workspace_bytes || !workspace)
+    return fail(WITCERT_EINVAL, "the workspace needs %zu bytes, got %zu", plan.bytes(), workspace ? workspace_bytes : 0);
   auto st = static_cast<cudaStream_t>(stream);
   order_after_gate(c, layer, st);
-  for (AttendArgs& a : groups) {
+  uint8_t* images = static_cast<uint8_t*>(workspace);
+  uint4* dither = plan.dither_tiles ? reinterpret_cast<uint4*>(images + plan.image_bytes + plan.rec_bytes) : nullptr;
+  if (dither) {
+    cudaError_t e = launch_dither_table(store_args(c, layer), dither, plan.dither_tiles, st);
+    if (e != cudaSuccess) return cuda_fail(e, "dither launch");
+  }
+  for (AttendArgs& a : plan.groups) {
     a.q = q; a.out = out;
-    a.images = static_cast<uint8_t*>(workspace);
-    a.rec = reinterpret_cast<float*>(a.images + image);
+    a.images = images;
+    a.rec = reinterpret_cast<float*>(images + plan.image_bytes);
+    a.s.dither = dither;
     cudaError_t e = attend_group(c->scheme, a, st);
     if (e != cudaSuccess) return cuda_fail(e, "attend launch");
   }
