@@ -54,6 +54,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
   if (warp == 2) tmem_alloc<512>(slot);
+  pdl_wait();                                              // the images
+  if (a.cut) pdl_trigger();                                // a call's last kernel lets nothing start early
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -195,60 +197,84 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
 
 // Records of the units that cross CTAs joined: out = sum 2^(m - M) O / sum 2^(m - M) l.  Block row
 // blockIdx.y takes the unit that CTA c = blockIdx.y starts without finishing (its slot 2c + 1, then
-// the slots 2c' of the CTAs that go on); one warp a row.  Lane p holds part p's m and l, so the loads
-// of a row's parts do not wait for one another.
+// the slots 2c' of the CTAs that go on).  Bound by latency: a warp joins R rows of two parts at once,
+// all their loads in flight together (units of 256 rows mostly have two parts: 35 us with one row a
+// warp), or, where units have few rows and many parts, the block's eight warps share a row's parts
+// (R = 0).
+template <int R>
 __global__ void __launch_bounds__(256) attend_merge_kernel(const __grid_constant__ AttendArgs a) {
-  const int c0 = blockIdx.y, lane = threadIdx.x & 31;
-  const AttendStart next = a.start[c0 + 1];
+  pdl_wait();
+  const int c0 = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const AttendStart here = a.start[c0], next = a.start[c0 + 1];
   if (next.j == 0) return;                                 // the CTA ends on a unit's end
-  if (a.start[c0].unit == next.unit && a.start[c0].j > 0) return;   // a part in the middle
+  if (same_unit(here, next) && here.j > 0) return;         // a part in the middle
   Segment u;
-  unit_place(a, next.unit, u);
-  const int row = u.r0 + blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (row >= u.rows || row >= u.r0 + a.unit_rows) return;
-  const float* first = a.rec + ((size_t)2 * c0 * a.unit_rows + (row - u.r0)) * kRecStride;
-  const size_t step = (size_t)2 * a.unit_rows * kRecStride;          // to the next CTA's slot
-  auto part = [&](int p) { return first + p * step + (p == 0 ? step / 2 : 0); };
-  float top = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int p0 = 0; ; p0 += 32) {
-    const int c = c0 + p0 + lane;
-    const bool mine = c < a.n_ctas && (c == c0 || (a.start[c].unit == next.unit && a.start[c].j > 0));
-    const int n = __popc(__ballot_sync(0xffffffffu, mine));          // parts of a unit are consecutive CTAs'
-    const float2 ml = mine ? *reinterpret_cast<const float2*>(part(p0 + lane)) : make_float2(-INFINITY, 0.f);
-    float t = ml.x;
-#pragma unroll
-    for (int x = 16; x; x >>= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, x));
-    t = fmaxf(t, top);
-    const float keep = top == t ? 1.0f : ex2(top - t);               // of what is joined so far
-    const float f = t == -INFINITY ? 0.f : ex2(ml.x - t);            // a part may see no key
-    top = t;
-    l *= keep;
-#pragma unroll
-    for (int x = 0; x < 4; ++x) o[x] *= keep;
-    float s = mine ? f * ml.y : 0.f;
-#pragma unroll
-    for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-    l += s;
-#pragma unroll 8
-    for (int p = 0; p < n; ++p) {
-      const float4 v = *reinterpret_cast<const float4*>(part(p0 + p) + 4 + 4 * lane);
-      const float w = __shfl_sync(0xffffffffu, f, p);
-      o[0] = fmaf(w, v.x, o[0]); o[1] = fmaf(w, v.y, o[1]); o[2] = fmaf(w, v.z, o[2]); o[3] = fmaf(w, v.w, o[3]);
+  int row_tiles;
+  unit_place(a, next, u, row_tiles);
+  const int r0 = blockIdx.x * (R ? 8 * R : 1) + (R ? warp * R : 0);          // of the unit
+  if (u.r0 + r0 >= u.rows) return;
+  int n = 2;                                               // parts: consecutive CTAs', two at least
+  while (c0 + n < a.n_ctas && same_unit(a.start[c0 + n], next)) ++n;
+  const size_t step = (size_t)2 * a.unit_rows * kRecStride;                  // to the next CTA's slot
+  auto part = [&](int r, int p) {
+    return a.rec + ((size_t)2 * c0 * a.unit_rows + r0 + r) * kRecStride + p * step + (p == 0 ? step / 2 : 0);
+  };
+  struct Sum {
+    float m, l;
+    float4 o;
+    __device__ __forceinline__ void join(float2 ml, float4 v) {
+      const float t = fmaxf(m, ml.x), f = t == -INFINITY ? 0.f : ex2(m - t), g = t == -INFINITY ? 0.f : ex2(ml.x - t);
+      l = f * l + g * ml.y;
+      o.x = f * o.x + g * v.x; o.y = f * o.y + g * v.y; o.z = f * o.z + g * v.z; o.w = f * o.w + g * v.w;
+      m = t;
     }
-    if (n < 32) break;
+  };
+  auto ml = [&](int r, int p) { return *reinterpret_cast<const float2*>(part(r, p)); };
+  auto sums = [&](int r, int p) { return *reinterpret_cast<const float4*>(part(r, p) + 8 + 4 * lane); };
+  auto store = [&](int r, const Sum& x) {
+    const int row = u.r0 + r0 + r;
+    const float inv = 1.0f / x.l;
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) +
+                              ((size_t)(a.row0[u.k] + row / a.grp) * a.Hq + u.h * a.grp + row % a.grp) * kD + 4 * lane) =
+        make_uint2(pack2<true>(x.o.x * inv, x.o.y * inv), pack2<true>(x.o.z * inv, x.o.w * inv));
+  };
+  if constexpr (R > 0) {
+    const int rows = min(R, u.rows - u.r0 - r0);
+    float2 m[R][2];
+    float4 v[R][2];
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int p = 0; p < 2; ++p)
+        if (r < rows) { m[r][p] = ml(r, p); v[r][p] = sums(r, p); }
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      if (r < rows) {
+        Sum x{m[r][0].x, m[r][0].y, v[r][0]};
+        x.join(m[r][1], v[r][1]);
+        for (int p = 2; p < n; ++p) x.join(ml(r, p), sums(r, p));
+        store(r, x);
+      }
+  } else {
+    __shared__ float sm[8][kRecStride];
+    Sum x{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+#pragma unroll 4
+    for (int p = warp; p < n; p += 8) x.join(ml(0, p), sums(0, p));
+    if (lane == 0) { sm[warp][0] = x.m; sm[warp][1] = x.l; }
+    *reinterpret_cast<float4*>(&sm[warp][8 + 4 * lane]) = x.o;
+    __syncthreads();
+    if (warp) return;
+    for (int w = 1; w < 8; ++w)
+      x.join(make_float2(sm[w][0], sm[w][1]), *reinterpret_cast<const float4*>(&sm[w][8 + 4 * lane]));
+    store(0, x);
   }
-  const float inv = 1.0f / l;
-  *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) +
-                            ((size_t)(a.row0[u.k] + row / a.grp) * a.Hq + u.h * a.grp + row % a.grp) * kD + 4 * lane) =
-      make_uint2(pack2<true>(o[0] * inv, o[1] * inv), pack2<true>(o[2] * inv, o[3] * inv));
 }
 
 template <bool BF16>
 cudaError_t launch_t(const AttendArgs& a, cudaStream_t st) {
   cudaError_t e = cudaFuncSetAttribute(attend_kernel<BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (e != cudaSuccess) return e;
-  attend_kernel<BF16><<<(unsigned)a.n_ctas, kThreads, kSmemBytes, st>>>(a);
-  return cudaGetLastError();
+  return launch_after(attend_kernel<BF16>, dim3((unsigned)a.n_ctas), kThreads, kSmemBytes, st, a);
 }
 
 }  // namespace
@@ -258,11 +284,10 @@ cudaError_t launch_attend(int scheme, const AttendArgs& a, cudaStream_t st) {
 }
 
 cudaError_t launch_attend_merge(const AttendArgs& a, cudaStream_t st) {
-  bool any = false;
-  for (int c = 1; c < a.n_ctas; ++c) any |= a.start[c].j > 0;
-  if (!any) return cudaSuccess;
-  attend_merge_kernel<<<dim3((unsigned)(a.unit_rows / 8), (unsigned)(a.n_ctas - 1)), 256, 0, st>>>(a);
-  return cudaGetLastError();
+  if (!a.cut) return cudaSuccess;
+  const unsigned cuts = (unsigned)(a.n_ctas - 1);
+  return a.unit_rows > kTinyRows ? launch_after(attend_merge_kernel<4>, dim3((unsigned)(a.unit_rows / 32), cuts), 256, 0, st, a)
+                                 : launch_after(attend_merge_kernel<0>, dim3((unsigned)a.unit_rows, cuts), 256, 0, st, a);
 }
 
 }  // namespace witcert

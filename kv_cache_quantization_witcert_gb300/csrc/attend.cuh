@@ -19,6 +19,23 @@ namespace witcert {
 constexpr float kOff = 8.0f, kGrow = 7.0f;
 constexpr uint64_t kAttendWaitNs = 2000000000ull;          // 2 s per barrier wait
 
+// A kernel of a call behind the call's earlier ones: it may start while its predecessor ends, and
+// waits for it (pdl_wait) before it reads anything.
+template <typename K>
+cudaError_t launch_after(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t st, const AttendArgs& a) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = a.after ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
 // One stretch of key tiles of one unit.
 struct Segment {
   int k, h, r0, rows;        // sequence, KV head, first query row of the unit, rows of the sequence
@@ -26,38 +43,41 @@ struct Segment {
   bool whole;                // all of the unit's key tiles: the output is final
   int slot;                  // otherwise: where its records go
 };
-// Rows of unit u and its key tiles.
-__device__ __forceinline__ int unit_place(const AttendArgs& a, int u, Segment& x) {
-  int lo = 0, hi = a.n_seq - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (a.unit_off[mid] <= u) lo = mid; else hi = mid - 1;
-  }
-  u -= a.unit_off[lo];
-  x.k = lo;
-  x.rows = a.n[lo] * a.grp;
-  const int tiles = (x.rows + a.unit_rows - 1) / a.unit_rows;
-  x.h = u % a.s.Hkv;
-  x.r0 = (tiles - 1 - u / a.s.Hkv) * a.unit_rows;          // last rows, which see most keys, first
+__device__ __forceinline__ bool same_unit(const AttendStart& a, const AttendStart& b) {
+  return a.k == b.k && a.tile == b.tile && a.h == b.h;
+}
+// Rows of a unit and its key tiles; row_tiles: the sequence's units a head.
+__device__ __forceinline__ int unit_place(const AttendArgs& a, const AttendStart& at, Segment& x, int& row_tiles) {
+  const int n = a.n[at.k], len = a.len[at.k];
+  x.k = at.k;
+  x.h = at.h;
+  x.rows = n * a.grp;
+  row_tiles = (x.rows + a.unit_rows - 1) / a.unit_rows;
+  x.r0 = (row_tiles - 1 - at.tile) * a.unit_rows;          // last rows, which see most keys, first
   const int last = min(x.rows, x.r0 + a.unit_rows) - 1;
-  return (a.len[lo] - a.n[lo] + last / a.grp) / kTileTok + 1;
+  return (len - n + last / a.grp) / kTileTok + 1;
 }
 // The segments of CTA c in order: f(segment) until it returns false.
 template <typename F>
 __device__ __forceinline__ void walk(const AttendArgs& a, int c, F f) {
   AttendStart at = a.start[c];
   const AttendStart end = a.start[c + 1];
-  while (at.unit < end.unit || (at.unit == end.unit && at.j < end.j)) {
+  while (!(same_unit(at, end) && at.j >= end.j)) {
     Segment x;
-    const int nt = unit_place(a, at.unit, x);
-    const int to = at.unit == end.unit ? end.j : nt;
+    int row_tiles;
+    const int nt = unit_place(a, at, x, row_tiles);
+    const int to = same_unit(at, end) ? end.j : nt;
     x.j0 = at.j;
     x.nk = to - at.j;
     x.whole = at.j == 0 && to == nt;
     x.slot = 2 * c + (at.j == 0 ? 1 : 0);
     if (!f(x)) return;
-    at.unit += to == nt;
-    at.j = to == nt ? 0 : to;
+    if (to < nt) return;                                   // the CTA ends inside this unit
+    at.j = 0;
+    if (++at.h == a.s.Hkv) {
+      at.h = 0;
+      if (++at.tile == row_tiles) { at.tile = 0; ++at.k; }
+    }
   }
 }
 
@@ -126,6 +146,17 @@ struct RowGroup {
   __device__ __forceinline__ float sum(float v) { return all(v, [](float a, float b) { return a + b; }); }
 };
 
+// 32 bytes a thread: a whole sector, where a warp's threads each have a row of their own.
+__device__ __forceinline__ void load32(const void* p, uint4& a, uint4& b) {
+  asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
+               : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w) : "l"(p));
+}
+__device__ __forceinline__ void store32(void* p, const uint32_t (&v)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]),
+               "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
 // This thread's 128 / N channels of query row `row` of a segment as operand words in the key images'
 // channel order; zero for rows past the sequence's.  Returns log2(e)/sqrt(d) times the power of two
 // that the row was divided by: fp16 rows are scaled to a largest element in [1, 2).
@@ -140,7 +171,7 @@ __device__ __forceinline__ float query_words(const AttendArgs& a, const Segment&
         static_cast<const __nv_bfloat16*>(a.q) +
         ((size_t)(a.row0[u.k] + row / a.grp) * a.Hq + u.h * a.grp + row % a.grp) * kD + (128 / N) * grp.part);
 #pragma unroll
-    for (int c = 0; c < 16 / N; ++c) v[c] = src[c];
+    for (int c = 0; c < 16 / N; c += 2) load32(src + c, v[c], v[c + 1]);
   }
   // 16-byte piece 4 jj + t: channels 32 jj + 4t .. + 3 and 32 jj + 16 + 4t .. + 3
 #pragma unroll
@@ -308,7 +339,7 @@ __device__ __forceinline__ void store_row(const AttendArgs& a, const Segment& u,
   } else {
     rec = a.rec + ((size_t)u.slot * a.unit_rows + (row - u.r0)) * kRecStride;
     if (store && part == 0) *reinterpret_cast<float2*>(rec) = make_float2(m == -INFINITY ? m : m * scale, l);
-    rec += 4 + kCols * part;
+    rec += 8 + kCols * part;
   }
   const float inv = 1.0f / l;                              // a whole unit's row sees at least one key
 #pragma unroll 1
@@ -319,17 +350,16 @@ __device__ __forceinline__ void store_row(const AttendArgs& a, const Segment& u,
     float x[16];                                           // by channel
 #pragma unroll
     for (int e = 0; e < 16; ++e) x[e] = __uint_as_float(o[(e & 8) + 4 * (e & 1) + ((e & 7) >> 1)]);
+    uint32_t b[2][8];
     if (store && !u.whole) {
 #pragma unroll
-      for (int e = 0; e < 16; e += 4) *reinterpret_cast<float4*>(rec + c + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+      for (int e = 0; e < 16; ++e) b[e >> 3][e & 7] = __float_as_uint(x[e]);
+      store32(rec + c, b[0]);
+      store32(rec + c + 8, b[1]);
     } else if (store) {
 #pragma unroll
-      for (int e = 0; e < 16; e += 8) {
-        uint32_t b[4];
-#pragma unroll
-        for (int y = 0; y < 4; ++y) b[y] = pack2<true>(x[e + 2 * y] * inv, x[e + 2 * y + 1] * inv);
-        *reinterpret_cast<uint4*>(out + c + e) = make_uint4(b[0], b[1], b[2], b[3]);
-      }
+      for (int e = 0; e < 8; ++e) b[0][e] = pack2<true>(x[2 * e] * inv, x[2 * e + 1] * inv);
+      store32(out + c, b[0]);
     }
     __syncwarp();
   }

@@ -81,6 +81,8 @@ __global__ void __launch_bounds__(FewSmem<SCH, TINY>::kThreads, 1) attend_few_ke
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
   if (warp == 2) tmem_alloc<512>(slot);
+  pdl_wait();                                              // the dither, or whatever came before the call
+  if (a.cut) pdl_trigger();                                // a call's last kernel lets nothing start early
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -275,8 +277,7 @@ cudaError_t launch_few(const AttendArgs& a, cudaStream_t st) {
   using L = FewSmem<SCH, TINY>;
   cudaError_t e = cudaFuncSetAttribute(attend_few_kernel<SCH, TINY>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
   if (e != cudaSuccess) return e;
-  attend_few_kernel<SCH, TINY><<<(unsigned)a.n_ctas, L::kThreads, L::kBytes, st>>>(a);
-  return cudaGetLastError();
+  return launch_after(attend_few_kernel<SCH, TINY>, dim3((unsigned)a.n_ctas), L::kThreads, L::kBytes, st, a);
 }
 
 template <int SCH>

@@ -4,6 +4,7 @@
 // A CTA per (128-token tile, KV head), a warp per two blocks and half of the channels.  Bound by HBM
 // (codes in, 64 KB a tile and head out) and, for the dithered store, by the integer work of its
 // dither.
+#include "attend.cuh"
 #include "expand.cuh"
 
 namespace witcert {
@@ -13,6 +14,8 @@ namespace {
 template <int SCH>
 __global__ void __launch_bounds__(256) expand_kernel(const __grid_constant__ AttendArgs a) {
   __shared__ __align__(16) uint32_t scratch[SCH == kInt8 ? 8 : 1][SCH == kInt8 ? kXwWords : 1];
+  pdl_wait();
+  pdl_trigger();
   const int warp = threadIdx.x >> 5;
   const int tile_all = blockIdx.x / a.s.Hkv;
   int k = 0;
@@ -38,6 +41,7 @@ __global__ void __launch_bounds__(256) expand_kernel(const __grid_constant__ Att
 // The dither of a tile and head in the order the expanding lanes fetch it.
 __global__ void __launch_bounds__(256) dither_kernel(const __grid_constant__ StoreArgs s, uint4* table) {
   __shared__ __align__(16) uint32_t scratch[8][kXwWords];
+  pdl_trigger();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int h = blockIdx.x % s.Hkv, tile = blockIdx.x / s.Hkv, pr = warp >> 1, j0 = 2 * (warp & 1);
 #pragma unroll 1
@@ -63,13 +67,12 @@ cudaError_t launch_expand(int scheme, const AttendArgs& a, cudaStream_t st) {
   const unsigned grid = (unsigned)(a.tile_off[a.n_seq] * a.s.Hkv);
   if (grid == 0) return cudaSuccess;
   switch (scheme) {
-    case kInt8: expand_kernel<kInt8><<<grid, 256, 0, st>>>(a); break;
-    case kRtn: expand_kernel<kRtn><<<grid, 256, 0, st>>>(a); break;
-    case kFp8: expand_kernel<kFp8><<<grid, 256, 0, st>>>(a); break;
-    case kKivi: expand_kernel<kKivi><<<grid, 256, 0, st>>>(a); break;
-    default: expand_kernel<kBbox><<<grid, 256, 0, st>>>(a); break;
+    case kInt8: return launch_after(expand_kernel<kInt8>, dim3(grid), 256, 0, st, a);
+    case kRtn: return launch_after(expand_kernel<kRtn>, dim3(grid), 256, 0, st, a);
+    case kFp8: return launch_after(expand_kernel<kFp8>, dim3(grid), 256, 0, st, a);
+    case kKivi: return launch_after(expand_kernel<kKivi>, dim3(grid), 256, 0, st, a);
+    default: return launch_after(expand_kernel<kBbox>, dim3(grid), 256, 0, st, a);
   }
-  return cudaGetLastError();
 }
 
 }  // namespace witcert

@@ -195,8 +195,8 @@ cudaError_t launch_read(int scheme, const ReadArgs& a, cudaStream_t st);
 // Chunk attention (attend.cuh).  Sequences of one launch, passed by value: the n[k] newest tokens
 // of sequence seq[k] (len[k] tokens long) are the queries, packed from token row row0[k] on.  A
 // query row of a KV head is (token, head of the group), token-major: rows_k = n grp.  A unit is a
-// row tile of one KV head; CTA c takes the key tiles from start[c] up to start[c + 1] in (unit, key
-// tile) order, so every CTA has the same number of them, and a unit that crosses CTAs leaves one
+// row tile of one KV head; CTA c takes the key tiles from start[c] up to start[c + 1] in (sequence,
+// row tile, head, key tile) order, so every CTA has the same number of them, and a unit that crosses CTAs leaves one
 // record per row and part.
 constexpr int kAttendSeqs = 64;
 constexpr int kAttendCtas = 192;
@@ -204,8 +204,8 @@ constexpr int kTileTok = 128;                    // tokens of a key / value tile
 constexpr int kTileBytes = kTileTok * 128 * 2;   // one operand image: 128 x 128 two-byte elements
 constexpr int kTileRows = 128;                   // query rows of one tensor-core tile
 constexpr int kTinyRows = 32;                    // units of sequences with so few rows (one tensor-memory quadrant)
-constexpr int kRecStride = 132;                  // split record: m (log2), l, two unused, 128 sums
-struct AttendStart { int unit, j; };
+constexpr int kRecStride = 136;                  // split record: m (log2), l, six unused, 128 sums
+struct alignas(16) AttendStart { int k, tile, h, j; };   // sequence, row tile (last rows first), KV head, key tile
 struct AttendArgs {
   StoreArgs s;
   const void* q;             // [rows][Hq][128] bf16
@@ -215,9 +215,10 @@ struct AttendArgs {
   int* err;                  // device error word (waits that ran out)
   int Hq, grp, n_seq, n_ctas, unit_rows;
   float scale_log2;          // log2(e) / sqrt(d)
+  int after;                 // behind another kernel of the same call
+  int cut;                   // some unit crosses CTAs: a merge follows
   int seq[kAttendSeqs], n[kAttendSeqs], len[kAttendSeqs], row0[kAttendSeqs];
   int tile_off[kAttendSeqs + 1];       // image tiles before sequence k
-  int unit_off[kAttendSeqs + 1];       // units before sequence k
   AttendStart start[kAttendCtas + 1];
 };
 constexpr size_t kDitherTile = 2 * kTileTok * 128 * 2;   // bytes of a tile and head's dither

@@ -752,39 +752,34 @@ static int attend_key_tiles(const AttendArgs& a, int k, int rt) {
 static void share_units(AttendArgs& a, int sm_count) {
   constexpr int kCutTiles = 6, kMinShare = 4;
   const int Hkv = a.s.Hkv, sms = std::min(sm_count, kAttendCtas);
-  long long total = 0;
-  int units = 0, most = 1;
-  for (int k = 0; k < a.n_seq; ++k) {
-    const int rts = attend_row_tiles(a, k);
-    a.unit_off[k] = units;
-    units += rts * Hkv;
-    for (int rt = 0; rt < rts; ++rt) {
-      const int nt = attend_key_tiles(a, k, rt);
-      total += (long long)nt * Hkv;
-      most = std::max(most, nt);
-    }
-  }
-  a.unit_off[a.n_seq] = units;
-  const int per_cta = (units + sms - 1) / sms;
-  const long long share = std::max<long long>((total + sms - 1) / sms, std::min(kMinShare, most));
-  if ((long long)per_cta * most <= share + kCutTiles) {      // whole units
-    a.n_ctas = (units + per_cta - 1) / per_cta;
-    for (int c = 0; c <= a.n_ctas; ++c) a.start[c] = {std::min(units, c * per_cta), 0};
-    return;
-  }
-  a.n_ctas = (int)((total + share - 1) / share);
-  int c = 0;
-  long long at = 0;                                          // tiles before the present row tile's units
+  long long total = 0, units = 0;
+  int most = 1;
   for (int k = 0; k < a.n_seq; ++k)
     for (int rt = 0, rts = attend_row_tiles(a, k); rt < rts; ++rt) {
       const int nt = attend_key_tiles(a, k, rt);
-      for (; c < a.n_ctas && c * share < at + (long long)nt * Hkv; ++c) {
-        const long long in = c * share - at;
-        a.start[c] = {a.unit_off[k] + rt * Hkv + (int)(in / nt), (int)(in % nt)};
-      }
-      at += (long long)nt * Hkv;
+      units += Hkv;
+      total += (long long)nt * Hkv;
+      most = std::max(most, nt);
     }
-  a.start[a.n_ctas] = {units, 0};
+  const long long per_cta = (units + sms - 1) / sms;
+  const long long even = std::max<long long>((total + sms - 1) / sms, std::min(kMinShare, most));
+  const bool whole = per_cta * most <= even + kCutTiles;
+  // CTA c starts at place c * share, counted in units or in key tiles
+  const long long share = whole ? per_cta : even;
+  a.n_ctas = (int)(((whole ? units : total) + share - 1) / share);
+  int c = 0;
+  long long at = 0;                                          // places before the present row tile's units
+  for (int k = 0; k < a.n_seq; ++k)
+    for (int rt = 0, rts = attend_row_tiles(a, k); rt < rts; ++rt) {
+      const int weight = whole ? 1 : attend_key_tiles(a, k, rt);
+      for (; c < a.n_ctas && c * share < at + (long long)weight * Hkv; ++c) {
+        const long long in = c * share - at;
+        a.start[c] = {k, rt, (int)(in / weight), whole ? 0 : (int)(in % weight)};
+        a.cut |= a.start[c].j > 0;
+      }
+      at += (long long)weight * Hkv;
+    }
+  a.start[a.n_ctas] = {a.n_seq, 0, 0, 0};
 }
 
 // Sequences of at most this many query rows a KV head are attended straight from the store, each
@@ -852,7 +847,9 @@ static void plan_attend(const witcert_cache* c, int layer, const int32_t* n_tok,
   }
 }
 
-static cudaError_t attend_group(int scheme, const AttendArgs& a, cudaStream_t st) {
+// The kernels of a call overlap their starts with their predecessors' ends; the first one (after = 0)
+// is launched like any other kernel.
+static cudaError_t attend_group(int scheme, AttendArgs& a, cudaStream_t st) {
   cudaError_t e;
   if (a.unit_rows <= kTileRows) {
     switch (scheme) {
@@ -864,8 +861,10 @@ static cudaError_t attend_group(int scheme, const AttendArgs& a, cudaStream_t st
     }
   } else {
     e = launch_expand(scheme, a, st);
+    a.after = 1;
     if (e == cudaSuccess) e = launch_attend(scheme, a, st);
   }
+  a.after = 1;
   return e == cudaSuccess ? launch_attend_merge(a, st) : e;
 }
 
@@ -920,6 +919,7 @@ witcert_status witcert_attend(witcert_cache* c, int layer, const void* q, const 
     a.images = images;
     a.rec = reinterpret_cast<float*>(images + plan.image_bytes);
     a.s.dither = dither;
+    a.after = dither || &a != plan.groups.data();
     cudaError_t e = attend_group(c->scheme, a, st);
     if (e != cudaSuccess) return cuda_fail(e, "attend launch");
   }
