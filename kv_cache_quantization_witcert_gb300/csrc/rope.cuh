@@ -17,8 +17,17 @@ __device__ __forceinline__ void rope_cs(uint64_t turn, int64_t pos, float gain, 
   const uint64_t near = phase + (1ull << 61);
   const int quarter = (int)(near >> 62);
   const float r = __fmul_rn((float)(int32_t)((phase - ((uint64_t)quarter << 62)) >> 32), 0x1p-31f);   // half turns
-  float sr, cr;
-  sincospif(r, &sr, &cr);
+  // Taylor series at pi r, |pi r| <= pi / 4: the first terms left out are below 2^-29 and 2^-33
+  const float t = __fmul_rn(r, 3.14159265358979f), q = __fmul_rn(t, t);
+  float sr = __fmaf_rn(q, 1.0f / 362880.0f, -1.0f / 5040.0f);
+  sr = __fmaf_rn(q, sr, 1.0f / 120.0f);
+  sr = __fmaf_rn(q, sr, -1.0f / 6.0f);
+  sr = __fmaf_rn(__fmul_rn(q, sr), t, t);
+  float cr = __fmaf_rn(q, -1.0f / 3628800.0f, 1.0f / 40320.0f);
+  cr = __fmaf_rn(q, cr, -1.0f / 720.0f);
+  cr = __fmaf_rn(q, cr, 1.0f / 24.0f);
+  cr = __fmaf_rn(q, cr, -0.5f);
+  cr = __fmaf_rn(q, cr, 1.0f);
   const float cs = quarter & 1 ? sr : cr, sn = quarter & 1 ? cr : sr;
   // quarter 0: (c, s), 1: (-s, c), 2: (-c, -s), 3: (s, -c)
   c = __fmul_rn(gain, quarter == 1 || quarter == 2 ? -cs : cs);

@@ -456,8 +456,8 @@ static witcert_status write_impl(witcert_cache* c, int layer, const void* K, con
       if (n[i] > 0) upd.emplace_back(layer * B + i, c->slen[layer][i] + n[i]);
     if ((e = push_lengths(c, upd, st, pdl)) != cudaSuccess) return cuda_fail(e, "sequence lengths");
     const WriteArgs all = layer_write_args(c, layer, K, V, Kh, Vh, 0, 0);
-    // long appends: the batched writers on that sequence alone; short ones: ragged launches
-    // of up to kRaggedPerLaunch sequences
+    // ragged launches of up to kRaggedPerLaunch sequences; with a backing store, bulk appends go
+    // sequence by sequence (their exact keys by the copy engines)
     RaggedArgs g{};
     auto flush = [&]() -> cudaError_t {
       if (g.n_seq == 0) return cudaSuccess;
@@ -476,18 +476,16 @@ static witcert_status write_impl(witcert_cache* c, int layer, const void* K, con
       if (n[i] == 0) continue;
       const int t0 = c->slen[layer][i];
       first_blk = t0 / kBlk < first_blk ? t0 / kBlk : first_blk;
-      if (n[i] >= kBlk) {
+      if (c->backing_host && n[i] >= kBulkBackingTokens && !rope) {
         WriteArgs a = seq_write_args(c, all, i, row, n[i], t0);
-        if (c->backing_host && n[i] >= kBulkBackingTokens && !rope) {
-          e = backing_copy(c, layer, K, i, row, n[i], t0, st);
-          if (e != cudaSuccess) {
-            c->backing_lost[layer] = 1;
-            return cuda_fail(e, "backing-store copy");
-          }
-          a.backing = nullptr;
-          pdl = false;
+        e = backing_copy(c, layer, K, i, row, n[i], t0, st);
+        if (e != cudaSuccess) {
+          c->backing_lost[layer] = 1;
+          return cuda_fail(e, "backing-store copy");
         }
-        e = rope ? launch_write_rope(c->scheme, a, rp, st, pdl) : launch_write(c->scheme, a, st, pdl);
+        a.backing = nullptr;
+        pdl = false;
+        e = launch_write(c->scheme, a, st, pdl);
       } else {
         g.seq[g.n_seq] = i;
         g.t0[g.n_seq] = t0;

@@ -80,11 +80,10 @@ struct LaneTurn {
   // from a table of (cos, sin) of all the pairs
   __device__ __forceinline__ void from(const RopeArgs& rp, const float2* tab, int lane) {
     const int p0 = 4 * lane >= rp.rot ? 0 : lane_pair(rp, lane);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float2 v = tab[rp.interleaved && e > 1 ? p0 : p0 + e];
-      c[e] = v.x; s[e] = v.y;
-    }
+    const float4 a = *reinterpret_cast<const float4*>(tab + p0);
+    const float4 b = *reinterpret_cast<const float4*>(tab + (rp.interleaved ? p0 : p0 + 2));
+    c[0] = a.x; s[0] = a.y; c[1] = a.z; s[1] = a.w;
+    c[2] = b.x; s[2] = b.y; c[3] = b.z; s[3] = b.w;
   }
 };
 template <typename T>
@@ -650,9 +649,45 @@ __global__ void __launch_bounds__(128) write_token_kernel(const WriteArgs a, con
 // With a rotation a CTA's warps take up to four KV heads of one block, so that they share the
 // (cos, sin) table of its sixteen positions: 64 x 16 pairs by 128 threads instead of by each warp.
 constexpr int kBlockWriterWarps = 4;
-template <typename T, int SCH, bool VW, typename RP>
+// AT says which blocks: UniformBlocks, nblocks blocks from blk0 on of every sequence, or RaggedBlocks.
+struct UniformBlocks {
+  int blk0, nblocks;
+  __host__ __device__ long long blocks(const WriteArgs& a) const { return (long long)a.B * nblocks; }
+  __device__ __forceinline__ bool unit(const WriteArgs& a, long long u, int& i, int& h, int& blk) const {
+    if (u >= (long long)a.B * a.Hkv * nblocks) return false;   // (i * Hkv + h) * nblocks + b
+    const int sh = (int)(u / nblocks);
+    i = sh / a.Hkv; h = sh % a.Hkv; blk = blk0 + (int)(u % nblocks);
+    return true;
+  }
+  __device__ __forceinline__ void place(const WriteArgs&, int ib, int& i, int& blk) const { i = ib / nblocks; blk = blk0 + ib % nblocks; }
+  __device__ __forceinline__ size_t row(const WriteArgs& a, int i, int t, int h) const { return uniform_row(a, i, t - a.t0, h); }
+};
+struct RaggedBlocks {
+  RaggedArgs g;              // off counts whole blocks; sequence k's first whole block is blk0[k]
+  int blk0[kRaggedPerLaunch];
+  __host__ __device__ long long blocks(const WriteArgs&) const { return g.off[g.n_seq]; }
+  __device__ __forceinline__ int find(int b) const {         // the k with off[k] <= b < off[k + 1]
+    int lo = 0, hi = g.n_seq - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (g.off[mid] <= b) lo = mid; else hi = mid - 1;
+    }
+    return lo;
+  }
+  __device__ __forceinline__ bool unit(const WriteArgs& a, long long u, int& k, int& h, int& blk) const {
+    if (u >= (long long)a.Hkv * g.off[g.n_seq]) return false;
+    h = (int)(u % a.Hkv);
+    place(a, (int)(u / a.Hkv), k, blk);
+    return true;
+  }
+  __device__ __forceinline__ void place(const WriteArgs&, int b, int& k, int& blk) const { k = find(b); blk = blk0[k] + b - g.off[k]; }
+  __device__ __forceinline__ size_t row(const WriteArgs& a, int k, int t, int h) const {
+    return ((size_t)(g.row0[k] + t - g.t0[k]) * a.Hkv + h) * kD;
+  }
+};
+template <typename T, int SCH, bool VW, typename RP, typename AT>
 __global__ void __launch_bounds__(kBlockWriterWarps * 32, SCH == kBbox || kRotates<RP> ? 6 : 8)
-write_block_kernel(const WriteArgs a, const __grid_constant__ RP rp, int blk0, int nblocks) {
+write_block_kernel(const WriteArgs a, const __grid_constant__ RP rp, const __grid_constant__ AT at) {
   const ChainEntry chain(a.late_wait != 0);
   constexpr int kBytes = block_bytes(SCH);
   constexpr bool kStaged = SCH != kBbox;
@@ -662,12 +697,10 @@ write_block_kernel(const WriteArgs a, const __grid_constant__ RP rp, int blk0, i
   [[maybe_unused]] const float2* turns = nullptr;
   int i, h, blk;
   if constexpr (kRotates<RP>) {
-    __shared__ float2 tab[kBlk][kRopePairs];
+    __shared__ __align__(16) float2 tab[kBlk][kRopePairs];
     const int hgroups = (a.Hkv + kBlockWriterWarps - 1) / kBlockWriterWarps;
-    const int ib = blockIdx.x / hgroups;                                     // (i * nblocks + b) * hgroups + head group
     h = blockIdx.x % hgroups * kBlockWriterWarps + warp;
-    blk = blk0 + ib % nblocks;
-    i = ib / nblocks;
+    at.place(a, blockIdx.x / hgroups, i, blk);                               // block-major, then head group
     for (int k = threadIdx.x; k < kBlk * kRopePairs; k += blockDim.x) {
       const int p = k % kRopePairs;
       float2 v = make_float2(1.f, 0.f);
@@ -678,25 +711,26 @@ write_block_kernel(const WriteArgs a, const __grid_constant__ RP rp, int blk0, i
     if (h >= a.Hkv) return;
     turns = tab[0];
   } else {
-    const long long unit = (long long)blockIdx.x * kBlockWriterWarps + warp;   // (i * Hkv + h) * nblocks + b
-    if (unit >= (long long)a.B * a.Hkv * nblocks) return;
-    const int sh = (int)(unit / nblocks);
-    i = sh / a.Hkv; h = sh % a.Hkv; blk = blk0 + (int)(unit % nblocks);
+    const long long unit = (long long)blockIdx.x * kBlockWriterWarps + warp;
+    if (!at.unit(a, unit, i, h, blk)) return;
   }
   uint8_t* im = img[warp];
   uint32_t* vst = vstage[warp];
   TokIn<T> cur, nxt;
-  cur.load(a, uniform_row(a, i, blk * kBlk - a.t0, h), lane, SCH == kBbox);
+  // i: the sequence, or its place among the launch's; seq: the sequence
+  int seq = i;
+  if constexpr (std::is_same<AT, RaggedBlocks>::value) seq = at.g.seq[i];
+  cur.load(a, at.row(a, i, blk * kBlk, h), lane, SCH == kBbox);
   for (int r = 0; r < kBlk; ++r) {
     const int t = blk * kBlk + r;
-    if (r + 1 < kBlk) nxt.load(a, uniform_row(a, i, t + 1 - a.t0, h), lane, SCH == kBbox);
+    if (r + 1 < kBlk) nxt.load(a, at.row(a, i, t + 1, h), lane, SCH == kBbox);
     if constexpr (kRotates<RP>) {
       LaneTurn w;
       w.from(rp, turns + r * kRopePairs, lane);
       turn_row(rp, w, cur.k, lane);
       if (SCH == kBbox) turn_row(rp, w, cur.kh, lane);
     }
-    write_token<T, SCH, VW, kStaged>(a, im, vst, i, h, t, lane, cur);
+    write_token<T, SCH, VW, kStaged>(a, im, vst, seq, h, t, lane, cur);
     cur = nxt;
   }
   __syncwarp();
@@ -715,7 +749,7 @@ write_block_kernel(const WriteArgs a, const __grid_constant__ RP rp, int blk0, i
     }
     __syncwarp();
   }
-  uint4* dst = reinterpret_cast<uint4*>(a.blocks + block_index(a.table, a.Hkv, a.nblk_max, i, h, blk) * kBytes);
+  uint4* dst = reinterpret_cast<uint4*>(a.blocks + block_index(a.table, a.Hkv, a.nblk_max, seq, h, blk) * kBytes);
   const uint4* src = reinterpret_cast<const uint4*>(im);
   for (int k = lane; k < kBytes / 16; k += 32) dst[k] = src[k];
 }
@@ -803,10 +837,10 @@ __global__ void __launch_bounds__(128) write_ragged_kernel(const WriteArgs a, co
                                                            const RaggedArgs g) {
   pdl_wait();
   pdl_trigger();
-  const int wid = (blockIdx.x * blockDim.x + threadIdx.x) >> 5, lane = threadIdx.x & 31;
-  const int total = g.off[g.n_seq];
-  if (wid >= total * a.Hkv) return;
-  const int h = wid % a.Hkv, tok = wid / a.Hkv;
+  const long long wid = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+  const int lane = threadIdx.x & 31;
+  if (wid >= (long long)g.off[g.n_seq] * a.Hkv) return;
+  const int h = (int)(wid % a.Hkv), tok = (int)(wid / a.Hkv);
   int lo = 0, hi = g.n_seq - 1;                     // the k with off[k] <= tok < off[k + 1]
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -941,10 +975,41 @@ cudaError_t kivi_keys_t(const WriteArgs& a, const RP& rp, cudaStream_t st, bool 
   return e;
 }
 
+// Writers by scheme; the INT8 ones compile the value witness in or out.
+#define WITCERT_WRITERS(NAME, KERNEL, ...)                                                                              \
+  template <typename T, typename RP, typename... Args>                                                                  \
+  cudaError_t NAME(int scheme, dim3 grid, dim3 block, cudaStream_t st, bool pdl, const WriteArgs& a, const RP& rp,      \
+                   const Args&... args) {                                                                               \
+    switch (scheme) {                                                                                                   \
+      case kInt8: return a.vwit ? launch_pdl(KERNEL<T, kInt8, true, RP __VA_ARGS__>, grid, block, st, pdl, a, rp, args...)   \
+                                : launch_pdl(KERNEL<T, kInt8, false, RP __VA_ARGS__>, grid, block, st, pdl, a, rp, args...); \
+      case kRtn: return a.vwit ? launch_pdl(KERNEL<T, kRtn, true, RP __VA_ARGS__>, grid, block, st, pdl, a, rp, args...)     \
+                               : launch_pdl(KERNEL<T, kRtn, false, RP __VA_ARGS__>, grid, block, st, pdl, a, rp, args...);   \
+      case kFp8: return launch_pdl(KERNEL<T, kFp8, false, RP __VA_ARGS__>, grid, block, st, pdl, a, rp, args...);            \
+      default: return launch_pdl(KERNEL<T, kBbox, false, RP __VA_ARGS__>, grid, block, st, pdl, a, rp, args...);             \
+    }                                                                                                                   \
+  }
+#define WITCERT_COMMA ,
+WITCERT_WRITERS(launch_tokens, write_token_kernel)
+WITCERT_WRITERS(launch_blocks, write_block_kernel, WITCERT_COMMA Args...)
+#undef WITCERT_WRITERS
+#undef WITCERT_COMMA
+
+template <typename T, typename RP, typename AT>
+cudaError_t launch_whole_blocks(int scheme, const WriteArgs& a, const RP& rp, const AT& at, cudaStream_t st, bool pdl) {
+  const long long ctas = kRotates<RP> ? at.blocks(a) * ((a.Hkv + kBlockWriterWarps - 1) / kBlockWriterWarps)
+                                      : (at.blocks(a) * a.Hkv + kBlockWriterWarps - 1) / kBlockWriterWarps;
+  return launch_blocks<T>(scheme, dim3((unsigned)ctas), dim3(kBlockWriterWarps * 32), st, pdl, a, rp, at);
+}
+
+// Writes of at most this many (token, KV head) rows go token by token, a warp each, even where they
+// fill blocks: a block's sixteen tokens one after another take about 30 us, and only a full GPU of
+// such warps makes up for it.  Blocks against tokens, dithered INT8: 512 rows 28.7 / 6.2 us, 8192
+// 30.7 / 12.3, 32768 36.9 / 28.7, 131072 86.0 / 96.2; FP8 22.5 / 8.2, 24.6 / 12.3, 30.7 / 24.6, 65.6 / 71.7.
+constexpr long long kTokenRows = 32768;
+
 template <typename T, typename RP>
 cudaError_t launch_t(int scheme, const WriteArgs& a, const RP& rp, cudaStream_t st, bool pdl) {
-  const int warps = a.B * a.n_tok * a.Hkv;
-  const dim3 blocks((warps * 32 + 127) / 128);
   if (scheme != kKivi) {
     // whole blocks through shared-memory images, the rest token by token
     const int t_end = a.t0 + a.n_tok;
@@ -955,40 +1020,23 @@ cudaError_t launch_t(int scheme, const WriteArgs& a, const RP& rp, cudaStream_t 
       b.tok_begin = begin;
       b.tok_count = count;
       const dim3 g(((unsigned)(a.B * count * a.Hkv) * 32u + 127u) / 128u);
-      const bool vw = a.vwit != nullptr;        // the INT8 writers compile the value witness in or out
-      return scheme == kInt8  ? (vw ? launch_pdl(write_token_kernel<T, kInt8, true, RP>, g, dim3(128), st, pdl, b, rp)
-                                    : launch_pdl(write_token_kernel<T, kInt8, false, RP>, g, dim3(128), st, pdl, b, rp))
-             : scheme == kRtn ? (vw ? launch_pdl(write_token_kernel<T, kRtn, true, RP>, g, dim3(128), st, pdl, b, rp)
-                                    : launch_pdl(write_token_kernel<T, kRtn, false, RP>, g, dim3(128), st, pdl, b, rp))
-             : scheme == kFp8 ? launch_pdl(write_token_kernel<T, kFp8, false, RP>, g, dim3(128), st, pdl, b, rp)
-                              : launch_pdl(write_token_kernel<T, kBbox, false, RP>, g, dim3(128), st, pdl, b, rp);
+      return launch_tokens<T>(scheme, g, dim3(128), st, pdl, b, rp);
     };
-    if (hi_full <= lo_full) return tokens(0, a.n_tok);
+    if (hi_full <= lo_full || (long long)a.B * a.n_tok * a.Hkv <= kTokenRows) return tokens(0, a.n_tok);
     cudaError_t e = tokens(0, lo_full - a.t0);
     if (e != cudaSuccess) return e;
-    const int nblocks = (hi_full - lo_full) / kBlk;
-    const long long ctas = kRotates<RP> ? (long long)a.B * nblocks * ((a.Hkv + kBlockWriterWarps - 1) / kBlockWriterWarps)
-                                        : ((long long)a.B * a.Hkv * nblocks + kBlockWriterWarps - 1) / kBlockWriterWarps;
-    const dim3 g((unsigned)ctas);
-    const dim3 wb(kBlockWriterWarps * 32);
-    const int b0 = lo_full / kBlk;
-    const bool vw = a.vwit != nullptr;
-    e = scheme == kInt8  ? (vw ? launch_pdl(write_block_kernel<T, kInt8, true, RP>, g, wb, st, pdl, a, rp, b0, nblocks)
-                               : launch_pdl(write_block_kernel<T, kInt8, false, RP>, g, wb, st, pdl, a, rp, b0, nblocks))
-        : scheme == kRtn ? (vw ? launch_pdl(write_block_kernel<T, kRtn, true, RP>, g, wb, st, pdl, a, rp, b0, nblocks)
-                               : launch_pdl(write_block_kernel<T, kRtn, false, RP>, g, wb, st, pdl, a, rp, b0, nblocks))
-        : scheme == kFp8 ? launch_pdl(write_block_kernel<T, kFp8, false, RP>, g, wb, st, pdl, a, rp, b0, nblocks)
-                         : launch_pdl(write_block_kernel<T, kBbox, false, RP>, g, wb, st, pdl, a, rp, b0, nblocks);
+    e = launch_whole_blocks<T>(scheme, a, rp, UniformBlocks{lo_full / kBlk, (hi_full - lo_full) / kBlk}, st, pdl);
     if (e != cudaSuccess) return e;
     return tokens(hi_full - a.t0, t_end - hi_full);
   }
-  cudaError_t e = launch_pdl(write_kivi_v_kernel<T, RP>, blocks, dim3(128), st, pdl, a, rp);
+  const int warps = a.B * a.n_tok * a.Hkv;
+  cudaError_t e = launch_pdl(write_kivi_v_kernel<T, RP>, dim3((warps * 32 + 127) / 128), dim3(128), st, pdl, a, rp);
   if (e != cudaSuccess) return e;
   return kivi_keys_t<T>(a, rp, st, pdl);
 }
 
 template <typename T, typename RP>
-cudaError_t launch_ragged_t(int scheme, const WriteArgs& a, const RP& rp, const RaggedArgs& g, cudaStream_t st, bool pdl) {
+cudaError_t launch_ragged_tokens(int scheme, const WriteArgs& a, const RP& rp, const RaggedArgs& g, cudaStream_t st, bool pdl) {
   const int total = g.off[g.n_seq];
   if (total == 0) return cudaSuccess;
   const dim3 grid((unsigned)(((long long)total * a.Hkv * 32 + 127) / 128));
@@ -1001,6 +1049,37 @@ cudaError_t launch_ragged_t(int scheme, const WriteArgs& a, const RP& rp, const 
     case kKivi: return launch_pdl(write_ragged_kernel<T, kKivi, false, RP>, grid, dim3(128), st, pdl, a, rp, g);
     default: return launch_pdl(write_ragged_kernel<T, kBbox, false, RP>, grid, dim3(128), st, pdl, a, rp, g);
   }
+}
+
+// Ragged appends of one launch's sequences: all their tokens, or, where there are many, their whole
+// blocks and then the tokens before and after those.
+template <typename T, typename RP>
+cudaError_t launch_ragged_t(int scheme, const WriteArgs& a, const RP& rp, const RaggedArgs& g, cudaStream_t st, bool pdl) {
+  if (scheme == kKivi || (long long)g.off[g.n_seq] * a.Hkv <= kTokenRows) return launch_ragged_tokens<T>(scheme, a, rp, g, st, pdl);
+  RaggedBlocks b{};
+  RaggedArgs ends[2]{};
+  for (int k = 0; k < g.n_seq; ++k) {
+    const int n = g.off[k + 1] - g.off[k], t0 = g.t0[k], t_end = t0 + n;
+    int lo = (t0 + kBlk - 1) / kBlk * kBlk, hi = t_end / kBlk * kBlk;
+    if (hi <= lo) lo = hi = t_end;                           // no whole block: all tokens count as before them
+    else {
+      const int x = b.g.n_seq++;
+      b.g.seq[x] = g.seq[k]; b.g.t0[x] = t0; b.g.row0[x] = g.row0[k];
+      b.blk0[x] = lo / kBlk;
+      b.g.off[x + 1] = b.g.off[x] + (hi - lo) / kBlk;
+    }
+    const int from[2] = {t0, hi}, to[2] = {lo, t_end};
+    for (int e = 0; e < 2; ++e) {
+      if (to[e] <= from[e]) continue;
+      const int x = ends[e].n_seq++;
+      ends[e].seq[x] = g.seq[k]; ends[e].t0[x] = from[e]; ends[e].row0[x] = g.row0[k] + from[e] - t0;
+      ends[e].off[x + 1] = ends[e].off[x] + to[e] - from[e];
+    }
+  }
+  cudaError_t e = cudaSuccess;
+  if (b.g.n_seq) e = launch_whole_blocks<T>(scheme, a, rp, b, st, pdl);
+  for (int k = 0; k < 2 && e == cudaSuccess; ++k) e = launch_ragged_tokens<T>(scheme, a, rp, ends[k], st, pdl);
+  return e;
 }
 
 }  // namespace

@@ -211,6 +211,59 @@ def test_rotated_ragged_append(scheme, pages):
     assert torch.equal(a[0], b[0]) and torch.equal(a[1]["raw_a"], b[1]["raw_a"])
 
 
+@pytest.mark.parametrize("scheme", SCHEMES)
+@pytest.mark.parametrize("pages", [0, 200])
+@pytest.mark.parametrize("turn", [False, True])
+def test_long_ragged_appends_equal_short_ones(scheme, pages, turn):
+    """Appends that go by whole blocks (many rows at once) store what appends of few tokens do."""
+    lens, hkv, at0 = [900, 0, 1307, 30], 16, [5, 3, 0, 16]
+    rope = wc.Rope(128)
+    mk = lambda: wc.Cache(1, hkv, hkv, 4, 1400, scheme, seed=8, max_pages=pages, v_witness=True)
+    whole, parts = mk(), mk()
+    K, V = (x.to("cuda", torch.bfloat16) for x in draws(3, sum(lens) + sum(at0), hkv))
+    Kh, Vh = (K * 0.984375, V * 0.984375) if scheme == "blackbox" else (None, None)
+
+    def write(c, rows, n):
+        hat = (None, None) if Kh is None else (Kh[rows], Vh[rows])
+        if turn:
+            c.witcert_write_rope_ragged(0, K[rows], V[rows], n, rope, *hat)
+        else:
+            c.witcert_write_ragged(0, K[rows], V[rows], n, *hat)
+
+    first = [sum(lens[:i]) for i in range(4)]
+    head = torch.arange(sum(at0), device="cuda") + sum(lens)
+    for c in (whole, parts):
+        write(c, head, at0)
+    write(whole, torch.arange(sum(lens), device="cuda"), lens)
+    done = [0] * 4
+    while done != lens:                                    # at most 301 tokens a sequence and call
+        n = [min(301, a - b) for a, b in zip(lens, done)]
+        rows = torch.cat([torch.arange(f + d, f + d + m) for f, d, m in zip(first, done, n)]).cuda()
+        write(parts, rows, n)
+        done = [a + b for a, b in zip(done, n)]
+    total = [a + b for a, b in zip(lens, at0)]
+    for a, b in zip(whole.read(0, total), parts.read(0, total)):
+        assert torch.equal(a, b)
+    for a, b in zip(store(whole, 0, scheme), store(parts, 0, scheme)):
+        for i, m in enumerate(total):
+            m = m // 16 if scheme == "kivi2" and a.shape[1] < 200 else m
+            assert torch.equal(a[i, :m], b[i, :m])
+
+
+@pytest.mark.parametrize("scheme", SCHEMES)
+def test_long_uniform_appends_equal_short_ones(scheme):
+    B, hkv, n = 2, 9, 1900                                 # 34200 rows: by whole blocks; 500 tokens: one by one
+    whole, parts = (wc.Cache(1, hkv, hkv, B, n + 7, scheme, seed=8) for _ in range(2))
+    K, V = (x.to("cuda", torch.bfloat16) for x in draws(4, B, n + 7, hkv))
+    rope = wc.Rope(96, interleaved=True)
+    for c, cuts in ((whole, [0, 7, n + 7]), (parts, [0, 7, 500, 1000, 1500, n + 7])):
+        for a, b in zip(cuts, cuts[1:]):
+            k, v = K[:, a:b].contiguous(), V[:, a:b].contiguous()
+            c.witcert_write_rope(0, k, v, rope, *((k, v) if scheme == "blackbox" else ()))
+    for a, b in zip(store(whole, 0, scheme), store(parts, 0, scheme)):
+        assert torch.equal(a, b)
+
+
 def test_rotated_keys_reach_the_backing_store():
     """A gated cache pages in the rotated exact keys, after bulk and single appends alike."""
     B, hkv, n = 1, 1, 80
