@@ -21,13 +21,13 @@ _TORCH_DT = {F32: torch.float32, BF16: torch.bfloat16}
 
 
 def _stream_ptr(stream) -> int:
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:          # the current stream's handle, without a Stream object around it
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return int(stream.cuda_stream)
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _extent(t, i):
@@ -111,22 +111,27 @@ def _need_rope(rope, head_dim):
 
 
 def _rope_tensor(name, x, y, n_tok, like):
-    """A tensor [n_tok, heads, head_dim] with adjacent channels and its output, for witcert_rope."""
+    """A tensor [n_tok, heads, head_dim] with adjacent channels and its output (None: a new contiguous
+    one): the output and what witcert_rope takes."""
+    if isinstance(x, torch.Tensor) and y is None:
+        y = x.new_empty(x.shape)
     for nm, t in ((name, x), (name + "_out", y)):
         if not isinstance(t, torch.Tensor):
             raise ValueError(f"{nm} must be a torch.Tensor, got {type(t).__name__}")
-        if t.dim() != 3 or t.shape[0] != n_tok or t.shape[2] != like.shape[2] or t.shape[1] != x.shape[1]:
-            raise ValueError(f"{nm} must have shape ({n_tok}, {x.shape[1] if x.dim() == 3 else '*'}, {like.shape[2]}), "
-                             f"got {tuple(t.shape)}")
-        if t.dtype != like.dtype:
-            raise ValueError(f"{nm} must be {like.dtype}, got {t.dtype}")
-        if t.stride(2) != 1:
-            raise ValueError(f"{nm} must have adjacent channels (stride 1), got stride {t.stride(2)}")
-    for nm, t in ((name, x), (name + "_out", y)):
-        if not t.is_cuda:
-            raise ValueError(f"{nm} must be a CUDA tensor")
-    return _lib.witcert_rope_tensor(x.data_ptr(), y.data_ptr(), x.shape[1], x.stride(0), x.stride(1), y.stride(0),
-                                    y.stride(1))
+    xs, shape = x.stride(), x.shape
+    ys = y.stride()
+    if not (len(shape) == 3 and y.shape == shape and shape[0] == n_tok and shape[2] == like.shape[2] and
+            x.dtype == like.dtype == y.dtype and xs[2] == 1 == ys[2] and x.is_cuda and y.is_cuda):
+        for nm, t in ((name, x), (name + "_out", y)):
+            if t.dim() != 3 or t.shape[0] != n_tok or t.shape[2] != like.shape[2] or t.shape[1] != x.shape[1]:
+                raise ValueError(f"{nm} must have shape ({n_tok}, {x.shape[1] if x.dim() == 3 else '*'}, "
+                                 f"{like.shape[2]}), got {tuple(t.shape)}")
+            if t.dtype != like.dtype:
+                raise ValueError(f"{nm} must be {like.dtype}, got {t.dtype}")
+            if t.stride(2) != 1:
+                raise ValueError(f"{nm} must have adjacent channels (stride 1), got stride {t.stride(2)}")
+        raise ValueError(f"{name if not x.is_cuda else name + '_out'} must be a CUDA tensor")
+    return y, _lib.witcert_rope_tensor(x.data_ptr(), y.data_ptr(), shape[1], xs[0], xs[1], ys[0], ys[1])
 
 
 def witcert_rope(rope, positions, q, k=None, q_out=None, k_out=None, inverse=False, stream=None):
@@ -141,18 +146,13 @@ def witcert_rope(rope, positions, q, k=None, q_out=None, k_out=None, inverse=Fal
     n_tok, _, head_dim = q.shape
     _need_rope(rope, head_dim)
     _need(("positions", positions, torch.int64, (n_tok,)))
-    if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    tq = _rope_tensor("q", q, q_out, n_tok, q)
-    tk = None
+    q_out, tq = _rope_tensor("q", q, q_out, n_tok, q)
     if k is not None:
-        if k_out is None:
-            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-        tk = _rope_tensor("k", k, k_out, n_tok, q)
+        k_out, tk = _rope_tensor("k", k, k_out, n_tok, q)
     elif k_out is not None:
         raise ValueError("k_out needs k")
     check(load().witcert_rope(rope._ref, BF16 if q.dtype == torch.bfloat16 else F32, head_dim, n_tok,
-                              _ptr(positions), ctypes.addressof(tq), None if tk is None else ctypes.addressof(tk),
+                              _ptr(positions), ctypes.addressof(tq), None if k is None else ctypes.addressof(tk),
                               int(bool(inverse)), _stream_ptr(stream)), "witcert_rope")
     return q_out if k is None else (q_out, k_out)
 
@@ -204,9 +204,10 @@ class Cache:
     def _counts(self, name, values):
         """One host integer per sequence, as the library takes them."""
         counts = [int(x) for x in values]
-        if len(counts) != self.cfg.batch:
-            raise ValueError(f"{name} needs one count per sequence ({self.cfg.batch}), got {len(counts)}")
-        return counts, (ctypes.c_int32 * len(counts))(*counts)
+        batch = self.cfg.batch
+        if len(counts) != batch:
+            raise ValueError(f"{name} needs one count per sequence ({batch}), got {len(counts)}")
+        return counts, (ctypes.c_int32 * batch)(*counts)
 
     def witcert_write_rope(self, layer, K, V, rope, K_hat=None, V_hat=None, stream=None):
         """witcert_write (witcert_write_hat with K_hat, V_hat) of keys without positions: each is turned by
@@ -241,6 +242,9 @@ class Cache:
         start = None if t0 is None else self._counts("t0", t0)[1]
         shape = (sum(counts), self.cfg.n_kv_heads, 128)
         _need(("K", K, self.dtype, shape), ("V", V, self.dtype, shape))
+        self._read(layer, start, arr, K, V, stream)
+
+    def _read(self, layer, start, arr, K, V, stream):
         check(load().witcert_read(self._h, layer, start, arr, _ptr(K), _ptr(V), _stream_ptr(stream)), "witcert_read")
 
     def witcert_attend_workspace(self, layer, n_tok):
@@ -257,14 +261,21 @@ class Cache:
         shape = (sum(counts), self.cfg.n_q_heads, 128)
         _need(("q", q, torch.bfloat16, shape), ("out", out, torch.bfloat16, shape),
               ("workspace", workspace, torch.uint8, (None,)))
+        self._attend(layer, q, arr, out, workspace, stream)
+
+    def _attend(self, layer, q, arr, out, workspace, stream):
         check(load().witcert_attend(self._h, layer, _ptr(q), arr, _ptr(out), _ptr(workspace), workspace.numel(),
                                     _stream_ptr(stream)), "witcert_attend")
 
     def attend(self, layer, q, n_tok, stream=None):
         """Chunk attention with a fresh output and workspace (see witcert_attend)."""
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        workspace = torch.empty(self.witcert_attend_workspace(layer, n_tok), dtype=torch.uint8, device=q.device)
-        self.witcert_attend(layer, q, n_tok, out, workspace, stream=stream)
+        counts, arr = self._counts("n_tok", n_tok)
+        n = ctypes.c_size_t()
+        check(load().witcert_attend_workspace(self._h, layer, arr, ctypes.byref(n)), "witcert_attend_workspace")
+        _need(("q", q, torch.bfloat16, (sum(counts), self.cfg.n_q_heads, 128)))
+        out = torch.empty_like(q)
+        workspace = torch.empty(n.value, dtype=torch.uint8, device=q.device)
+        self._attend(layer, q, arr, out, workspace, stream)
         if stream is not None:
             workspace.record_stream(stream)
             out.record_stream(stream)
@@ -374,10 +385,15 @@ class Cache:
 
     def read(self, layer, n_tok, t0=None, stream=None):
         """Keys and values the cache stands for, packed [sum(n_tok), Hkv, 128] (see witcert_read)."""
-        rows = sum(max(int(x), 0) for x in n_tok)
-        dev = torch.device("cuda", torch.cuda.current_device())
-        K, V = torch.empty((2, rows, self.cfg.n_kv_heads, 128), dtype=self.dtype, device=dev)
-        self.witcert_read(layer, t0, n_tok, K, V, stream=stream)
+        counts, arr = self._counts("n_tok", n_tok)
+        start = None if t0 is None else self._counts("t0", t0)[1]
+        shape = (max(sum(counts), 0), self.cfg.n_kv_heads, 128)      # the library refuses negative counts
+        K = torch.empty(shape, dtype=self.dtype, device="cuda")
+        V = torch.empty(shape, dtype=self.dtype, device="cuda")
+        self._read(layer, start, arr, K, V, stream)
+        if stream is not None:
+            K.record_stream(stream)
+            V.record_stream(stream)
         return K, V
 
     def export(self, layer, what, stream=None):
