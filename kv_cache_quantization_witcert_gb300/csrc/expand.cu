@@ -12,7 +12,7 @@ namespace witcert {
 namespace {
 
 template <int SCH>
-__global__ void __launch_bounds__(256) expand_kernel(const __grid_constant__ AttendArgs a) {
+__global__ void __launch_bounds__(256, SCH == kInt8 ? 4 : 3) expand_kernel(const __grid_constant__ AttendArgs a) {
   __shared__ __align__(16) uint32_t scratch[SCH == kInt8 ? 8 : 1][SCH == kInt8 ? kXwWords : 1];
   pdl_wait();
   pdl_trigger();

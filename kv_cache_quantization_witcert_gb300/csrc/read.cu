@@ -19,7 +19,7 @@ namespace {
 constexpr int kWarps = 4;
 
 template <int SCH, bool BF16>
-__global__ void __launch_bounds__(kWarps * 32) read_kernel(const __grid_constant__ ReadArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, SCH == kInt8 ? 9 : 8) read_kernel(const __grid_constant__ ReadArgs a) {
   __shared__ float scratch[SCH == kInt8 ? kWarps : 1][SCH == kInt8 ? kXsFloats : 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const long long unit = (long long)blockIdx.x * kWarps + warp;      // block * Hkv + head
