@@ -22,8 +22,9 @@
 // 4 x 64 = 488.
 // Two S buffers let S(j + 1) be formed while P(j) is; O += P V(j) follows S(j + 1), so a softmax warp
 // that must rescale O waits for it, and a row's threads swap through alternate words (S(j + 1) says
-// nothing about the partners' P(j)).  Images live in a ring of four 32 KB stages, keys and values of
-// a tile in turn.
+// nothing about the partners' P(j)).  Images live in 32 KB stages, two for keys and one or two for
+// values: what is left of shared memory is the ring of codes, whose size bounds the bytes in flight
+// (FP8: four half tiles 4.9 TB/s).
 #pragma once
 #include "attend.cuh"
 #include "expand.cuh"
@@ -32,19 +33,20 @@ namespace witcert {
 
 namespace {
 
-constexpr int kFewImages = 4;
 constexpr int kHalfBlocks = kTileTok / kBlk / 2;           // blocks of a half tile
 template <int SCH, bool TINY> struct FewSmem {
   static constexpr int kThreads = TINY ? 768 : 896;
   static constexpr int kN = TINY ? 4 : 2;                  // threads a row
   static constexpr int kSoftWarps = TINY ? 4 : 8;
   static constexpr int kHalf = kHalfBlocks * block_bytes(SCH);
+  // a second value stage costs the one-byte stores a third of their ring
+  static constexpr int kVStages = SCH == kKivi || SCH == kBbox ? 2 : 1, kImages = 2 + kVStages;
   // half tiles of codes in flight: what fits beside the images, at most eight
   static constexpr int kScratch = SCH == kInt8 ? 8 * kXwWords * 4 : 0;
-  static constexpr int kRoom = 232448 - kFewImages * kTileBytes - kScratch - 2 * kN * kTileRows * 4 - 512;
+  static constexpr int kRoom = 232448 - kImages * kTileBytes - kScratch - 2 * kN * kTileRows * 4 - 512;
   // (an even number, so that a stage always holds the same half and the same warps see its every use)
   static constexpr int kRing = kRoom / kHalf < 8 ? kRoom / kHalf / 2 * 2 : 8;
-  static constexpr int kRaw = kFewImages * kTileBytes;
+  static constexpr int kRaw = kImages * kTileBytes;
   static constexpr int kXs = kRaw + kRing * kHalf;
   static constexpr int kSwap = kXs + kScratch;
   static constexpr int kBar = kSwap + 2 * kN * kTileRows * 4;
@@ -61,14 +63,14 @@ __global__ void __launch_bounds__(FewSmem<SCH, TINY>::kThreads, 1) attend_few_ke
   extern __shared__ __align__(1024) uint8_t sm[];
   const uint32_t base = smem_addr(sm), bars = base + L::kBar;
   const uint32_t q_full = bars, raw_full = bars + 8, raw_empty = raw_full + 8 * kRing, img_full = raw_empty + 8 * kRing;
-  const uint32_t img_empty = img_full + 8 * kFewImages, s_full = img_empty + 8 * kFewImages, p_full = s_full + 16;
+  const uint32_t img_empty = img_full + 8 * L::kImages, s_full = img_empty + 8 * L::kImages, p_full = s_full + 16;
   const uint32_t pv_done = p_full + 32, o_full = pv_done + 8, pairs = o_full + 8, drain = pairs + 32, slot = drain + 8;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
 
   if (threadIdx.x == 0) {
     mbar_init(q_full, L::kSoftWarps);
     for (int s = 0; s < kRing; ++s) { mbar_init(raw_full + 8 * s, 1); mbar_init(raw_empty + 8 * s, 8); }
-    for (int s = 0; s < kFewImages; ++s) { mbar_init(img_full + 8 * s, 8); mbar_init(img_empty + 8 * s, 1); }
+    for (int s = 0; s < L::kImages; ++s) { mbar_init(img_full + 8 * s, 8); mbar_init(img_empty + 8 * s, 1); }
     for (int b = 0; b < 2; ++b) {
       mbar_init(s_full + 8 * b, 1);
       mbar_init(p_full + 16 * b, L::kSoftWarps);
@@ -119,22 +121,24 @@ __global__ void __launch_bounds__(FewSmem<SCH, TINY>::kThreads, 1) attend_few_ke
     int tiles = 0, done = 0;                               // of this CTA; tiles whose keys were taken
     uint32_t seg = 0;
     walk(a, cta, [&](const Segment& u) { tiles += u.nk; return true; });
-    auto image = [&](int x) { return base + (x % kFewImages) * kTileBytes; };     // image x: keys 2j, values 2j + 1
-    auto wait_image = [&](int x) { return warp_wait(img_full + 8 * (x % kFewImages), (x / kFewImages) & 1); };
-    // nobody waits for a stage that is not filled again
-    auto release = [&](int x) { if (x + kFewImages < 2 * tiles) warp_commit(img_empty + 8 * (x % kFewImages)); };
+    // tile j's keys are in stage j mod 2, its values in stage 2 + j mod kVStages; the barriers tell
+    // visits apart by parity, and a stage that is not filled again needs no release
+    auto k_stage = [&](int j) { return j & 1; };
+    auto v_stage = [&](int j) { return 2 + j % L::kVStages; };
+    auto image = [&](int st) { return base + st * kTileBytes; };
+    auto release = [&](int st, int next) { if (next < tiles) warp_commit(img_empty + 8 * st); };
     auto qk = [&](int j) {                                 // tile j of this CTA
-      if (!wait_image(2 * j)) return false;
+      if (!warp_wait(img_full + 8 * k_stage(j), (j >> 1) & 1)) return false;
       tc_fence_after();
       if (elect_one()) {
-        const uint64_t kd = sw128_desc(image(2 * j));
+        const uint64_t kd = sw128_desc(image(k_stage(j)));
 #pragma unroll
         for (int x = 0; x < 8; ++x)
           mma_ts(tm + (j & 1) * 128, tmem_q + x * 8, kd + (uint64_t)(x >> 2) * (kTileRows * 128 >> 4) + (x & 3) * 2, idesc, x > 0);
         mma_commit(s_full + 8 * (j & 1));
       }
       __syncwarp();
-      release(2 * j);
+      release(k_stage(j), j + 2);
       return true;
     };
     walk(a, cta, [&](const Segment& u) {
@@ -146,11 +150,11 @@ __global__ void __launch_bounds__(FewSmem<SCH, TINY>::kThreads, 1) attend_few_ke
       for (int s = 0; s < u.nk; ++s) {
         const int j = done + s;
         if (s + 1 < u.nk) dead = !qk(j + 1);
-        dead = dead || !wait_image(2 * j + 1) ||
-               !issue_pv<N>(tmem_o, tm + (j & 1) * 128, sw128_desc(image(2 * j + 1)), idesc, s == 0, p_full + 16 * (j & 1), (j >> 1) & 1);
+        dead = dead || !warp_wait(img_full + 8 * v_stage(j), (j / L::kVStages) & 1) ||
+               !issue_pv<N>(tmem_o, tm + (j & 1) * 128, sw128_desc(image(v_stage(j))), idesc, s == 0, p_full + 16 * (j & 1), (j >> 1) & 1);
         if (dead) return false;
         warp_commit(s + 1 < u.nk ? pv_done : o_full);
-        release(2 * j + 1);
+        release(v_stage(j), j + L::kVStages);
       }
       done += u.nk;
       return true;
@@ -217,28 +221,33 @@ __global__ void __launch_bounds__(FewSmem<SCH, TINY>::kThreads, 1) attend_few_ke
     x.pr = (e >> 1) & 3;
     [[maybe_unused]] uint32_t* xs = reinterpret_cast<uint32_t*>(sm + L::kXs) + (e & 7) * kXwWords;
     RingAt<kRing / 2> at;                                  // the tile's halves: stages 2 at.st and + 1
-    RingAt<kFewImages / 2> img;                            // image x of the CTA in stage x mod 4: keys 0 and 2, values 1 and 3
-    int made = 0;
+    const int stages = values ? L::kVStages : 2;
+    int made = 0, in = 0;                                  // tiles so far; this tile's stage among them
+    uint32_t ph = 0;
     walk(a, cta, [&](const Segment& u) {
       x.h = u.h;
       x.len = a.len[u.k];
       for (int j = u.j0; j < u.j0 + u.nk; ++j, ++made) {
-        const int raw_st = 2 * at.st + half, st = 2 * img.st + values;
+        const int raw_st = 2 * at.st + half, st = 2 * values + in;
         x.tb = j * kTileTok + x.pr * 2 * kBlk;
         x.bp[0] = sm + L::kRaw + raw_st * L::kHalf + (x.pr & 1) * 2 * block_bytes(SCH);
         x.bp[1] = x.bp[0] + block_bytes(SCH);
-        if (!warp_wait(raw_full + 8 * raw_st, at.ph) ||
-            (made >= kFewImages / 2 && !warp_wait(img_empty + 8 * st, img.ph ^ 1))) { dead = true; return false; }
+        // the codes leave the ring as soon as they are in registers, before this tile's stage is free
+        auto got = [&] { warp_arrive(raw_empty + 8 * raw_st); };
+        auto ready = [&] { return made < stages || warp_wait(img_empty + 8 * st, ph ^ 1); };
+        dead = !warp_wait(raw_full + 8 * raw_st, at.ph);
+        if (dead) return false;
         if (values) {
-          expand_values<SCH>(a.s, x, j0, xs, sm + st * kTileBytes, [&] { warp_arrive(raw_empty + 8 * raw_st); });
+          dead = !expand_values<SCH>(a.s, x, j0, xs, sm + st * kTileBytes, got, ready);
         } else {
           find_exact<SCH>(a.s, a.seq[u.k], x);
-          expand_keys<SCH>(a.s, x, j0, sm + st * kTileBytes, [&] { warp_arrive(raw_empty + 8 * raw_st); });
+          dead = !expand_keys<SCH>(a.s, x, j0, sm + st * kTileBytes, got, ready);
         }
+        if (dead) return false;
         fence_proxy_async();
         warp_arrive(img_full + 8 * st);
-        img.next();
         at.next();
+        if (++in == stages) { in = 0; ph ^= 1; }
       }
       return true;
     });

@@ -34,8 +34,8 @@ __global__ void __launch_bounds__(256, SCH == kInt8 ? 4 : 3) expand_kernel(const
     x.bp[b] = a.s.blocks + block_index(a.s.table, a.s.Hkv, a.s.nblk_max, i, x.h,
                                        x.tb + b * kBlk < x.len ? x.tb / kBlk + b : first) * block_bytes(SCH);
   find_exact<SCH>(a.s, i, x);
-  expand_keys<SCH>(a.s, x, 2 * (warp & 1), img, [] {});
-  expand_values<SCH>(a.s, x, 2 * (warp & 1), scratch[SCH == kInt8 ? warp : 0], img + kTileBytes, [] {});
+  expand_keys<SCH>(a.s, x, 2 * (warp & 1), img, [] {}, [] { return true; });
+  expand_values<SCH>(a.s, x, 2 * (warp & 1), scratch[SCH == kInt8 ? warp : 0], img + kTileBytes, [] {}, [] { return true; });
 }
 
 // The dither of a tile and head in the order the expanding lanes fetch it.

@@ -258,10 +258,11 @@ __device__ __forceinline__ void find_exact(const StoreArgs& s, int i, BlockPair&
   }
 }
 // Steps j0 and j0 + 1 (j0 = 0 or 2: one panel of the key image) of the two blocks into the key image,
-// or the value image.  got() is called when the last codes are in registers.  What is decoded together
-// is decoded before any of it is stored: loads do not pass stores that might alias them.
-template <int SCH, typename F>
-__device__ __forceinline__ void expand_keys(const StoreArgs& s, const BlockPair& x, int j0, uint8_t* img, F got) {
+// or the value image.  got() is called when the last codes are in registers, ready() before the first
+// store: false gives up.  What is decoded together is decoded before any of it is stored: loads do
+// not pass stores that might alias them.
+template <int SCH, typename F, typename G>
+__device__ __forceinline__ bool expand_keys(const StoreArgs& s, const BlockPair& x, int j0, uint8_t* img, F got, G ready) {
   constexpr int S = kSteps<SCH>;
   const int g = x.lane >> 2, t = x.lane & 3;
   const bool tail = x.tb + 2 * kBlk > x.len;
@@ -296,6 +297,7 @@ __device__ __forceinline__ void expand_keys(const StoreArgs& s, const BlockPair&
           codes[b].words(jj, n[b], w[jj][b]);
         }
       }
+    if (ja == 0 && !ready()) return false;
 #pragma unroll
     for (int jj = 0; jj < S; ++jj)
 #pragma unroll
@@ -308,9 +310,11 @@ __device__ __forceinline__ void expand_keys(const StoreArgs& s, const BlockPair&
           *reinterpret_cast<uint4*>(img + (j0 >> 1) * (kTileTok * 128) + row * 128 + (((4 * (ja + jj) + t) ^ (row & 7)) << 4)) = v;
         }
   }
+  return true;
 }
-template <int SCH, typename F>
-__device__ __forceinline__ void expand_values(const StoreArgs& s, const BlockPair& x, int j0, uint32_t* xs, uint8_t* img, F got) {
+template <int SCH, typename F, typename G>
+__device__ __forceinline__ bool expand_values(const StoreArgs& s, const BlockPair& x, int j0, uint32_t* xs, uint8_t* img, F got,
+                                              G ready) {
   constexpr int S = kSteps<SCH>;
   const int g = x.lane >> 2, t = x.lane & 3;
   const bool tail = x.tb + 2 * kBlk > x.len;
@@ -345,6 +349,7 @@ __device__ __forceinline__ void expand_values(const StoreArgs& s, const BlockPai
           }
         }
       }
+    if (ja == 0 && !ready()) return false;
 #pragma unroll
     for (int jj = 0; jj < S; ++jj)
 #pragma unroll
@@ -358,6 +363,7 @@ __device__ __forceinline__ void expand_values(const StoreArgs& s, const BlockPai
                          __byte_perm(a[1], b[1], 0x7632));
         }
   }
+  return true;
 }
 
 }  // namespace witcert
