@@ -746,9 +746,12 @@ static int attend_key_tiles(const AttendArgs& a, int k, int rt) {
 
 // Shares the units' key tiles out to CTAs, one an SM: the same number to each, units cut where that
 // falls, unless whole units do as well.  A cut costs the records' merge and a second start of the
-// pipeline, about kCutTiles key tiles' time, and shares below kMinShare tiles are not worth it.
+// pipeline, about kCutTiles key tiles' time, and shares below kMinShare tiles are not worth it: FP8,
+// 32 query heads on 8, four tokens a sequence, with (kCutTiles, kMinShare) of (0, 1), (3, 2) and only
+// whole units: 16 sequences of 1000 tokens 29.3, 21.2, 21.2 us; 4 of 1024 17.1, 17.1, 19.1; 1 of 512
+// 12.9, 14.3, 15.0; 40 of 2000 68.2, 67.2, 76.4.
 static void share_units(AttendArgs& a, int sm_count) {
-  constexpr int kCutTiles = 6, kMinShare = 4;
+  constexpr int kCutTiles = 3, kMinShare = 2;
   const int Hkv = a.s.Hkv, sms = std::min(sm_count, kAttendCtas);
   long long total = 0, units = 0;
   int most = 1;
@@ -781,8 +784,12 @@ static void share_units(AttendArgs& a, int sm_count) {
 }
 
 // Sequences of at most this many query rows a KV head are attended straight from the store, each
-// row tile of 128 reading the codes itself; longer ones share operand images.
-constexpr int kFewRows = kTileRows;
+// row tile of 128 reading the codes itself; longer ones share operand images.  Images against store,
+// us, 32 query heads on 8: one sequence of 32768 tokens, FP8, 256 rows 109.8 / 74.4, 512 117.4 / 105.1,
+// 1024 152.8 / 176.8; two-bit 256 105.7 / 92.8, 384 112.1 / 117.4; eight sequences of 4096, FP8, 256
+// 93.4 / 58.0, 512 99.0 / 109.2.  Where every row tile forms the dither itself, one is the limit: 132
+// rows 140.8 / 187.0 (with a shared dither, eight sequences, 256 rows: 110.2 / 99.0).
+constexpr int kFewRows = 2 * kTileRows, kFewRowsDither = kTileRows;
 
 // What an attend call launches, and the parts of its workspace: the images and the records of the
 // largest group, and the dithered store's dither.
@@ -792,8 +799,10 @@ struct AttendPlan {
   int dither_tiles = 0;
   size_t bytes() const { return image_bytes + rec_bytes + dither_bytes; }
 };
-// Sequences that share a dither have it formed once when together they read it at least twice
-// (forming it takes a tile's expansion some 4000 cycles of integer work, fetching it 64 KB).
+// Sequences that share a dither have it formed once when together they read it at least twice.  Formed
+// once against formed by each, us, sequences of 8192 tokens, four new tokens each: 1 sequence 39.6 /
+// 39.6, 2 49.8 / 58.0, 4 65.0 / 96.9, 8 98.9 / 174.7; 128 new tokens: 1 75.4 / 70.8, 2 95.4 / 91.4,
+// 8 236.2 / 255.2.
 constexpr int kDitherShare = 2;
 
 static void plan_attend(const witcert_cache* c, int layer, const int32_t* n_tok, AttendPlan& plan) {
@@ -810,6 +819,7 @@ static void plan_attend(const witcert_cache* c, int layer, const int32_t* n_tok,
     }
   if (read_tiles < (long long)kDitherShare * plan.dither_tiles) plan.dither_tiles = 0;
   plan.dither_bytes = plan.dither_tiles * Hkv * kDitherTile;
+  const long long most_few = c->scheme == kInt8 && !plan.dither_tiles ? kFewRowsDither : kFewRows;
   for (const int unit_rows : {kTinyRows, kTileRows, 2 * kTileRows}) {
     const bool few = unit_rows <= kTileRows;
     bool open = false;
@@ -818,7 +828,7 @@ static void plan_attend(const witcert_cache* c, int layer, const int32_t* n_tok,
       const int n = n_tok[i], len = c->slen[layer][i], at = row0;
       row0 += n;
       const long long rows = (long long)n * grp;
-      if (n == 0 || unit_rows != (rows <= kTinyRows ? kTinyRows : rows <= kFewRows ? kTileRows : 2 * kTileRows)) continue;
+      if (n == 0 || unit_rows != (rows <= kTinyRows ? kTinyRows : rows <= most_few ? kTileRows : 2 * kTileRows)) continue;
       const int tiles = (len + kTileTok - 1) / kTileTok;
       if (!open || groups.back().n_seq == kAttendSeqs ||
           (!few && (groups.back().tile_off[groups.back().n_seq] + (size_t)tiles) * tile > kImageCap)) {
