@@ -1,6 +1,7 @@
 // The keys and values a compressed cache stands for, as rows of the cache's dtype.
 //
-// One warp per (sequence, KV head, 16-token block).  Bound by HBM: codes in, rows out (272 B and
+// One warp per (sequence, KV head, 16-token block), or, where that leaves the GPU empty, one per
+// quarter of its channels (128 blocks of the dithered store: 12.2 us by whole blocks).  Bound by HBM: codes in, rows out (272 B and
 // 512 B a token and head for INT8 caches of bf16 rows); the dithered store adds the regeneration
 // of its dither, 2 x 32 Philox calls a token and head on the integer units.
 //
@@ -17,12 +18,15 @@ namespace witcert {
 namespace {
 
 constexpr int kWarps = 4;
+constexpr long long kFewUnits = 4096;            // about the warps the GPU holds at once
 
-template <int SCH, bool BF16>
+template <int SCH, bool BF16, bool QUARTERS>
 __global__ void __launch_bounds__(kWarps * 32, SCH == kInt8 ? 9 : 8) read_kernel(const __grid_constant__ ReadArgs a) {
   __shared__ float scratch[SCH == kInt8 ? kWarps : 1][SCH == kInt8 ? kXsFloats : 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const long long unit = (long long)blockIdx.x * kWarps + warp;      // block * Hkv + head
+  static_assert(kWarps == 4, "a warp a quarter");
+  const long long unit = QUARTERS ? (long long)blockIdx.x : (long long)blockIdx.x * kWarps + warp;   // block * Hkv + head
+  const int first = QUARTERS ? warp : 0;
   const int bidx = (int)(unit / a.s.Hkv), h = (int)(unit % a.s.Hkv);
   if (bidx >= a.blk_off[a.n_seq]) return;
   int lo = 0, hi = a.n_seq - 1;                                      // the k with blk_off[k] <= bidx < blk_off[k + 1]
@@ -43,7 +47,7 @@ __global__ void __launch_bounds__(kWarps * 32, SCH == kInt8 ? 9 : 8) read_kernel
   T* K = static_cast<T*>(a.K);
   T* V = static_cast<T*>(a.V);
 #pragma unroll 1
-  for (int j = 0; j < 4; ++j) {
+  for (int j = first; j < (QUARTERS ? first + 1 : 4); ++j) {
     float x[2][2][4];
     if (exact) exact_keys(a.s, exact, ebf, j, lane, x);
     else block_keys<SCH>(a.s, bp, h, a.s.pos0 + tb, j, lane, x);
@@ -89,10 +93,15 @@ __global__ void __launch_bounds__(kWarps * 32, SCH == kInt8 ? 9 : 8) read_kernel
 
 template <int SCH>
 cudaError_t launch_s(const ReadArgs& a, cudaStream_t st) {
-  const long long warps = (long long)a.blk_off[a.n_seq] * a.s.Hkv;
-  const unsigned grid = (unsigned)((warps + kWarps - 1) / kWarps);
-  if (a.s.is_bf16) read_kernel<SCH, true><<<grid, kWarps * 32, 0, st>>>(a);
-  else read_kernel<SCH, false><<<grid, kWarps * 32, 0, st>>>(a);
+  const long long units = (long long)a.blk_off[a.n_seq] * a.s.Hkv;
+  if (units < kFewUnits) {
+    if (a.s.is_bf16) read_kernel<SCH, true, true><<<(unsigned)units, kWarps * 32, 0, st>>>(a);
+    else read_kernel<SCH, false, true><<<(unsigned)units, kWarps * 32, 0, st>>>(a);
+  } else {
+    const unsigned grid = (unsigned)((units + kWarps - 1) / kWarps);
+    if (a.s.is_bf16) read_kernel<SCH, true, false><<<grid, kWarps * 32, 0, st>>>(a);
+    else read_kernel<SCH, false, false><<<grid, kWarps * 32, 0, st>>>(a);
+  }
   return cudaGetLastError();
 }
 

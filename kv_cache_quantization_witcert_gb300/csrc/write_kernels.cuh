@@ -66,7 +66,9 @@ template <typename RP> inline constexpr bool kRotates = !std::is_same<RP, NoRope
 __device__ __forceinline__ int lane_pair(const RopeArgs& rp, int lane) {
   return rp.interleaved ? 2 * lane : 4 * (lane % (rp.rot >> 3));
 }
-// cos and sin of the lane's pairs at position pos.
+// cos and sin of the lane's pairs at position pos; in the half layout with -sin for lanes of the first
+// half, so that both halves are x c + other s.
+__device__ __forceinline__ bool first_half(const RopeArgs& rp, int lane) { return !rp.interleaved && lane < (rp.rot >> 3); }
 struct LaneTurn {
   float c[4], s[4];
   __device__ __forceinline__ void at(const RopeArgs& rp, int64_t pos, int lane) {
@@ -75,6 +77,7 @@ struct LaneTurn {
     for (int e = 0; e < 4; ++e) {
       c[e] = 1.f; s[e] = 0.f;
       if (e < n) rope_cs(rp.turn[p0 + e], pos, rp.gain, c[e], s[e]);
+      if (first_half(rp, lane)) s[e] = -s[e];
     }
   }
   // from a table of (cos, sin) of all the pairs
@@ -84,6 +87,10 @@ struct LaneTurn {
     const float4 b = *reinterpret_cast<const float4*>(tab + (rp.interleaved ? p0 : p0 + 2));
     c[0] = a.x; s[0] = a.y; c[1] = a.z; s[1] = a.w;
     c[2] = b.x; s[2] = b.y; c[3] = b.z; s[3] = b.w;
+    if (first_half(rp, lane)) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[e] = -s[e];
+    }
   }
 };
 template <typename T>
@@ -98,13 +105,9 @@ __device__ __forceinline__ void turn_row(const RopeArgs& rp, const LaneTurn& w, 
     }
   } else {
     const int half = rp.rot >> 3;            // lanes of the first half of the rotated channels
-    const bool first = lane < half;
-    const int other = lane >= 2 * half ? lane : first ? lane + half : lane - half;
+    const int other = lane >= 2 * half ? lane : lane < half ? lane + half : lane - half;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float o = __shfl_sync(0xffffffffu, x[e], other);
-      y[e] = first ? rope_first(x[e], o, w.c[e], w.s[e]) : rope_second(o, x[e], w.c[e], w.s[e]);
-    }
+    for (int e = 0; e < 4; ++e) y[e] = rope_second(__shfl_sync(0xffffffffu, x[e], other), x[e], w.c[e], w.s[e]);
   }
   if (4 * lane < rp.rot) k.set(y);
 }
