@@ -417,6 +417,9 @@ static witcert_status write_impl(witcert_cache* c, int layer, const void* K, con
   if (total > 0 && (!K || !V)) return fail(WITCERT_EINVAL, "K and V must not be NULL");
   if (total > 0 && c->scheme == kBbox && (!Kh || !Vh)) return fail(WITCERT_EINVAL, "K_hat and V_hat must not be NULL");
   if (total == 0) { ok(); return WITCERT_OK; }
+  // the writers load four elements at a time
+  if (((uintptr_t)K | (uintptr_t)V | (uintptr_t)Kh | (uintptr_t)Vh) % (4 * c->elem))
+    return fail(WITCERT_EINVAL, "K, V, K_hat and V_hat must be %d-byte aligned", 4 * c->elem);
   bool uniform = !c->ragged;
   for (int i = 1; i < B && uniform; ++i) uniform = n[i] == n[0];
   std::vector<std::pair<int, int>> pages;
@@ -563,6 +566,9 @@ witcert_status witcert_rope(const witcert_rope_config* rope, witcert_dtype dtype
     const witcert_rope_tensor& t = *in[i];
     if (t.n_heads < 1 || t.n_heads > 65535) return fail(WITCERT_EINVAL, "n_heads must be in [1, 65535]");
     if (n_tok > 0 && (!t.x || !t.y)) return fail(WITCERT_EINVAL, "x and y must not be NULL");
+    if (((uintptr_t)t.x | (uintptr_t)t.y) % (dtype == WITCERT_BF16 ? 2 : 4)) return fail(WITCERT_EINVAL, "x and y must be aligned to their elements");
+    if ((n_tok > 1 && t.y_token_stride == 0) || (t.n_heads > 1 && t.y_head_stride == 0))
+      return fail(WITCERT_EINVAL, "outputs must not share their elements (stride 0)");
     a.t[i] = RopeTensor{t.x, t.y, t.x_token_stride, t.x_head_stride, t.y_token_stride, t.y_head_stride, t.n_heads};
   }
   if (n_tok == 0) { ok(); return WITCERT_OK; }
@@ -702,6 +708,7 @@ witcert_status witcert_read(witcert_cache* c, int layer, const int32_t* t0, cons
   }
   if (total == 0) { ok(); return WITCERT_OK; }
   if (!K || !V) return fail(WITCERT_EINVAL, "K and V must not be NULL");
+  if (((uintptr_t)K | (uintptr_t)V) % 16) return fail(WITCERT_EINVAL, "K and V must be 16-byte aligned");
   auto st = static_cast<cudaStream_t>(stream);
   order_after_gate(c, layer, st);
   ReadArgs a{};
@@ -908,8 +915,8 @@ witcert_status witcert_attend(witcert_cache* c, int layer, const void* q, const 
   if (witcert_status s = check_attend(c, layer, n_tok, rows)) return s;
   if (rows == 0) { ok(); return WITCERT_OK; }
   if (!q || !out) return fail(WITCERT_EINVAL, "q and out must not be NULL");
-  if (((uintptr_t)q | (uintptr_t)out | (uintptr_t)workspace) % 16)
-    return fail(WITCERT_EINVAL, "q, out and workspace must be 16-byte aligned");
+  if (((uintptr_t)q | (uintptr_t)out | (uintptr_t)workspace) % 32)
+    return fail(WITCERT_EINVAL, "q, out and workspace must be 32-byte aligned");
   AttendPlan plan;
   plan_attend(c, layer, n_tok, plan);
   if (plan.bytes() > workspace_bytes || !workspace)

@@ -215,6 +215,46 @@ def test_attend_on_another_stream_and_twice():
     assert torch.equal(first, again)
 
 
+def test_misaligned_buffers_are_refused():
+    c = wc.Cache(1, 2, 1, 1, 64, "fp8_e4m3")
+    flat = torch.zeros(64 * 128 + 64, dtype=torch.bfloat16, device="cuda")
+    off = lambda n, rows, heads: flat[n:n + rows * heads * 128].view(rows, heads, 128)
+    with pytest.raises(wc.WitcertError, match="aligned"):
+        c.witcert_write(0, off(1, 5, 1)[None].view(1, 5, 1, 128), off(0, 5, 1).view(1, 5, 1, 128))
+    assert c.witcert_length(0) == 0
+    c.witcert_write(0, off(4, 5, 1).view(1, 5, 1, 128), off(0, 5, 1).view(1, 5, 1, 128))
+    with pytest.raises(wc.WitcertError, match="aligned"):
+        c.attend(0, off(8, 5, 2), [5])
+    with pytest.raises(wc.WitcertError, match="aligned"):
+        c.witcert_read(0, None, [5], off(0, 5, 1), off(4, 5, 1))
+    assert c.attend(0, off(16, 5, 2), [5]).shape == (5, 2, 128)
+
+
+def test_calls_can_be_captured():
+    """A captured step (rotation and chunk attention) replays on new queries."""
+    p = Pair("int8_dither", 8, 2, [400, 90], seed=13)
+    n = [4, 3]
+    rope, pos = wc.Rope(128), torch.arange(7, device="cuda")
+    q = p.queries(n).cuda()
+    out = torch.empty_like(q)
+    ws = torch.empty(p.gpu.witcert_attend_workspace(0, n), dtype=torch.uint8, device="cuda")
+
+    def step():
+        p.gpu.witcert_attend(0, wc.witcert_rope(rope, pos, q), n, out, ws)
+
+    step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    q.copy_(p.queries(n, seed=99))
+    g.replay()
+    torch.cuda.synchronize()
+    got = out.clone()
+    step()
+    assert torch.equal(got, out)
+
+
 def test_refusals():
     c = wc.Cache(1, 4, 2, 2, 64, "fp8_e4m3")
     K = torch.zeros(2, 5, 2, 128, dtype=torch.bfloat16, device="cuda")

@@ -147,6 +147,10 @@ def test_library_refuses_bad_arguments(lib):
     assert rope(k=ctypes.addressof(headless)) == _lib.EINVAL and b"n_heads" in lib.witcert_last_error()
     nothing = _lib.witcert_rope_tensor(None, 16, 2, 256, 128, 256, 128)
     assert rope(q=ctypes.addressof(nothing)) == _lib.EINVAL
+    shared = _lib.witcert_rope_tensor(16, 16, 2, 256, 128, 0, 128)
+    assert rope(n=2, q=ctypes.addressof(shared)) == _lib.EINVAL and b"stride 0" in lib.witcert_last_error()
+    odd = _lib.witcert_rope_tensor(17, 16, 2, 256, 128, 256, 128)
+    assert rope(q=ctypes.addressof(odd)) == _lib.EINVAL and b"aligned" in lib.witcert_last_error()
     assert rope(n=0) == _lib.OK                                  # nothing to do, no GPU needed
     for dim, freq, scale in ((12, 1.0, 1.0), (136, 1.0, 1.0), (128, math.inf, 1.0), (128, 1.0, math.nan)):
         bad = _lib.witcert_rope_config(dim, 0, scale, (ctypes.c_double * 128)(*([freq] * 128)))
