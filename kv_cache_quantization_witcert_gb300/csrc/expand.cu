@@ -38,15 +38,16 @@ __global__ void __launch_bounds__(256, SCH == kInt8 ? 4 : 3) expand_kernel(const
   expand_values<SCH>(a.s, x, 2 * (warp & 1), scratch[SCH == kInt8 ? warp : 0], img + kTileBytes, [] {}, [] { return true; });
 }
 
-// The dither of a tile and head in the order the expanding lanes fetch it.
+// The dither of a tile and head in the order the expanding lanes fetch it; a quarter of it a CTA (keys
+// or values, one step of a warp's two), as there are few tiles: 128 tiles and heads 6.2 us by whole ones.
 __global__ void __launch_bounds__(256) dither_kernel(const __grid_constant__ StoreArgs s, uint4* table) {
   __shared__ __align__(16) uint32_t scratch[8][kXwWords];
   pdl_trigger();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int h = blockIdx.x % s.Hkv, tile = blockIdx.x / s.Hkv, pr = warp >> 1, j0 = 2 * (warp & 1);
 #pragma unroll 1
-  for (int k = 0; k < 8; ++k) {
-    const int values = k >> 2, j = j0 + ((k >> 1) & 1), b = k & 1, tb = s.pos0 + tile * kTileTok + (2 * pr + b) * kBlk;
+  for (int b = 0; b < 2; ++b) {
+    const int values = blockIdx.y >> 1, j = j0 + (blockIdx.y & 1), tb = s.pos0 + tile * kTileTok + (2 * pr + b) * kBlk;
     uint32_t n[2][2][2];
     if (values) value_dither(s, h, tb, j, lane, scratch[warp], n);
     else key_dither(s, h, tb, j, lane, n);
@@ -59,7 +60,7 @@ __global__ void __launch_bounds__(256) dither_kernel(const __grid_constant__ Sto
 }  // namespace
 
 cudaError_t launch_dither_table(const StoreArgs& s, uint4* table, int tiles, cudaStream_t st) {
-  dither_kernel<<<(unsigned)(tiles * s.Hkv), 256, 0, st>>>(s, table);
+  dither_kernel<<<dim3((unsigned)(tiles * s.Hkv), 4), 256, 0, st>>>(s, table);
   return cudaGetLastError();
 }
 
