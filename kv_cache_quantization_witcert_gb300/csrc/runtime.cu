@@ -751,14 +751,19 @@ static int attend_key_tiles(const AttendArgs& a, int k, int rt) {
   return (int)((a.len[k] - a.n[k] + last / a.grp) / kTileTok) + 1;
 }
 
-// Shares the units' key tiles out to CTAs, one an SM: the same number to each, units cut where that
-// falls, unless whole units do as well.  A cut costs the records' merge and a second start of the
+// Shares the units' key tiles out to CTAs, one an SM: the same time to each, units cut where that
+// falls, unless whole units do as well.  A unit's time is its key tiles and its start and end (queries
+// in, outputs out, the pipeline empty), as long as kStart tiles: with 0, 2, 3, 4 and 6 of them 4096 new
+// tokens of 4096 take 318.7, 190.0, 156.3, 147.1, 144.6 us, 700 of 6000 in three sequences 197.8,
+// 187.9, 187.6, 187.6, 189.6, and, straight from the store, 4 of 700 in forty sequences 40.5, 39.6,
+// 39.6, 41.6, 41.6, 16 of 16384 in two 51.8, 49.8, 47.1, 47.1, 47.7.  A cut costs the records' merge and a second start of the
 // pipeline, about kCutTiles key tiles' time, and shares below kMinShare tiles are not worth it: FP8,
 // 32 query heads on 8, four tokens a sequence, with (kCutTiles, kMinShare) of (0, 1), (3, 2) and only
 // whole units: 16 sequences of 1000 tokens 29.3, 21.2, 21.2 us; 4 of 1024 17.1, 17.1, 19.1; 1 of 512
 // 12.9, 14.3, 15.0; 40 of 2000 68.2, 67.2, 76.4.
 static void share_units(AttendArgs& a, int sm_count) {
   constexpr int kCutTiles = 3, kMinShare = 2;
+  const int kStart = a.unit_rows > kTileRows ? 4 : 3;
   const int Hkv = a.s.Hkv, sms = std::min(sm_count, kAttendCtas);
   long long total = 0, units = 0;
   int most = 1;
@@ -766,23 +771,23 @@ static void share_units(AttendArgs& a, int sm_count) {
     for (int rt = 0, rts = attend_row_tiles(a, k); rt < rts; ++rt) {
       const int nt = attend_key_tiles(a, k, rt);
       units += Hkv;
-      total += (long long)nt * Hkv;
+      total += (long long)(nt + kStart) * Hkv;
       most = std::max(most, nt);
     }
   const long long per_cta = (units + sms - 1) / sms;
-  const long long even = std::max<long long>((total + sms - 1) / sms, std::min(kMinShare, most));
-  const bool whole = per_cta * most <= even + kCutTiles;
-  // CTA c starts at place c * share, counted in units or in key tiles
+  const long long even = std::max<long long>((total + sms - 1) / sms, std::min(kMinShare, most) + kStart);
+  const bool whole = per_cta * (most + kStart) <= even + kCutTiles;
+  // CTA c starts at place c * share, counted in units or in tiles' times (a unit's start first)
   const long long share = whole ? per_cta : even;
   a.n_ctas = (int)(((whole ? units : total) + share - 1) / share);
   int c = 0;
   long long at = 0;                                          // places before the present row tile's units
   for (int k = 0; k < a.n_seq; ++k)
     for (int rt = 0, rts = attend_row_tiles(a, k); rt < rts; ++rt) {
-      const int weight = whole ? 1 : attend_key_tiles(a, k, rt);
+      const int weight = whole ? 1 : attend_key_tiles(a, k, rt) + kStart;
       for (; c < a.n_ctas && c * share < at + (long long)weight * Hkv; ++c) {
         const long long in = c * share - at;
-        a.start[c] = {k, rt, (int)(in / weight), whole ? 0 : (int)(in % weight)};
+        a.start[c] = {k, rt, (int)(in / weight), whole ? 0 : std::max(0, (int)(in % weight) - kStart)};
         a.cut |= a.start[c].j > 0;
       }
       at += (long long)weight * Hkv;
