@@ -427,7 +427,8 @@ typedef enum {
  *   WITCERT_X_SLOTS             int32 [batch][n_kv_heads][nblk] (-1 = not repaired)
  *   WITCERT_X_BLOCK_RISK        float [batch][n_q_heads][nblk] (last decode; gate enabled)
  *   WITCERT_X_V_WITNESS         fp16 [batch][len][n_kv_heads] (v_witness caches)
- * nblk = ceil(len/16).  Asynchronous on `stream`. */
+ * nblk = ceil(len/16); len is the longest sequence's.  Rows past a shorter sequence's length are zero
+ * where a paged store holds no page for them, unspecified elsewhere.  Asynchronous on `stream`. */
 witcert_status witcert_export(witcert_cache* cache, int layer, witcert_export_kind what,
                               void* dst, size_t bytes, void* stream);
 

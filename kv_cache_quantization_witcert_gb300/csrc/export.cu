@@ -9,30 +9,36 @@ namespace {
 
 enum { X_KC = 0, X_VC, X_KS, X_VS, X_VZ, X_KIVI_KS, X_KIVI_KZ, X_W, X_SLOTS, X_RISK, X_VW };
 
+// Block b of (sequence i, KV head h); null where a paged store has given the sequence no page for it
+// (the output is as long as the longest sequence, and a table entry of -1 lies before the pool).
+__device__ __forceinline__ const uint8_t* stored_block(const ExportArgs& a, int i, int h, int b) {
+  if (a.table && a.table[(size_t)i * a.nblk_max + b] < 0) return nullptr;
+  return a.blocks + block_index(a.table, a.Hkv, a.nblk_max, i, h, b) * block_bytes(a.scheme);
+}
+
 __global__ void export_kernel(const ExportArgs a, size_t n) {
   const size_t idx = (size_t)blockIdx.x * blockDim.x + threadIdx.x;
   if (idx >= n) return;
-  const int bb = block_bytes(a.scheme);
   const int nblk = (a.S + kBlk - 1) / kBlk;
   switch (a.what) {
     case X_KC:
     case X_VC: {  // [B][S][Hkv][128]
       const int c = idx % kD, h = (idx / kD) % a.Hkv, t = (idx / ((size_t)kD * a.Hkv)) % a.S;
       const int i = idx / ((size_t)kD * a.Hkv * a.S);
-      const uint8_t* bp = a.blocks + block_index(a.table, a.Hkv, a.nblk_max, i, h, t >> 4) * bb;
+      const uint8_t* bp = stored_block(a, i, h, t >> 4);
       const int r = t & 15;
       if (a.scheme == kBbox) {   // the stored bf16 values
         const int off = a.what == X_KC ? BboxLayout::KH + kbf_off(r, c) : BboxLayout::VH + vbf_off(r, c);
-        reinterpret_cast<uint16_t*>(a.dst)[idx] = *reinterpret_cast<const uint16_t*>(bp + off);
+        reinterpret_cast<uint16_t*>(a.dst)[idx] = bp ? *reinterpret_cast<const uint16_t*>(bp + off) : 0;
         break;
       }
-      uint8_t v;
-      if (a.scheme == kKivi) {
+      uint8_t v = 0;
+      if (bp && a.scheme == kKivi) {
         int off, bit;
         if (a.what == X_KC) kivi_k_pos(r, c, off, bit); else kivi_v_pos(r, c, off, bit);
         const uint32_t w = *reinterpret_cast<const uint32_t*>(bp + (a.what == X_KC ? KiviLayout::KC : KiviLayout::VC) + off);
         v = (uint8_t)((w >> bit) & 3u);
-      } else {
+      } else if (bp) {
         const int base = a.what == X_KC ? 0 : 2048;
         v = bp[base + (a.what == X_KC ? kcode_off(r, c) : vcode_off(r, c))];
         if (int8_layout(a.scheme)) v = (uint8_t)(v ^ 0x80u);    // stored biased by 128
@@ -45,12 +51,12 @@ __global__ void export_kernel(const ExportArgs a, size_t n) {
     case X_VZ: {  // [B][S][Hkv][4]
       const int G = idx % 4, h = (idx / 4) % a.Hkv, t = (idx / (4 * (size_t)a.Hkv)) % a.S;
       const int i = idx / (4 * (size_t)a.Hkv * a.S);
-      const uint8_t* bp = a.blocks + block_index(a.table, a.Hkv, a.nblk_max, i, h, t >> 4) * bb;
+      const uint8_t* bp = stored_block(a, i, h, t >> 4);
       const int r = t & 15;
-      __half v;
-      if (a.scheme == kKivi) {
+      __half v = __float2half_rn(0.f);
+      if (bp && a.scheme == kKivi) {
         v = reinterpret_cast<const __half*>(bp + KiviLayout::VP)[(r * 4 + G) * 2 + (a.what == X_VZ ? 1 : 0)];
-      } else {
+      } else if (bp) {
         v = a.what == X_KS ? reinterpret_cast<const __half*>(bp + Int8Layout::KS)[r * 4 + G]
                            : *reinterpret_cast<const __half*>(bp + Int8Layout::VS + vscale_off(r, G));
       }
@@ -61,17 +67,18 @@ __global__ void export_kernel(const ExportArgs a, size_t n) {
     case X_KIVI_KZ: {  // [B][nblk][Hkv][128]
       const int c = idx % kD, h = (idx / kD) % a.Hkv, b = (idx / ((size_t)kD * a.Hkv)) % nblk;
       const int i = idx / ((size_t)kD * a.Hkv * nblk);
-      const uint8_t* bp = a.blocks + block_index(a.table, a.Hkv, a.nblk_max, i, h, b) * bb;
+      const uint8_t* bp = stored_block(a, i, h, b);
       reinterpret_cast<__half*>(a.dst)[idx] =
-          reinterpret_cast<const __half*>(bp + KiviLayout::KP + (a.what == X_KIVI_KZ ? 256 : 0))[kivi_kparam_idx(c)];
+          bp ? reinterpret_cast<const __half*>(bp + KiviLayout::KP + (a.what == X_KIVI_KZ ? 256 : 0))[kivi_kparam_idx(c)]
+             : __float2half_rn(0.f);
       break;
     }
     case X_W: {  // [B][S][Hkv][16]
       const int b = idx % kBands, h = (idx / kBands) % a.Hkv, t = (idx / ((size_t)kBands * a.Hkv)) % a.S;
       const int i = idx / ((size_t)kBands * a.Hkv * a.S);
-      const uint8_t* bp = a.blocks + block_index(a.table, a.Hkv, a.nblk_max, i, h, t >> 4) * bb;
+      const uint8_t* bp = stored_block(a, i, h, t >> 4);
       reinterpret_cast<__half*>(a.dst)[idx] =
-          *reinterpret_cast<const __half*>(bp + witness_off(a.scheme) + wit_off(t & 15, b));
+          bp ? *reinterpret_cast<const __half*>(bp + witness_off(a.scheme) + wit_off(t & 15, b)) : __float2half_rn(0.f);
       break;
     }
     case X_SLOTS: {  // [B][Hkv][nblk]

@@ -340,3 +340,27 @@ def test_reset_clears_value_witnesses_of_the_last_block():
     assert not np.any(wv[1, 10:16])
     _, mm, _ = rg.check_decode(0, gen_q(w, 0, 0), w.delta_req)
     assert np.all(np.isfinite(mm["meter_v"]))
+
+
+@pytest.mark.parametrize("scheme", ALL_SCHEMES)
+def test_paged_export_past_a_sequences_pages(scheme):
+    """An export is as long as the longest sequence: blocks a shorter one has no page for come out
+    as zeros, blocks it has as in a contiguous cache."""
+    w = WORKLOADS["qwen_1l"].with_(batch=3, context=100, steps=1, scheme=scheme)
+    K, V = gen_kv(w, 0)
+    lens = [0, 5, 100]
+    kinds = [_lib.X_K_CODES, _lib.X_V_CODES, _lib.X_WITNESS, _lib.X_V_WITNESS]
+    kinds += [_lib.X_K_SCALES, _lib.X_V_SCALES] if scheme.startswith("int8") else []
+    kinds += [_lib.X_V_SCALES, _lib.X_V_ZEROS, _lib.X_KIVI_K_SCALE, _lib.X_KIVI_K_ZERO] if scheme == "kivi2" else []
+    out = []
+    for pages in (0, 8):
+        rg = Ragged(w, scheme, cap=112, max_pages=pages)
+        rg.write(0, list(zip(_split(K, lens), _split(V, lens))))
+        out.append([rg.gpu.export(0, k).view(torch.uint8).cpu() for k in kinds])
+    for kind, whole, paged in zip(kinds, *out):
+        blocks = kind in (_lib.X_KIVI_K_SCALE, _lib.X_KIVI_K_ZERO)
+        for i, n in enumerate(lens):
+            own, held = (n // 16, (n + 15) // 16) if blocks else (n, (n + 15) // 16 * 16)
+            assert torch.equal(paged[i, :own], whole[i, :own])
+            if kind != _lib.X_V_WITNESS:                  # kept per sequence, not in pages
+                assert not paged[i, held:].any()
