@@ -6,17 +6,22 @@
 // and more warps to hide the latency of a tile's chain (tensor memory, maximum, exponentials, tensor
 // memory), which is what bounds a step.  They agree on the row's maximum through shared memory.
 //
-// Softmax: weights 2^(s c - m + kOff) with the row's reference m in log2 units.  m follows the
-// running maximum only when that has grown by more than kGrow, so O and the sum l are rescaled
-// rarely, by the softmax threads themselves.  kOff keeps the small weights of fp16 normal: weights
-// reach 2^15 at most, and those below 2^-22 of the reference (2^-32 before they vanish) lose bits.
+// Softmax: weights 2^(s c - m + off) with the row's reference m in log2 units.  m follows the running
+// maximum only when that has grown by more than grow, so O and the sum l are rescaled rarely, by the
+// softmax threads themselves.  fp16 weights reach 2^15 at most; off keeps the small ones normal, for a
+// key's value can be zero where the weights are large: those below 2^-26 of the reference (2^-36 before
+// they vanish) lose bits (off 8, grow 7: 864 us against 882 for 2048 of 32768 tokens, but 2^-22).
+// bf16 has fp32's range, so m hardly ever moves.
 #pragma once
 #include "kernels.h"
 #include "tcgen05.cuh"
 
 namespace witcert {
 
-constexpr float kOff = 8.0f, kGrow = 7.0f;
+template <bool BF16>
+struct WeightRange {
+  static constexpr float off = BF16 ? 0.0f : 12.0f, grow = BF16 ? 40.0f : 3.0f;
+};
 constexpr uint64_t kAttendWaitNs = 2000000000ull;          // 2 s per barrier wait
 
 // A kernel of a call behind the call's earlier ones: it may start while its predecessor ends, and
@@ -239,7 +244,7 @@ __device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t tp, uint32_t 
   }
   // the partners' logits have left tensor memory when this returns: weights may overwrite them
   const float top = grp.top(fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]));
-  const bool grow = (top - m) * scale > kGrow;             // also from -inf; false while nothing is visible
+  const bool grow = (top - m) * scale > WeightRange<BF16>::grow;   // also from -inf; false while nothing is visible
   if (__any_sync(0xffffffffu, grow)) {
     const float mn = grow ? top : m, f = grow ? ex2((m - mn) * scale) : 1.0f;
     l *= f;
@@ -257,7 +262,7 @@ __device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t tp, uint32_t 
       }
     }
   }
-  const float bias = kOff - (m == -INFINITY ? 0.f : m * scale);
+  const float bias = WeightRange<BF16>::off - (m == -INFINITY ? 0.f : m * scale);
   const float2 sc2 = make_float2(scale, scale), b2 = make_float2(bias, bias);
   float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll

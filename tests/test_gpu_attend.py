@@ -134,6 +134,22 @@ def test_more_sequences_than_a_launch_takes():
     Pair("fp8_e4m3", 2, 1, lens).check([min(x, 1 + i % 40 * (i % 3)) for i, x in enumerate(lens)])
 
 
+@pytest.mark.parametrize("seed", range(24))
+def test_random_batches(seed):
+    """Lengths, chunk sizes, heads and stores at random: every kernel, cut and merge there is."""
+    rng = np.random.default_rng(seed)
+    B = int(rng.integers(1, 7))
+    hkv, grp = int(rng.integers(1, 4)), int(rng.integers(1, 9))
+    lens = [int(np.exp(rng.uniform(0, np.log(900)))) for _ in range(B)]
+    # decodes, drafts, chunks and whole prompts side by side
+    n = [min(s, int(rng.choice([0, 1, 1 + rng.integers(8), 1 + rng.integers(150), s]))) for s in lens]
+    if not any(n):
+        n[0] = 1
+    scheme = SCHEMES[seed % 5]
+    pages = int(rng.integers(2)) * (sum((s + 15) // 16 for s in lens) + 3)
+    Pair(scheme, hkv * grp, hkv, lens, seed=seed, max_pages=pages, pos_offset=int(rng.integers(2)) * 16 if scheme != "int8_dither" else 0).check(n, seed)
+
+
 @pytest.mark.parametrize("scale", [1e-3, 30.0])
 def test_flat_and_sharp_weights(scale):
     """Nearly equal weights, and one key that takes all (rescaling, weights that vanish)."""
