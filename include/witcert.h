@@ -237,9 +237,10 @@ witcert_status witcert_read(witcert_cache* cache, int layer, const int32_t* t0, 
  * witcert_decode gives at that length (KIVI2: with the blocks finished since then quantized), to
  * bf16; no meters are formed.  Products run on the tensor cores: decoded keys and values and the
  * softmax weights are rounded to fp16 (keys and values beyond 65504 saturate), for a black-box
- * cache to bf16, with fp32 sums.  Keys a query does not see have weight 0; values among the same
- * 128 tokens must be finite for that to hold.  bf16 caches only.  q, out and workspace are 32-byte aligned; workspace: device, at
- * least what witcert_attend_workspace says for the same n_tok; nothing in it is kept between calls.
+ * cache to bf16, with fp32 sums (fp16 weights below 2^-26 of a row's largest are off by at most 2^-37
+ * of it).  Keys a query does not see have weight 0; values among the same 128 tokens must be finite
+ * for that to hold.  bf16 caches only.  q, out and workspace are 32-byte aligned; workspace: device,
+ * at least what witcert_attend_workspace says for the same n_tok; nothing in it is kept between calls.
  * EINVAL on bad arguments.  Asynchronous on `stream`, after a pending gate of the layer.  A device
  * wait that runs out (2 s) leaves the rows it concerns unwritten and counts in witcert_stats'
  * device_errors. */
