@@ -143,12 +143,10 @@ witcert_status witcert_write(witcert_cache* cache, int layer, const void* K, con
  * K, V as in witcert_write; K_hat, V_hat are the tensor function's outputs f(K), f(V)
  * in the same layout and dtype.  The cache stores bf16(K_hat), bf16(V_hat) (nearest
  * even; unchanged for bf16 inputs), and the key witness w_{t,b} = ||K - bf16(K_hat)||
- * of each band, so the decode and the bound use exactly what is stored.  K_hat and V_hat
- * must be finite: the rows of a sequence's last block past its length take part in the
- * decode's P.V product with weight 0, and a non-finite value left there (by the rows'
- * occupant before a reset, or in a page that held another sequence) makes 0 x inf a NaN in
- * that later sequence's output.  EINVAL on a cache of another scheme (which takes
- * witcert_write) and as witcert_write otherwise. */
+ * of each band, so the decode and the bound use exactly what is stored.  A value that is not
+ * finite reaches the outputs of the sequence that holds it, and no other: rows past a length
+ * (dropped tokens, a slot's or a page's occupant before) take no part in a decode.  EINVAL on a
+ * cache of another scheme (which takes witcert_write) and as witcert_write otherwise. */
 witcert_status witcert_write_hat(witcert_cache* cache, int layer, const void* K, const void* V,
                                  const void* K_hat, const void* V_hat, int n_tok, void* stream);
 
@@ -215,8 +213,8 @@ witcert_status witcert_write_rope_ragged(witcert_cache* cache, int layer, const 
  * every layer if layer is -1, keeps its first lengths[i] tokens (host [batch], >= 0; a sequence that
  * is not longer stays as it is).  The next append takes the freed positions.  Pages stay with the
  * sequence until it is reset; repairs of its blocks stay.  Block risks become stale (witcert_gate
- * needs a new decode).  EINVAL for a KIVI2 cache where a finished 16-token block would reopen: its
- * exact keys are gone.  Asynchronous on `stream`. */
+ * needs a new decode).  Dropped rows take no part in later calls, whatever they hold.  EINVAL for a
+ * KIVI2 cache where a finished 16-token block would reopen: its exact keys are gone.  Asynchronous on `stream`. */
 witcert_status witcert_truncate(witcert_cache* cache, int layer, const int32_t* lengths, void* stream);
 
 /* The keys and values the cache stands for: tokens t0[i] .. t0[i] + n_tok[i] - 1 of every sequence
@@ -253,8 +251,7 @@ witcert_status witcert_attend_workspace(const witcert_cache* cache, int layer, c
 
 /* Empty sequence `seq` in every layer so the slot can serve a new request (continuous
  * batching).  Its repairs are dropped too (their slots in the exact-key pool are not
- * reused), a paged cache returns its pages to the pool, and its value witnesses are zeroed
- * (the decode weighs the rows past a length by 0, which needs finite values there).
+ * reused), a paged cache returns its pages to the pool, and its value witnesses are zeroed.
  * Asynchronous on `stream`; decodes issued after it see the sequence empty.  EINVAL if
  * seq is out of range. */
 witcert_status witcert_reset_sequence(witcert_cache* cache, int seq, void* stream);

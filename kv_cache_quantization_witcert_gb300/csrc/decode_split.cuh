@@ -117,6 +117,40 @@ __device__ __forceinline__ float sqrt_up(float x) {
   return y;
 }
 
+// Rows n .. 15 of a staged block, past the sequence's length, made zero where the decode weighs them by
+// 0: they may hold what 0 does not cancel (a dropped token's NaN values, infinite value witnesses).  Keys
+// and key witnesses need no such care: their rows end in logits and bounds of their own, which are
+// replaced.  KIVI's values are always finite.
+template <int SCHEME, bool VW>
+__device__ __forceinline__ void drop_values(uint8_t* sb, int n, int lane) {
+  using L = Lay<SCHEME>;
+  // this lane's tokens 2t, 2t + 1, 2t + 8, 2t + 9 in the order of its value operands
+  const int t = lane & 3;
+  auto kept = [&](int tok, uint32_t bits) { return tok < n ? bits : 0u; };
+  if constexpr (SCHEME == kFp8) {
+    const uint32_t m = kept(2 * t, 0xFFu) | kept(2 * t + 1, 0xFF00u) | kept(2 * t + 8, 0xFF0000u) | kept(2 * t + 9, 0xFF000000u);
+#pragma unroll 1
+    for (int j = 0; j < 4; ++j) {
+      uint4* v = reinterpret_cast<uint4*>(sb + L::VC + j * 512 + lane * 16);
+      *v = make_uint4(v->x & m, v->y & m, v->z & m, v->w & m);
+    }
+  } else if constexpr (SCHEME == kBbox) {
+    const uint32_t a = kept(2 * t, 0xFFFFu) | kept(2 * t + 1, 0xFFFF0000u), b = kept(2 * t + 8, 0xFFFFu) | kept(2 * t + 9, 0xFFFF0000u);
+#pragma unroll 1
+    for (int mt = 0; mt < 8; ++mt) {
+      uint4* v = reinterpret_cast<uint4*>(sb + L::VH + (mt * 32 + lane) * 16);
+      *v = make_uint4(v->x & a, v->y & a, v->z & b, v->w & b);
+    }
+  } else if constexpr (int8_layout(SCHEME)) {
+    if (lane < kBlk && lane >= n) {
+#pragma unroll
+      for (int G = 0; G < 4; ++G) *reinterpret_cast<uint16_t*>(sb + L::VS + vscale_off(lane, G)) = 0;
+    }
+  }
+  if (VW && lane < kBlk && lane >= n) *reinterpret_cast<uint16_t*>(sb + L::BYTES + 2 * lane) = 0;
+  __syncwarp();
+}
+
 // Packed pairs (two query heads of a lane): fp32x2 arithmetic of sm_100+.
 __device__ __forceinline__ float2 f2(float v) { return make_float2(v, v); }
 __device__ __forceinline__ float2 ex2x2(float2 v) { return make_float2(ex2(v.x), ex2(v.y)); }
@@ -715,6 +749,7 @@ __global__ void __launch_bounds__(NW * 32, MinBlocks<NW>::value) decode_split_ke
         const int tok0 = blk * kBlk + g, tok1 = tok0 + 8;
         if (tok0 >= S_blk) { lgA = f2(-INFINITY); epsA = f2(0.f); ubA = f2(0.f); }
         if (tok1 >= S_blk) { lgB = f2(-INFINITY); epsB = f2(0.f); ubB = f2(0.f); }
+        drop_values<SCHEME, VW && METER>(ring + stage * STB, S_blk - blk * kBlk, lane);
       }
 
       // ------------------------------------------------------------ online softmax + meters
