@@ -142,10 +142,10 @@ __device__ __forceinline__ void drop_values(uint8_t* sb, int n, int lane) {
       *v = make_uint4(v->x & a, v->y & a, v->z & b, v->w & b);
     }
   } else if constexpr (int8_layout(SCHEME)) {
-    if (lane < kBlk && lane >= n) {
-#pragma unroll
-      for (int G = 0; G < 4; ++G) *reinterpret_cast<uint16_t*>(sb + L::VS + vscale_off(lane, G)) = 0;
-    }
+    // word `lane` of the scales: two tokens of a group
+    const int tok = 2 * ((lane >> 1) & 3) + 8 * (lane & 1);
+    uint32_t* w = reinterpret_cast<uint32_t*>(sb + L::VS) + lane;
+    *w &= kept(tok, 0xFFFFu) | kept(tok + 1, 0xFFFF0000u);
   }
   if (VW && lane < kBlk && lane >= n) *reinterpret_cast<uint16_t*>(sb + L::BYTES + 2 * lane) = 0;
   __syncwarp();
@@ -749,7 +749,6 @@ __global__ void __launch_bounds__(NW * 32, MinBlocks<NW>::value) decode_split_ke
         const int tok0 = blk * kBlk + g, tok1 = tok0 + 8;
         if (tok0 >= S_blk) { lgA = f2(-INFINITY); epsA = f2(0.f); ubA = f2(0.f); }
         if (tok1 >= S_blk) { lgB = f2(-INFINITY); epsB = f2(0.f); ubB = f2(0.f); }
-        drop_values<SCHEME, VW && METER>(ring + stage * STB, S_blk - blk * kBlk, lane);
       }
 
       // ------------------------------------------------------------ online softmax + meters
@@ -800,6 +799,7 @@ __global__ void __launch_bounds__(NW * 32, MinBlocks<NW>::value) decode_split_ke
           for (int G = 0; G < 4; ++G) zc[G] *= scg;
         }
       }
+      if (ragged) drop_values<SCHEME, VW && METER>(ring + stage * STB, S_blk - blk * kBlk, lane);
       const float2 peA = ex2x2(dA), peB = ex2x2(dB);
       Zl = __fadd2_rn(Zl, __fadd2_rn(peA, peB));
       if (METER) {
