@@ -282,6 +282,8 @@ witcert_status witcert_reset_sequence(witcert_cache* cache, int seq, void* strea
  * with large outlier channels reach c_t near 30 and logits of tens of units, where the
  * tensor cores' fp32 accumulation of eps_t and of the logits is covered by the margin as
  * measured, not by a worst-case bound.
+ * A bound that no number holds (a witness above fp16's range, inputs that are not finite) is
+ * +inf: 1 in meter_a and meter_b, +inf in the other meters and the block risks.
  * Any meter pointer may be NULL; if all five are NULL the meter work is
  * compiled out and `out` is bit-identical to the metered run's.
  * With the gate enabled, per-16-token-block risks of the gate's tier

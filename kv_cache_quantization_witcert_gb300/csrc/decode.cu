@@ -27,9 +27,12 @@ __device__ __forceinline__ void kahan_add(float& hi, float& lo, float x) {
   hi = t;
 }
 
-// D = S / Z with the meters' margin, rounded up; D + D^2 / 2 rounded up.
+// D = S / Z with the meters' margin, rounded up; D + D^2 / 2 rounded up.  A sum that is no number (an
+// infinite term leaves inf - inf in its compensation, a weight that underflowed 0 x inf) bounds nothing
+// but +inf.
 __device__ __forceinline__ float meter_ratio(float S_hi, float S_lo, float Z_dn) {
   const float S_up = __fadd_ru(S_hi, S_lo);
+  if (!(S_up <= FLT_MAX) || isnan(Z_dn)) return INFINITY;
   if (!(S_up > 0.f) || !(Z_dn > 0.f)) return 0.f;
   return __fadd_ru(__fmul_ru(__fdiv_ru(S_up, Z_dn), kMeterMargin), kMeterFloor);
 }
@@ -147,6 +150,8 @@ __global__ void __launch_bounds__(kMergeWarps * 32) decode_merge_kernel(const De
       if (v.y > 0.f && Zdn > 0.f) {
         const float k = v.x == Mx ? 0.f : v.x - Mx;
         r = __fadd_ru(__fmul_ru(__fmul_ru(v.y, pow2_up(k)), scale), kMeterFloor);
+      } else if (isnan(v.y) || isnan(Zdn)) {
+        r = INFINITY;
       }
       ro[b] = r;
     }
