@@ -258,7 +258,7 @@ cudaError_t launch_decode(int scheme, const DecodeArgs& a0, int sm_count, cudaSt
   if (e != cudaSuccess) return e;
   if (split_stop && (e = cudaEventRecord(split_stop, st)) != cudaSuccess) return e;
   const dim3 mg(a.B * a.Hq);
-  const bool risk = a.risk_raw != nullptr && a.meter;
+  const bool risk = a.risk != nullptr && a.meter;
   if (scheme == kInt8)
     e = risk ? launch_pdl(decode_merge_kernel<true, true>, mg, dim3(kMergeWarps * 32), 0, st, pdl_allowed, a)
              : launch_pdl(decode_merge_kernel<true, false>, mg, dim3(kMergeWarps * 32), 0, st, pdl_allowed, a);

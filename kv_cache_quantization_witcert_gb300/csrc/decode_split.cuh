@@ -1081,6 +1081,7 @@ cudaError_t dispatch_combo(const DecodeArgs& a, dim3 grid, cudaStream_t st, bool
   const bool gate = a.slots != nullptr, vw = a.vwit != nullptr;
   if (!a.meter) return gate ? dispatch_nw<SCHEME, QT, false, false, true, false, PAGED>(a, grid, st, pdl, occ)
                             : dispatch_nw<SCHEME, QT, false, false, false, false, PAGED>(a, grid, st, pdl, occ);
+  if (gate && !a.risk_raw && !occ) return cudaErrorInvalidValue;   // the kernels below write block risks
   if (gate) return vw ? dispatch_nw<SCHEME, QT, true, true, true, true, PAGED>(a, grid, st, pdl, occ)
                       : dispatch_nw<SCHEME, QT, true, true, true, false, PAGED>(a, grid, st, pdl, occ);
   return vw ? dispatch_nw<SCHEME, QT, true, false, false, true, PAGED>(a, grid, st, pdl, occ)

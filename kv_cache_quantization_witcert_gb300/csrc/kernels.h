@@ -62,8 +62,8 @@ struct DecodeArgs {
   int layer;
   float kappa;               // sqrt(2 ln(2S/delta_loc)), rounded up (Tier B)
   float* part;               // [B][Hq][n_splits][kPartStride]
-  float2* risk_raw;          // [B][Hq][nblk_max] (block max in log2 units, risk sum), or null
-  float* risk;               // [B][Hq][nblk_max] normalized block risk, or null
+  float2* risk_raw;          // [B][Hq][nblk_max] (block max in log2 units, risk sum): metered decodes with slots
+  float* risk;               // [B][Hq][nblk_max] normalized block risk, or null: the merge keeps none
   float* out;                // [B][Hq][128]
   float *meter_a, *meter_b, *raw_a, *raw_b;
   const __half* vwit;        // layer base [B][Hkv][nblk_max][16] value witnesses, or null

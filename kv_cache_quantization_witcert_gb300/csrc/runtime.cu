@@ -1101,6 +1101,7 @@ witcert_status witcert_decode_partial(witcert_cache* c, int layer, const void* q
   fill_decode(c, layer, q, delta_req, true, s_total, a);
   a.part = c->part;
   a.part_out = part;
+  a.risk_raw = c->risk_raw;      // a gated cache's split kernel writes block risks; the merge keeps none (no a.risk)
   cudaError_t e = launch_decode(c->scheme, a, c->sm_count, st, nullptr, nullptr, c->overlap && !waited);
   if (e != cudaSuccess) return cuda_fail(e, "decode launch");
   c->last_write_layer = -1;
