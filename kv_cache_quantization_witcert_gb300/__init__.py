@@ -30,6 +30,21 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+def _empty(stream, shape, dtype, device="cuda"):
+    """An output or workspace of a call on `stream` (None: the current stream).  It comes from that
+    stream's memory: a block freed on the current stream may still be in use by work queued there, which
+    another stream does not wait for.  It may be used on the current stream too (ordering is the caller's)."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream)
+    here = torch.cuda.current_stream(stream.device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(here)
+    return t
+
+
 def _extent(t, i):
     """Extent i of a tensor argument, or None when it has none (_need then rejects it)."""
     return t.shape[i] if isinstance(t, torch.Tensor) and t.dim() > i else None
@@ -110,11 +125,11 @@ def _need_rope(rope, head_dim):
         raise ValueError(f"rope turns {rope.rotary_dim} channels of a head of {head_dim}")
 
 
-def _rope_tensor(name, x, y, n_tok, like):
+def _rope_tensor(name, x, y, n_tok, like, stream=None):
     """A tensor [n_tok, heads, head_dim] with adjacent channels and its output (None: a new contiguous
     one): the output and what witcert_rope takes."""
     if isinstance(x, torch.Tensor) and y is None:
-        y = x.new_empty(x.shape)
+        y = _empty(stream if x.is_cuda else None, x.shape, x.dtype, x.device)
     for nm, t in ((name, x), (name + "_out", y)):
         if not isinstance(t, torch.Tensor):
             raise ValueError(f"{nm} must be a torch.Tensor, got {type(t).__name__}")
@@ -146,9 +161,9 @@ def witcert_rope(rope, positions, q, k=None, q_out=None, k_out=None, inverse=Fal
     n_tok, _, head_dim = q.shape
     _need_rope(rope, head_dim)
     _need(("positions", positions, torch.int64, (n_tok,)))
-    q_out, tq = _rope_tensor("q", q, q_out, n_tok, q)
+    q_out, tq = _rope_tensor("q", q, q_out, n_tok, q, stream)
     if k is not None:
-        k_out, tk = _rope_tensor("k", k, k_out, n_tok, q)
+        k_out, tk = _rope_tensor("k", k, k_out, n_tok, q, stream)
     elif k_out is not None:
         raise ValueError("k_out needs k")
     check(load().witcert_rope(rope._ref, BF16 if q.dtype == torch.bfloat16 else F32, head_dim, n_tok,
@@ -273,12 +288,9 @@ class Cache:
         n = ctypes.c_size_t()
         check(load().witcert_attend_workspace(self._h, layer, arr, ctypes.byref(n)), "witcert_attend_workspace")
         _need(("q", q, torch.bfloat16, (sum(counts), self.cfg.n_q_heads, 128)))
-        out = torch.empty_like(q)
-        workspace = torch.empty(n.value, dtype=torch.uint8, device=q.device)
+        out = _empty(stream, q.shape, q.dtype, q.device)
+        workspace = _empty(stream, n.value, torch.uint8, q.device)
         self._attend(layer, q, arr, out, workspace, stream)
-        if stream is not None:
-            workspace.record_stream(stream)
-            out.record_stream(stream)
         return out
 
     def witcert_write_ragged(self, layer, K, V, n_tok, K_hat=None, V_hat=None, stream=None):
@@ -320,7 +332,7 @@ class Cache:
 
     def decode_partial(self, layer, q, delta_req, s_total, stream=None):
         """This shard's per-cell records [B, Hq, 136] (see witcert_decode_partial)."""
-        part = torch.empty((q.shape[0], q.shape[1], PART_STRIDE), dtype=torch.float32, device=q.device)
+        part = _empty(stream, (q.shape[0], q.shape[1], PART_STRIDE), torch.float32, q.device)
         self.witcert_decode_partial(layer, q, delta_req, s_total, part, stream=stream)
         return part
 
@@ -371,11 +383,11 @@ class Cache:
     # ------------------------------------------------------------------ conveniences (allocation + the calls above)
     def decode(self, layer, q, delta_req, meters=True, stream=None):
         B, Hq = q.shape[0], q.shape[1]
-        out = torch.empty((B, Hq, 128), dtype=torch.float32, device=q.device)
+        out = _empty(stream, (B, Hq, 128), torch.float32, q.device)
         if not meters:
             self.witcert_decode(layer, q, delta_req, out, stream=stream)
             return out, None
-        m = torch.empty((5, B, Hq), dtype=torch.float32, device=q.device)
+        m = _empty(stream, (5, B, Hq), torch.float32, q.device)
         self.witcert_decode(layer, q, delta_req, out, m[0], m[1], m[2], m[3], m[4] if self.v_witness else None,
                             stream=stream)
         meters = {"meter_a": m[0], "meter_b": m[1], "raw_a": m[2], "raw_b": m[3]}
@@ -388,12 +400,8 @@ class Cache:
         counts, arr = self._counts("n_tok", n_tok)
         start = None if t0 is None else self._counts("t0", t0)[1]
         shape = (max(sum(counts), 0), self.cfg.n_kv_heads, 128)      # the library refuses negative counts
-        K = torch.empty(shape, dtype=self.dtype, device="cuda")
-        V = torch.empty(shape, dtype=self.dtype, device="cuda")
+        K, V = _empty(stream, shape, self.dtype), _empty(stream, shape, self.dtype)
         self._read(layer, start, arr, K, V, stream)
-        if stream is not None:
-            K.record_stream(stream)
-            V.record_stream(stream)
         return K, V
 
     def export(self, layer, what, stream=None):
@@ -412,7 +420,7 @@ class Cache:
             _lib.X_BLOCK_RISK: ((B, Hq, nblk), torch.float32), _lib.X_V_WITNESS: ((B, S, Hkv), torch.float16),
         }
         shape, dt = shapes[what]
-        dst = torch.empty(shape, dtype=dt, device=dev)
+        dst = _empty(stream, shape, dt, dev)
         if dst.numel():
             self.witcert_export(layer, what, dst, stream=stream)
         return dst
@@ -427,9 +435,9 @@ def witcert_merge_partials(parts, scheme, out=None, meters=True, stream=None):
     _need(("parts", parts, torch.float32, (None, None, None, PART_STRIDE)))
     B, Hq, n = parts.shape[0], parts.shape[1], parts.shape[2]
     if out is None:
-        out = torch.empty((B, Hq, 128), dtype=torch.float32, device=parts.device)
+        out = _empty(stream, (B, Hq, 128), torch.float32, parts.device)
     _need(("out", out, torch.float32, (B, Hq, 128)))
-    m = torch.empty((5, B, Hq), dtype=torch.float32, device=parts.device) if meters else None
+    m = _empty(stream, (5, B, Hq), torch.float32, parts.device) if meters else None
     ptrs = tuple(_ptr(m[k]) for k in range(5)) if meters else (None,) * 5
     check(load().witcert_merge_partials(_ptr(parts), n, B, Hq, SCHEMES[scheme] if isinstance(scheme, str) else scheme,
                                         _ptr(out), *ptrs, _stream_ptr(stream)), "witcert_merge_partials")
@@ -445,7 +453,7 @@ def witcert_gate_select(risk, n_kv_heads, tau, repaired=None, selected=None, str
     B, Hq, nblk = risk.shape
     _need(("repaired", repaired, torch.uint8, (B, n_kv_heads, nblk), True))
     if selected is None:
-        selected = torch.empty((B, n_kv_heads, nblk // 32 + 1), dtype=torch.int32, device=risk.device)
+        selected = _empty(stream, (B, n_kv_heads, nblk // 32 + 1), torch.int32, risk.device)
     _need(("selected", selected, torch.int32, (B, n_kv_heads, nblk // 32 + 1)))
     check(load().witcert_gate_select(_ptr(risk), _ptr(repaired), B, Hq, n_kv_heads, nblk, float(tau), _ptr(selected),
                                      _stream_ptr(stream)), "witcert_gate_select")
@@ -469,7 +477,7 @@ def witcert_wait_selftest(limit_ns, stream=None):
 def witcert_dither(seed, layer, kv_head, t0, n, tensor, out=None, stream=None):
     """Device dither xi [n, 128] float32 (see witcert_dither in include/witcert.h)."""
     if out is None:
-        out = torch.empty((n, 128), dtype=torch.float32, device="cuda")
+        out = _empty(stream, (n, 128), torch.float32)
     _need(("out", out, torch.float32, (n, 128)))
     check(load().witcert_dither(seed, layer, kv_head, t0, n, tensor, _ptr(out), _stream_ptr(stream)),
           "witcert_dither")
