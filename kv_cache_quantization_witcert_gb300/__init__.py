@@ -115,7 +115,11 @@ class Rope:
         self.rotary_dim, self.interleaved = rotary_dim, bool(interleaved)
         self._cfg = _lib.witcert_rope_config(rotary_dim, int(self.interleaved), self.scale,
                                              (ctypes.c_double * 128)(*self.freq))
-        self._ref = ctypes.addressof(self._cfg)
+
+    @property
+    def _ref(self):
+        """Where this plan's own configuration lies (a copy has its own)."""
+        return ctypes.addressof(self._cfg)
 
 
 def _need_rope(rope, head_dim):
