@@ -226,6 +226,8 @@ class Cache:
         batch = self.cfg.batch
         if len(counts) != batch:
             raise ValueError(f"{name} needs one count per sequence ({batch}), got {len(counts)}")
+        if counts and not (-0x80000000 <= min(counts) and max(counts) <= 0x7FFFFFFF):
+            raise ValueError(f"{name} must fit 32 bits, got {counts}")
         return counts, (ctypes.c_int32 * batch)(*counts)
 
     def witcert_write_rope(self, layer, K, V, rope, K_hat=None, V_hat=None, stream=None):
