@@ -890,6 +890,8 @@ __global__ void __launch_bounds__(32) write_kivi_k_kernel(const WriteArgs a, con
       __syncwarp();
       return;
     }
+    // the keys of a repaired block (truncated and filled anew) are exact: no witness
+    const bool repaired = a.slots && a.slots[(size_t)sh * a.nblk_max + blk] >= 0;
     float x[16][4];
 #pragma unroll
     for (int r = 0; r < kBlk; ++r) {
@@ -938,11 +940,11 @@ __global__ void __launch_bounds__(32) write_kivi_k_kernel(const WriteArgs a, con
         kivi_k_pos(r, 4 * lane + e, off, bit);
         if (code) atomicOr(&img[off / 4], (unsigned int)code << bit);
       }
-      if (!store_witness_df(bp + KiviLayout::W, r, rdf, err, lane, false)) {
+      if (!store_witness_df(bp + KiviLayout::W, r, rdf, err, lane, repaired)) {
         double res[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) res[e] = (double)x[r][e] - ((double)zr[e] + (double)sc[e] * (double)codes[e]);
-        store_witness(bp + KiviLayout::W, r, res, lane, false);
+        store_witness(bp + KiviLayout::W, r, res, lane, repaired);
       }
     }
     __syncwarp();
