@@ -167,8 +167,9 @@ witcert_status witcert_write_ragged(witcert_cache* cache, int layer, const void*
 /* Rotary positions (Su et al., "RoFormer", 2021).  Pair p of a head's first rotary_dim channels,
  * channels (p, p + rotary_dim/2) or, interleaved, (2p, 2p + 1), turns by position x freq[p] radians
  * and is multiplied by scale; later channels pass unchanged (and unscaled).  Scaled frequencies for
- * long contexts are the caller's freq (the Python binding's Rope fills it).  Angles are exact to the
- * rounding of freq at any 64-bit position. */
+ * long contexts are the caller's freq (the Python binding's Rope fills it).  freq may be of either sign
+ * and is taken as it stands: the angle at a 64-bit position is position x freq to within |position| x
+ * 2^-65 turns, and its sine and cosine are formed in fp32. */
 typedef struct {
   int rotary_dim;            /* a multiple of 8, at most the head dimension */
   int interleaved;

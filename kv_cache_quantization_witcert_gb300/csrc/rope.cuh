@@ -1,9 +1,9 @@
 // Rotary positions: shared by the standalone kernel (rope.cu) and the rotating cache writers.
 //
 // Pair p of a head's first `rot` channels turns by pos f_p radians.  The angle is kept as a
-// fraction of a turn in 64-bit fixed point, turn_p = f_p / (2 pi) mod 1 in units of 2^-64, so
-// pos turn_p, wrapped by the integer product, is the reduced angle of any 64-bit position with
-// the error of f_p alone (no fp64, no table of positions).  The nearest quarter turn is taken
+// fraction of a turn in 64-bit fixed point, turn_p = f_p / (2 pi) mod 1 to the nearest multiple of
+// 2^-64, so pos turn_p, wrapped by the integer product, is the reduced angle of any 64-bit position to
+// within |pos| 2^-65 turns (no fp64, no table of positions).  The nearest quarter turn is taken
 // off before the remainder (at most 1/8 turn) becomes fp32, which leaves 2^-27 half turns.
 #pragma once
 #include "common.cuh"

@@ -132,6 +132,22 @@ bool order_after_gate(witcert_cache* c, int layer, cudaStream_t st) {
   return true;
 }
 
+// Turns per position of a frequency (see rope.cuh): f / (2 pi) mod 1 in units of 2^-64, to the nearest.
+// 1 / (2 pi) is the sum of two doubles, and the products that are split further are fma results, which no
+// compiler fuses with what follows.
+uint64_t turns_of(double f) {
+  constexpr double kHi = 0x1.45f306dc9c883p-3, kLo = -0x1.6b01ec5417056p-57;
+  const double a = std::fabs(f), hi = std::fma(a, kHi, 0.0);
+  double lo = std::fma(a, kLo, std::fma(a, kHi, -hi));       // hi + lo = |f| / (2 pi) to 2^-105 of it
+  lo -= std::nearbyint(lo);                                  // whole turns (only of enormous frequencies)
+  const double up = (hi - std::floor(hi)) * 0x1p64;          // exact, below 2^64: hi >= 0
+  const uint64_t whole = (uint64_t)up;
+  double rest = std::nearbyint((up - (double)whole) + lo * 0x1p64);
+  if (rest >= 0x1p63) rest -= 0x1p64;
+  const uint64_t t = whole + (uint64_t)(int64_t)rest;
+  return f < 0.0 ? 0 - t : t;
+}
+
 // Checks a rotation and converts its frequencies to turns (see rope.cuh).
 witcert_status rope_turns(const witcert_rope_config* rope, int head_dim, uint64_t* turn, float* gain) {
   if (!rope) return fail(WITCERT_EINVAL, "rope must not be NULL");
@@ -141,8 +157,7 @@ witcert_status rope_turns(const witcert_rope_config* rope, int head_dim, uint64_
   for (int p = 0; p < rope->rotary_dim / 2; ++p) {
     const double f = rope->freq[p];
     if (!std::isfinite(f)) return fail(WITCERT_EINVAL, "frequency %d of the rotation is not finite", p);
-    const double t = f * 0.15915494309189535;                // turns per position: f / (2 pi)
-    turn[p] = (uint64_t)std::ldexp(t - std::floor(t), 64);   // the fraction is below 1: no overflow
+    turn[p] = turns_of(f);
   }
   *gain = (float)rope->scale;
   return WITCERT_OK;
