@@ -173,7 +173,7 @@ witcert_status witcert_write_ragged(witcert_cache* cache, int layer, const void*
 typedef struct {
   int rotary_dim;            /* a multiple of 8, at most the head dimension */
   int interleaved;
-  double scale;
+  double scale;              /* finite as a float */
   double freq[128];          /* the first rotary_dim / 2 are used; finite */
 } witcert_rope_config;
 

@@ -153,7 +153,7 @@ witcert_status rope_turns(const witcert_rope_config* rope, int head_dim, uint64_
   if (!rope) return fail(WITCERT_EINVAL, "rope must not be NULL");
   if (rope->rotary_dim < 8 || rope->rotary_dim % 8 || rope->rotary_dim > head_dim)
     return fail(WITCERT_EINVAL, "rotary_dim must be a multiple of 8 in [8, %d] (got %d)", head_dim, rope->rotary_dim);
-  if (!std::isfinite(rope->scale)) return fail(WITCERT_EINVAL, "the rotation's scale must be finite");
+  if (!std::isfinite((float)rope->scale)) return fail(WITCERT_EINVAL, "the rotation's scale must be finite in fp32");
   for (int p = 0; p < rope->rotary_dim / 2; ++p) {
     const double f = rope->freq[p];
     if (!std::isfinite(f)) return fail(WITCERT_EINVAL, "frequency %d of the rotation is not finite", p);
