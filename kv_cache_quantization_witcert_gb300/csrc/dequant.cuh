@@ -17,16 +17,16 @@ constexpr int kXsPitch = 36;                     // floats per token: value dith
 constexpr int kXsFloats = kBlk * kXsPitch;       // scratch of one warp (dithered store only)
 
 // Integer to float by placing bits, without conversions (which share a pipe with the dither's XORs):
-// 2^23 + byte minus 2^23 + 128 is the code; 1 + 2^-23 m, m the upper 23 random bits, taken from 1.5 is
-// -xi to within 2^-24, less than the rounding of code - xi that follows.
+// 2^23 + byte minus 2^23 + 128 is the code.  m, the upper 24 random bits, read as a float is m 2^-149
+// (numbers below 2^-125 are evenly spaced, subnormal or not), so one FMA gives -xi = 1/2 - m 2^-24, exact.
 __device__ __forceinline__ float code_i8(uint32_t w, int e) {
   return __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7440u | (uint32_t)e)) - 8388736.0f;
 }
-__device__ __forceinline__ float neg_xi23(uint32_t u) { return 1.5f - __uint_as_float(__funnelshift_r(u, 0x7Fu, 9)); }
-__device__ __forceinline__ float4 neg_dither4_23(const StoreArgs& s, int h, int t, int quad, int tensor) {
+__device__ __forceinline__ float neg_xi24(uint32_t u) { return __fmaf_rn(__uint_as_float(u >> 8), -0x1p125f, 0.5f); }
+__device__ __forceinline__ float4 neg_dither4_24(const StoreArgs& s, int h, int t, int quad, int tensor) {
   const uint4 u = philox4x32_10_rk(make_uint4((uint32_t)t, (uint32_t)quad | ((uint32_t)tensor << 16),
                                               (uint32_t)h | ((uint32_t)s.layer << 16), 0u), s.rk0, s.rk1);
-  return make_float4(neg_xi23(u.x), neg_xi23(u.y), neg_xi23(u.z), neg_xi23(u.w));
+  return make_float4(neg_xi24(u.x), neg_xi24(u.y), neg_xi24(u.z), neg_xi24(u.w));
 }
 __device__ __forceinline__ void e4m3x4(uint32_t w, float (&x)[4]) {
   const float2 lo = __half22float2(bits_h2(e4m3x2_lo(w))), hi = __half22float2(bits_h2(e4m3x2_hi(w)));
@@ -52,7 +52,7 @@ __device__ __forceinline__ void block_keys(const StoreArgs& s, const uint8_t* bp
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         float4 nx = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (SCH == kInt8) nx = neg_dither4_23(s, h, tb + g + 8 * r, 8 * j + 4 * m + t, 0);
+        if (SCH == kInt8) nx = neg_dither4_24(s, h, tb + g + 8 * r, 8 * j + 4 * m + t, 0);
         const float n4[4] = {nx.x, nx.y, nx.z, nx.w};
         const uint32_t c = word_of(w, 2 * m + r);
 #pragma unroll
@@ -136,7 +136,7 @@ __device__ __forceinline__ void block_values(const StoreArgs& s, const uint8_t* 
       for (int k = 0; k < 4; ++k) {
         const int r = 4 * k + (lane >> 3), quad = lane & 7;
         *reinterpret_cast<float4*>(xs + r * kXsPitch + quad * 4) =
-            neg_dither4_23(s, h, tb + r, 8 * j + quad, 1);
+            neg_dither4_24(s, h, tb + r, 8 * j + quad, 1);
       }
       __syncwarp();
     }
