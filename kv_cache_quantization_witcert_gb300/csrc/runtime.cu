@@ -10,7 +10,9 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
-#include <string>
+#include <exception>
+#include <memory>
+#include <new>
 #include <thread>
 #include <vector>
 
@@ -22,21 +24,26 @@ using namespace witcert;
 
 namespace {
 
-thread_local std::string g_err;
+thread_local char g_err[512];          // no string: a message is also left when host memory ran out
 
 witcert_status fail(witcert_status s, const char* fmt, ...) {
-  char buf[512];
+  char buf[sizeof g_err];              // an argument may be the present message
   va_list ap;
   va_start(ap, fmt);
   vsnprintf(buf, sizeof buf, fmt, ap);
   va_end(ap);
-  g_err = buf;
+  memcpy(g_err, buf, sizeof buf);
   return s;
 }
 witcert_status cuda_fail(cudaError_t e, const char* where) {
   return fail(e == cudaErrorMemoryAllocation ? WITCERT_ENOMEM : WITCERT_ECUDA, "%s: %s", where, cudaGetErrorString(e));
 }
-void ok() { g_err.clear(); }
+void ok() { g_err[0] = 0; }
+
+// Ends a C entry whose body allocates host memory: nothing throws across the ABI.
+#define WITCERT_NO_THROW                                                                        \
+  catch (const std::bad_alloc&) { return fail(WITCERT_ENOMEM, "host allocation failed"); }      \
+  catch (const std::exception& e) { return fail(WITCERT_EINVAL, "%s", e.what()); }
 
 struct ProfPair { cudaEvent_t a, b; };
 
@@ -187,11 +194,11 @@ void collect_profile(witcert_cache* c) {
 
 extern "C" {
 
-const char* witcert_last_error(void) { return g_err.c_str(); }
+const char* witcert_last_error(void) { return g_err; }
 
 static int auto_splits(const witcert_cache* c, int nblk, bool meter, int cap);
 
-witcert_status witcert_create(const witcert_config* cfg, witcert_cache** out) {
+witcert_status witcert_create(const witcert_config* cfg, witcert_cache** out) try {
   if (!cfg || !out) return fail(WITCERT_EINVAL, "NULL argument");
   *out = nullptr;
   const witcert_config& f = *cfg;
@@ -212,12 +219,19 @@ witcert_status witcert_create(const witcert_config* cfg, witcert_cache** out) {
     return fail(WITCERT_EINVAL, "with the gate enabled max_tokens must be at most %d (the gate ranks up to %d blocks)",
                 gate_max_blocks() * kBlk, gate_max_blocks());
 
-  auto* c = new (std::nothrow) witcert_cache();
-  if (!c) return fail(WITCERT_ENOMEM, "host allocation failed");
+  std::unique_ptr<witcert_cache, void (*)(witcert_cache*)> owner(new witcert_cache(), [](witcert_cache* x) { free_all(x); delete x; });
+  witcert_cache* c = owner.get();
   c->cfg = f;
+  c->len.assign(f.n_layers, 0);
+  c->slen.assign(f.n_layers, std::vector<int>(f.batch, 0));
+  c->write_gen.assign(f.n_layers, 0);
+  c->risk_gen.assign(f.n_layers, ~uint64_t(0));
+  c->gate_done.assign(f.n_layers, nullptr);
+  c->gate_pending.assign(f.n_layers, 0);
+  c->backing_lost.assign(f.n_layers, 0);
   cudaError_t e = cudaGetDevice(&c->device);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&c->sm_count, cudaDevAttrMultiProcessorCount, c->device);
-  if (e != cudaSuccess) { delete c; return cuda_fail(e, "device query"); }
+  if (e != cudaSuccess) return cuda_fail(e, "device query");
   c->scheme = (int)f.scheme;
   c->bblk = block_bytes(c->scheme);
   c->nblk_max = (f.max_tokens + kBlk - 1) / kBlk;
@@ -226,17 +240,10 @@ witcert_status witcert_create(const witcert_config* cfg, witcert_cache** out) {
   const int auto_on = auto_splits(c, c->nblk_max, true, 0), auto_off = auto_splits(c, c->nblk_max, false, 0);
   const int auto_max = auto_on > auto_off ? auto_on : auto_off;
   c->max_splits = f.n_splits > auto_max ? f.n_splits : auto_max;
-  c->len.assign(f.n_layers, 0);
-  c->slen.assign(f.n_layers, std::vector<int>(f.batch, 0));
-  c->write_gen.assign(f.n_layers, 0);
-  c->risk_gen.assign(f.n_layers, ~uint64_t(0));
-  c->gate_done.assign(f.n_layers, nullptr);
-  c->gate_pending.assign(f.n_layers, 0);
-  c->backing_lost.assign(f.n_layers, 0);
   const size_t L = f.n_layers, cells = (size_t)f.batch * f.n_q_heads;
   const bool gate = f.max_repair_blocks > 0;
 
-#define TRY(x, what) do { e = (x); if (e != cudaSuccess) { free_all(c); delete c; return cuda_fail(e, what); } } while (0)
+#define TRY(x, what) do { e = (x); if (e != cudaSuccess) return cuda_fail(e, what); } while (0)
   TRY(dalloc(&c->blocks, L * c->layer_blocks), "allocating the block store");
   if (c->scheme == kKivi) TRY(dalloc(&c->kivi_tail, L * layer_rows(c) * kBlk * kD * sizeof(float)), "allocating the KIVI tail");
   if (f.v_witness) TRY(dalloc(&c->vwit, L * vwit_layer(c) * sizeof(__half)), "allocating value witnesses");
@@ -271,11 +278,11 @@ witcert_status witcert_create(const witcert_config* cfg, witcert_cache** out) {
   }
 #undef TRY
   e = cudaDeviceSynchronize();
-  if (e != cudaSuccess) { free_all(c); delete c; return cuda_fail(e, "create"); }
-  *out = c;
+  if (e != cudaSuccess) return cuda_fail(e, "create");
+  *out = owner.release();
   ok();
   return WITCERT_OK;
-}
+} WITCERT_NO_THROW
 
 witcert_status witcert_destroy(witcert_cache* c) {
   if (!c) return fail(WITCERT_EINVAL, "cache is NULL");
@@ -357,6 +364,9 @@ static cudaError_t push_lengths(witcert_cache* c, const std::vector<std::pair<in
 static witcert_status take_pages(witcert_cache* c, int layer, const std::vector<int>& n,
                                  std::vector<std::pair<int, int>>& upd) {
   if (!c->table) return WITCERT_OK;
+  size_t most = 0;
+  for (int i = 0; i < c->cfg.batch; ++i) most += n[i] > 0 ? n[i] / kBlk + 2 : 0;
+  upd.reserve(std::min(most, c->free_pages.size()));           // no allocation once pages are being taken
   for (int i = 0; i < c->cfg.batch; ++i) {
     if (n[i] == 0) continue;
     const int t0 = c->slen[layer][i];
@@ -529,41 +539,41 @@ static witcert_status write_impl(witcert_cache* c, int layer, const void* K, con
   return WITCERT_OK;
 }
 
-witcert_status witcert_write(witcert_cache* c, int layer, const void* K, const void* V, int n_tok, void* stream) {
+witcert_status witcert_write(witcert_cache* c, int layer, const void* K, const void* V, int n_tok, void* stream) try {
   if (c && c->scheme == kBbox) return fail(WITCERT_EINVAL, "a black-box cache is written with witcert_write_hat");
   if (n_tok < 0) return fail(WITCERT_EINVAL, "n_tok must be >= 0");
   return write_impl(c, layer, K, V, nullptr, nullptr, nullptr, n_tok, nullptr, stream);
-}
+} WITCERT_NO_THROW
 
 witcert_status witcert_write_hat(witcert_cache* c, int layer, const void* K, const void* V, const void* K_hat,
-                                 const void* V_hat, int n_tok, void* stream) {
+                                 const void* V_hat, int n_tok, void* stream) try {
   if (c && c->scheme != kBbox) return fail(WITCERT_EINVAL, "witcert_write_hat needs a WITCERT_BLACKBOX cache");
   if (n_tok < 0) return fail(WITCERT_EINVAL, "n_tok must be >= 0");
   return write_impl(c, layer, K, V, K_hat, V_hat, nullptr, n_tok, nullptr, stream);
-}
+} WITCERT_NO_THROW
 
 witcert_status witcert_write_ragged(witcert_cache* c, int layer, const void* K, const void* V, const void* K_hat,
-                                    const void* V_hat, const int32_t* n_tok, void* stream) {
+                                    const void* V_hat, const int32_t* n_tok, void* stream) try {
   if (!c || !n_tok) return fail(WITCERT_EINVAL, "cache and n_tok must not be NULL");
   if (c->scheme != kBbox && (K_hat || V_hat)) return fail(WITCERT_EINVAL, "K_hat and V_hat belong to black-box caches");
   return write_impl(c, layer, K, V, K_hat, V_hat, n_tok, 0, nullptr, stream);
-}
+} WITCERT_NO_THROW
 
 witcert_status witcert_write_rope(witcert_cache* c, int layer, const void* K, const void* V, const void* K_hat,
-                                  const void* V_hat, int n_tok, const witcert_rope_config* rope, void* stream) {
+                                  const void* V_hat, int n_tok, const witcert_rope_config* rope, void* stream) try {
   if (!c || !rope) return fail(WITCERT_EINVAL, "cache and rope must not be NULL");
   if (n_tok < 0) return fail(WITCERT_EINVAL, "n_tok must be >= 0");
   if (c->scheme != kBbox && (K_hat || V_hat)) return fail(WITCERT_EINVAL, "K_hat and V_hat belong to black-box caches");
   return write_impl(c, layer, K, V, K_hat, V_hat, nullptr, n_tok, rope, stream);
-}
+} WITCERT_NO_THROW
 
 witcert_status witcert_write_rope_ragged(witcert_cache* c, int layer, const void* K, const void* V, const void* K_hat,
                                          const void* V_hat, const int32_t* n_tok, const witcert_rope_config* rope,
-                                         void* stream) {
+                                         void* stream) try {
   if (!c || !n_tok || !rope) return fail(WITCERT_EINVAL, "cache, n_tok and rope must not be NULL");
   if (c->scheme != kBbox && (K_hat || V_hat)) return fail(WITCERT_EINVAL, "K_hat and V_hat belong to black-box caches");
   return write_impl(c, layer, K, V, K_hat, V_hat, n_tok, 0, rope, stream);
-}
+} WITCERT_NO_THROW
 
 witcert_status witcert_rope(const witcert_rope_config* rope, witcert_dtype dtype, int head_dim, int n_tok,
                             const int64_t* positions, const witcert_rope_tensor* q, const witcert_rope_tensor* k,
@@ -599,19 +609,20 @@ witcert_status witcert_rope(const witcert_rope_config* rope, witcert_dtype dtype
   return WITCERT_OK;
 }
 
-witcert_status witcert_reset_sequence(witcert_cache* c, int seq, void* stream) {
+witcert_status witcert_reset_sequence(witcert_cache* c, int seq, void* stream) try {
   if (!c) return fail(WITCERT_EINVAL, "cache is NULL");
   if (seq < 0 || seq >= c->cfg.batch) return fail(WITCERT_EINVAL, "sequence %d out of range [0, %d)", seq, c->cfg.batch);
   auto st = static_cast<cudaStream_t>(stream);
+  // host memory first: nothing may fail between what the device and what the host is told
+  std::vector<std::pair<int, int>> upd, freed;
+  for (int l = 0; l < c->cfg.n_layers; ++l) upd.emplace_back(l * c->cfg.batch + seq, 0);
+  if (c->table) freed.reserve(c->nblk_max);
   bool waited = false;
   for (int l = 0; l < c->cfg.n_layers; ++l) waited |= order_after_gate(c, l, st);
   bool pdl = c->overlap && !waited;
   cudaError_t e = enter_ragged(c, st, pdl);
-  std::vector<std::pair<int, int>> upd;
-  for (int l = 0; l < c->cfg.n_layers; ++l) upd.emplace_back(l * c->cfg.batch + seq, 0);
   if (e == cudaSuccess) e = push_lengths(c, upd, st, pdl);
   if (c->table && e == cudaSuccess) {       // its pages go back to the pool
-    std::vector<std::pair<int, int>> freed;
     for (int b = 0; b < c->nblk_max; ++b) {
       int32_t& pg = c->table_host[(size_t)seq * c->nblk_max + b];
       if (pg < 0) continue;
@@ -641,9 +652,9 @@ witcert_status witcert_reset_sequence(witcert_cache* c, int seq, void* stream) {
   c->lengths_last = true;
   ok();
   return WITCERT_OK;
-}
+} WITCERT_NO_THROW
 
-witcert_status witcert_truncate(witcert_cache* c, int layer, const int32_t* lengths, void* stream) {
+witcert_status witcert_truncate(witcert_cache* c, int layer, const int32_t* lengths, void* stream) try {
   if (!c || !lengths) return fail(WITCERT_EINVAL, "cache and lengths must not be NULL");
   if (layer != -1)
     if (witcert_status s = check_layer(c, layer)) return s;
@@ -692,7 +703,7 @@ witcert_status witcert_truncate(witcert_cache* c, int layer, const int32_t* leng
   }
   ok();
   return WITCERT_OK;
-}
+} WITCERT_NO_THROW
 
 // The layer's store as the kernels that expand it read it.
 static StoreArgs store_args(const witcert_cache* c, int layer) {
@@ -918,7 +929,7 @@ static witcert_status check_attend(const witcert_cache* c, int layer, const int3
   return WITCERT_OK;
 }
 
-witcert_status witcert_attend_workspace(const witcert_cache* c, int layer, const int32_t* n_tok, size_t* bytes) {
+witcert_status witcert_attend_workspace(const witcert_cache* c, int layer, const int32_t* n_tok, size_t* bytes) try {
   long long rows = 0;
   if (witcert_status s = check_attend(c, layer, n_tok, rows)) return s;
   if (!bytes) return fail(WITCERT_EINVAL, "bytes must not be NULL");
@@ -927,10 +938,10 @@ witcert_status witcert_attend_workspace(const witcert_cache* c, int layer, const
   *bytes = plan.bytes();
   ok();
   return WITCERT_OK;
-}
+} WITCERT_NO_THROW
 
 witcert_status witcert_attend(witcert_cache* c, int layer, const void* q, const int32_t* n_tok, void* out,
-                              void* workspace, size_t workspace_bytes, void* stream) {
+                              void* workspace, size_t workspace_bytes, void* stream) try {
   long long rows = 0;
   if (witcert_status s = check_attend(c, layer, n_tok, rows)) return s;
   if (rows == 0) { ok(); return WITCERT_OK; }
@@ -962,7 +973,7 @@ witcert_status witcert_attend(witcert_cache* c, int layer, const void* q, const 
   c->lengths_last = false;
   ok();
   return WITCERT_OK;
-}
+} WITCERT_NO_THROW
 
 // Automatic split count for a decode of nblk blocks: sized by how many split-kernel CTAs of
 // this configuration fit on an SM, and never above the scratch sized at create time.
@@ -1019,7 +1030,7 @@ static void fill_decode(witcert_cache* c, int layer, const void* q, double delta
 
 witcert_status witcert_decode(witcert_cache* c, int layer, const void* q, double delta_req, float* out,
                               float* meter_a, float* meter_b, float* raw_a, float* raw_b, float* meter_v,
-                              void* stream) {
+                              void* stream) try {
   if (witcert_status s = check_layer(c, layer)) return s;
   if (!q || !out) return fail(WITCERT_EINVAL, "q and out must not be NULL");
   if (meter_v && !c->vwit) return fail(WITCERT_EINVAL, "meter_v needs a cache created with v_witness");
@@ -1058,7 +1069,7 @@ witcert_status witcert_decode(witcert_cache* c, int layer, const void* q, double
   ++c->decode_calls;
   ok();
   return WITCERT_OK;
-}
+} WITCERT_NO_THROW
 
 witcert_status witcert_decode_noalloc(witcert_cache* c, int layer, const void* q, double delta_req, float* out,
                                       float* meter_a, float* meter_b, float* raw_a, float* raw_b, float* meter_v,
@@ -1238,7 +1249,7 @@ witcert_status witcert_gate_stats(witcert_cache* c, witcert_gate_counters* out, 
   return WITCERT_OK;
 }
 
-witcert_status witcert_stats(witcert_cache* c, witcert_stats_t* out) {
+witcert_status witcert_stats(witcert_cache* c, witcert_stats_t* out) try {
   if (!c || !out) return fail(WITCERT_EINVAL, "NULL argument");
   cudaError_t e = cudaDeviceSynchronize();
   if (e != cudaSuccess) return cuda_fail(e, "stats");
@@ -1258,9 +1269,9 @@ witcert_status witcert_stats(witcert_cache* c, witcert_stats_t* out) {
   out->pages_used = c->table ? (uint64_t)c->cfg.max_pages - c->free_pages.size() : 0;
   ok();
   return WITCERT_OK;
-}
+} WITCERT_NO_THROW
 
-witcert_status witcert_set_profiling(witcert_cache* c, int on) {
+witcert_status witcert_set_profiling(witcert_cache* c, int on) try {
   if (!c) return fail(WITCERT_EINVAL, "cache is NULL");
   if (!on && c->profiling) {
     cudaDeviceSynchronize();
@@ -1270,7 +1281,7 @@ witcert_status witcert_set_profiling(witcert_cache* c, int on) {
   c->profiling = on != 0;
   ok();
   return WITCERT_OK;
-}
+} WITCERT_NO_THROW
 
 witcert_status witcert_set_launch_overlap(witcert_cache* c, int on) {
   if (!c) return fail(WITCERT_EINVAL, "cache is NULL");
