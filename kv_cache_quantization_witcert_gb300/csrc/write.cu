@@ -21,7 +21,7 @@ cudaError_t launch_write_ragged(int scheme, const WriteArgs& a, const RaggedArgs
 }
 
 cudaError_t launch_kivi_keys(const WriteArgs& a, cudaStream_t st, bool pdl) {
-  if (a.B * a.n_tok * a.Hkv == 0) return cudaSuccess;
+  if (a.B == 0 || a.n_tok == 0 || a.Hkv == 0) return cudaSuccess;
   return a.is_bf16 ? kivi_keys_t<__nv_bfloat16>(a, NoRope{}, st, pdl) : kivi_keys_t<float>(a, NoRope{}, st, pdl);
 }
 
@@ -101,7 +101,7 @@ void philox_round_keys(uint64_t seed, uint32_t (&rk0)[10], uint32_t (&rk1)[10]) 
 }
 
 cudaError_t launch_write(int scheme, const WriteArgs& a, cudaStream_t st, bool pdl) {
-  if (a.B * a.n_tok * a.Hkv == 0) return cudaSuccess;
+  if (a.B == 0 || a.n_tok == 0 || a.Hkv == 0) return cudaSuccess;
   return a.is_bf16 ? launch_t<__nv_bfloat16>(scheme, a, NoRope{}, st, pdl) : launch_t<float>(scheme, a, NoRope{}, st, pdl);
 }
 

@@ -18,6 +18,7 @@
 // turn each by its position pos0 + t and round it to the input type before anything else sees it
 // (codes, witness and exact copies are those of a rotated key written by the plain writers).
 #pragma once
+#include <algorithm>
 #include <cfloat>
 #include <cmath>
 #include <type_traits>
@@ -628,9 +629,9 @@ __device__ __forceinline__ void write_token_direct(const WriteArgs& a, const RP&
 template <typename T, int SCH, bool VW, typename RP>
 __global__ void __launch_bounds__(128) write_token_kernel(const WriteArgs a, const __grid_constant__ RP rp) {
   const ChainEntry chain(a.late_wait != 0);
-  const int wid = (blockIdx.x * blockDim.x + threadIdx.x) >> 5, lane = threadIdx.x & 31;
-  if (wid >= a.B * a.tok_count * a.Hkv) return;
-  const int h = wid % a.Hkv, n = a.tok_begin + (wid / a.Hkv) % a.tok_count, i = wid / (a.Hkv * a.tok_count);
+  const uint32_t wid = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (wid >= (uint32_t)a.B * a.tok_count * a.Hkv) return;
+  const int h = wid % a.Hkv, n = a.tok_begin + wid / a.Hkv % a.tok_count, i = wid / ((uint32_t)a.Hkv * a.tok_count);
   const int blk = (a.t0 + n) >> 4;
   constexpr int kBytes = block_bytes(SCH);
   uint8_t* bp = a.blocks + block_index(a.table, a.Hkv, a.nblk_max, i, h, blk) * kBytes;
@@ -824,9 +825,10 @@ __device__ __forceinline__ void kivi_v_token(const WriteArgs& a, const RP& rp, u
 template <typename T, typename RP>
 __global__ void __launch_bounds__(128) write_kivi_v_kernel(const WriteArgs a, const __grid_constant__ RP rp) {
   const ChainEntry chain(a.late_wait != 0);
-  const int wid = (blockIdx.x * blockDim.x + threadIdx.x) >> 5, lane = threadIdx.x & 31;
-  if (wid >= a.B * a.n_tok * a.Hkv) return;
-  const int h = wid % a.Hkv, n = (wid / a.Hkv) % a.n_tok, i = wid / (a.Hkv * a.n_tok);
+  // rows are counted in 32 unsigned bits (2^32 of them would be a terabyte of keys), threads are not
+  const uint32_t wid = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (wid >= (uint32_t)a.B * a.n_tok * a.Hkv) return;
+  const int h = wid % a.Hkv, n = wid / a.Hkv % a.n_tok, i = wid / ((uint32_t)a.Hkv * a.n_tok);
   const int t = a.t0 + n;
   uint8_t* bp = a.blocks + block_index(a.table, a.Hkv, a.nblk_max, i, h, t >> 4) * KiviLayout::BYTES;
   kivi_v_token<T>(a, rp, bp, i, h, t, uniform_row(a, i, n, h), lane);
@@ -968,12 +970,13 @@ cudaError_t launch_pdl(K kernel, dim3 grid, dim3 block, cudaStream_t st, bool pd
 }
 
 // KIVI keys of a write: the blocks it completes, then the unfinished one (if any).
+constexpr int kMaxGridY = 65535;
 template <typename T, typename RP>
 cudaError_t kivi_keys_t(const WriteArgs& a, const RP& rp, cudaStream_t st, bool pdl) {
   cudaError_t e = cudaSuccess;
   const int t_end = a.t0 + a.n_tok, b0 = a.t0 / kBlk, nfull = t_end / kBlk - b0;
-  if (nfull > 0) {
-    e = launch_pdl(write_kivi_k_kernel<T, RP>, dim3(a.B * a.Hkv, nfull), dim3(32), st, pdl, a, rp, b0);
+  for (int b = 0; b < nfull; b += kMaxGridY) {
+    e = launch_pdl(write_kivi_k_kernel<T, RP>, dim3(a.B * a.Hkv, std::min(nfull - b, kMaxGridY)), dim3(32), st, pdl, a, rp, b0 + b);
     if (e != cudaSuccess) return e;
   }
   if (t_end % kBlk) e = launch_pdl(write_kivi_k_kernel<T, RP>, dim3(a.B * a.Hkv, 1), dim3(32), st, pdl, a, rp, t_end / kBlk);
@@ -1024,7 +1027,7 @@ cudaError_t launch_t(int scheme, const WriteArgs& a, const RP& rp, cudaStream_t 
       WriteArgs b = a;
       b.tok_begin = begin;
       b.tok_count = count;
-      const dim3 g(((unsigned)(a.B * count * a.Hkv) * 32u + 127u) / 128u);
+      const dim3 g((unsigned)(((long long)a.B * count * a.Hkv + 3) / 4));
       return launch_tokens<T>(scheme, g, dim3(128), st, pdl, b, rp);
     };
     if (hi_full <= lo_full || (long long)a.B * a.n_tok * a.Hkv <= kTokenRows) return tokens(0, a.n_tok);
@@ -1034,8 +1037,8 @@ cudaError_t launch_t(int scheme, const WriteArgs& a, const RP& rp, cudaStream_t 
     if (e != cudaSuccess) return e;
     return tokens(hi_full - a.t0, t_end - hi_full);
   }
-  const int warps = a.B * a.n_tok * a.Hkv;
-  cudaError_t e = launch_pdl(write_kivi_v_kernel<T, RP>, dim3((warps * 32 + 127) / 128), dim3(128), st, pdl, a, rp);
+  const long long warps = (long long)a.B * a.n_tok * a.Hkv;
+  cudaError_t e = launch_pdl(write_kivi_v_kernel<T, RP>, dim3((unsigned)((warps + 3) / 4)), dim3(128), st, pdl, a, rp);
   if (e != cudaSuccess) return e;
   return kivi_keys_t<T>(a, rp, st, pdl);
 }

@@ -4,7 +4,7 @@
 namespace witcert {
 
 cudaError_t launch_write_rope(int scheme, const WriteArgs& a, const RopeArgs& rp, cudaStream_t st, bool pdl) {
-  if (a.B * a.n_tok * a.Hkv == 0) return cudaSuccess;
+  if (a.B == 0 || a.n_tok == 0 || a.Hkv == 0) return cudaSuccess;
   return a.is_bf16 ? launch_t<__nv_bfloat16>(scheme, a, rp, st, pdl) : launch_t<float>(scheme, a, rp, st, pdl);
 }
 
@@ -15,7 +15,7 @@ cudaError_t launch_write_ragged_rope(int scheme, const WriteArgs& a, const RopeA
 }
 
 cudaError_t launch_kivi_keys_rope(const WriteArgs& a, const RopeArgs& rp, cudaStream_t st, bool pdl) {
-  if (a.B * a.n_tok * a.Hkv == 0) return cudaSuccess;
+  if (a.B == 0 || a.n_tok == 0 || a.Hkv == 0) return cudaSuccess;
   return a.is_bf16 ? kivi_keys_t<__nv_bfloat16>(a, rp, st, pdl) : kivi_keys_t<float>(a, rp, st, pdl);
 }
 
