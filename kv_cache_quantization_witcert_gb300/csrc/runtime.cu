@@ -219,6 +219,12 @@ witcert_status witcert_create(const witcert_config* cfg, witcert_cache** out) tr
     return fail(WITCERT_EINVAL, "with the gate enabled max_tokens must be at most %d (the gate ranks up to %d blocks)",
                 gate_max_blocks() * kBlk, gate_max_blocks());
 
+  // sizes that 64 bits do not hold would wrap to an allocation too small (the other arrays are smaller
+  // than the store)
+  const double nblk = (f.max_tokens + (double)kBlk - 1) / kBlk, pages = f.max_pages > 0 ? f.max_pages : f.batch * nblk;
+  if ((double)f.n_layers * pages * f.n_kv_heads * block_bytes((int)f.scheme) > 0x1p62 ||
+      (double)f.batch * f.n_q_heads * std::max(nblk, (double)f.n_splits) * kPartStride * sizeof(float) > 0x1p62)
+    return fail(WITCERT_ENOMEM, "a cache of this size cannot be addressed");
   std::unique_ptr<witcert_cache, void (*)(witcert_cache*)> owner(new witcert_cache(), [](witcert_cache* x) { free_all(x); delete x; });
   witcert_cache* c = owner.get();
   c->cfg = f;
@@ -234,7 +240,7 @@ witcert_status witcert_create(const witcert_config* cfg, witcert_cache** out) tr
   if (e != cudaSuccess) return cuda_fail(e, "device query");
   c->scheme = (int)f.scheme;
   c->bblk = block_bytes(c->scheme);
-  c->nblk_max = (f.max_tokens + kBlk - 1) / kBlk;
+  c->nblk_max = (f.max_tokens - 1) / kBlk + 1;                 // no sum that could pass 31 bits
   c->elem = f.kv_dtype == WITCERT_BF16 ? 2 : 4;
   c->layer_blocks = f.max_pages > 0 ? (size_t)f.max_pages * f.n_kv_heads * c->bblk : layer_rows(c) * c->nblk_max * c->bblk;
   const int auto_on = auto_splits(c, c->nblk_max, true, 0), auto_off = auto_splits(c, c->nblk_max, false, 0);

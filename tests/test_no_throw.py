@@ -35,3 +35,23 @@ def test_create_without_host_memory():
                        text=True, timeout=120)
     assert r.returncode == 0, r.stderr[-2000:]
     assert r.stdout.split(None, 2) == ["-2", "None", "host allocation failed\n"]
+
+
+@pytest.mark.parametrize("change", [dict(n_layers=64, batch=64, n_kv_heads=65535, n_q_heads=65535, max_tokens=2 ** 31 - 16),
+                                    dict(batch=1 << 14, n_kv_heads=1 << 12, n_q_heads=1 << 12, n_splits=2 ** 31 - 1),
+                                    dict(n_layers=65535, n_kv_heads=65535, n_q_heads=65535, max_pages=2 ** 31 - 1)])
+def test_sizes_beyond_64_bits(change):
+    """Refused before anything is allocated, not wrapped to a small allocation."""
+    import ctypes
+
+    from kv_cache_quantization_witcert_gb300 import _lib, load
+    try:
+        build.build()
+    except RuntimeError as e:  # no toolkit on this machine
+        pytest.skip(str(e))
+    cfg = _lib.witcert_config(1, 1, 1, 128, 1, 16, 1, _lib.BF16, 0, 1, 0, 0, 0, 0, 0)
+    for name, value in change.items():
+        setattr(cfg, name, value)
+    out = ctypes.c_void_p(1)
+    assert load().witcert_create(ctypes.byref(cfg), ctypes.byref(out)) == _lib.ENOMEM
+    assert out.value is None and b"addressed" in load().witcert_last_error()
