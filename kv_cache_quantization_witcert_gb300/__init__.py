@@ -6,6 +6,7 @@ the C ABI (include/witcert.h): witcert_create / write / decode / gate / ...
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import math
 
@@ -226,9 +227,10 @@ class Cache:
         batch = self.cfg.batch
         if len(counts) != batch:
             raise ValueError(f"{name} needs one count per sequence ({batch}), got {len(counts)}")
-        if counts and not (-0x80000000 <= min(counts) and max(counts) <= 0x7FFFFFFF):
-            raise ValueError(f"{name} must fit 32 bits, got {counts}")
-        return counts, (ctypes.c_int32 * batch)(*counts)
+        try:
+            return counts, (ctypes.c_int32 * batch).from_buffer(array.array("i", counts))
+        except OverflowError:
+            raise ValueError(f"{name} must fit 32 bits, got {counts}") from None
 
     def witcert_write_rope(self, layer, K, V, rope, K_hat=None, V_hat=None, stream=None):
         """witcert_write (witcert_write_hat with K_hat, V_hat) of keys without positions: each is turned by
