@@ -235,10 +235,13 @@ witcert_status witcert_read(witcert_cache* cache, int layer, const int32_t* t0, 
  * query head j reads KV head j / (Hq/Hkv).  out: device, q's shape, bf16.  Row by row this is what
  * witcert_decode gives at that length (KIVI2: with the blocks finished since then quantized), to
  * bf16; no meters are formed.  Products run on the tensor cores: decoded keys and values and the
- * softmax weights are rounded to fp16 (keys and values beyond 65504 saturate), for a black-box
- * cache to bf16, with fp32 sums (fp16 weights below 2^-26 of a row's largest are off by at most 2^-37
- * of it).  Keys a query does not see have weight 0; values among the same 128 tokens must be finite
- * for that to hold.  bf16 caches only.  q, out and workspace are 32-byte aligned; workspace: device,
+ * softmax weights are rounded to fp16, for a black-box cache to bf16, with fp32 sums.  In fp16 keys and
+ * values are off by 2^-11 of themselves, or 2^-25 below 2^-14 (the dithered store's by up to 2^-11 of
+ * their scale more: the dither is rounded before it is taken off), and saturate at 65504; query rows
+ * are scaled by a power of two first, and only elements below 2^-17 of a row's largest are rounded, by
+ * 2^-25 of it; weights below 2^-26 of a row's largest are off by at most 2^-37 of it.  Keys a query does
+ * not see have weight 0; the values of the 382 tokens after it must be finite for that to hold (rows
+ * past a sequence's end may hold anything).  bf16 caches only.  q, out and workspace are 32-byte aligned; workspace: device,
  * at least what witcert_attend_workspace says for the same n_tok; nothing in it is kept between calls.
  * EINVAL on bad arguments.  Asynchronous on `stream`, after a pending gate of the layer.  A device
  * wait that runs out (2 s) leaves the rows it concerns unwritten and counts in witcert_stats'

@@ -13,7 +13,7 @@
 // group that holds its last S_w may overwrite Q_w; and every softmax thread's P_w(j) was announced,
 // so its partner has read what they swapped for tile j.
 //
-// The operands are fp16 for the quantized stores (2^-12 rounding of the decoded values; query rows
+// The operands are fp16 for the quantized stores (2^-11 rounding of the decoded values; query rows
 // are scaled by powers of two) and bf16 for the black-box store, whose values bf16 holds exactly;
 // weights round to the same type.  Sums and products accumulate in fp32.  Rows are independent, so a
 // row tile may mix tokens; keys past a row's position, and image rows past the sequence's length

@@ -164,7 +164,8 @@ __device__ __forceinline__ void store32(void* p, const uint32_t (&v)[8]) {
 
 // This thread's 128 / N channels of query row `row` of a segment as operand words in the key images'
 // channel order; zero for rows past the sequence's.  Returns log2(e)/sqrt(d) times the power of two
-// that the row was divided by: fp16 rows are scaled to a largest element in [1, 2).
+// that the row was divided by: fp16 rows are scaled to a largest element in [1, 2), which keeps bf16's eight
+// bits of elements down to 2^-17 of it.
 template <bool BF16, int N>
 __device__ __forceinline__ float query_words(const AttendArgs& a, const Segment& u, int row, uint32_t (&w)[64 / N],
                                              RowGroup<N>& grp) {

@@ -30,8 +30,9 @@ template <int SCH> __device__ __forceinline__ uint32_t operand2(float a, float b
 }
 
 // The dithered store's operand: s (code - xi) = code s + (-xi) s with one rounding of the sum; -xi is
-// 1.5 - (1 + its upper 23 random bits), rounded to fp16 (an error below 2^-12 s), without an
-// integer-to-float conversion.
+// 1.5 - (1 + its upper 23 random bits), rounded to fp16 (2^-13 s), without an integer-to-float conversion,
+// and so is its product with s (2^-12 s; 2^-25 where it is subnormal).  Both stay under what the store itself
+// is off by, s / sqrt 12; formed in fp32 they would take two conversions and two FMAs an element.
 __device__ __forceinline__ uint32_t neg_xi2(uint32_t u0, uint32_t u1) {
   return h2_bits(__floats2half2_rn(1.5f - __uint_as_float(__funnelshift_r(u0, 0x7Fu, 9)),
                                    1.5f - __uint_as_float(__funnelshift_r(u1, 0x7Fu, 9))));

@@ -34,7 +34,7 @@ struct WriteArgs {
   int pos0;                  // global position of the cache's first token (dither key)
   int is_bf16;
   int late_wait;             // token, block and KIVI value kernels wait for their predecessor at
-                             // their end instead of their start (see ChainEntry in write.cu)
+                             // their end instead of their start (see ChainEntry in write_kernels.cuh)
   uint64_t seed;
   uint32_t rk0[10], rk1[10]; // Philox round keys of `seed` (as in DecodeArgs)
   void* backing;             // device-mapped pinned host, layer base [B][Hkv][backing_rows][128], or null
@@ -196,8 +196,8 @@ cudaError_t launch_read(int scheme, const ReadArgs& a, cudaStream_t st);
 // of sequence seq[k] (len[k] tokens long) are the queries, packed from token row row0[k] on.  A
 // query row of a KV head is (token, head of the group), token-major: rows_k = n grp.  A unit is a
 // row tile of one KV head; CTA c takes the key tiles from start[c] up to start[c + 1] in (sequence,
-// row tile, head, key tile) order, so every CTA has the same number of them, and a unit that crosses CTAs leaves one
-// record per row and part.
+// row tile, head, key tile) order: shares of the same time (a unit's start counts in it) or whole units
+// (share_units in runtime.cu).  A unit that crosses CTAs leaves one record per row and part.
 constexpr int kAttendSeqs = 64;
 constexpr int kAttendCtas = 192;
 constexpr int kTileTok = 128;                    // tokens of a key / value tile

@@ -396,9 +396,9 @@ __device__ __forceinline__ bool exact_side(const WriteArgs& a, int i, int h, int
 }
 
 // The token at position t (row r = t mod 16 of its block) of sequence i, KV head h, whose input
-// row's part of this lane is in `in` (keys already turned), quantized into the block image at bp (device memory or shared memory).  STAGED: the value
-// codes go, as one word of four channels per lane, to row r of the warp's staging area vst
-// (natural order) instead of their places in the block.
+// row's part of this lane is in `in` (keys already turned), quantized into the block image at bp
+// (device memory or shared memory).  STAGED: the value codes go, as one word of four channels per lane,
+// to row r of the warp's staging area vst (natural order) instead of their places in the block.
 template <typename T, bool DITHER, bool VW, bool STAGED>
 __device__ __forceinline__ void int8_token(const WriteArgs& a, uint8_t* bp, uint32_t* vst, int i, int h, int t,
                                            int lane, const TokIn<T>& in) {
@@ -1014,6 +1014,11 @@ cudaError_t launch_whole_blocks(int scheme, const WriteArgs& a, const RP& rp, co
 // fill blocks: a block's sixteen tokens one after another take about 30 us, and only a full GPU of
 // such warps makes up for it.  Blocks against tokens, dithered INT8: 512 rows 28.7 / 6.2 us, 8192
 // 30.7 / 12.3, 32768 36.9 / 28.7, 131072 86.0 / 96.2; FP8 22.5 / 8.2, 24.6 / 12.3, 30.7 / 24.6, 65.6 / 71.7.
+// With the keys' rotation (and cold inputs): dithered INT8 8192 35.5 / 15.0, 32768 43.6 / 37.5, 49152 53.9 /
+// 52.4, 65536 76.4 / 68.3, 98304 90.8 / 96.9, 131072 115 / 128; FP8 28.3 / 15.0, 36.6 / 33.4, 42.6 / 46.2,
+// 58.0 / 58.0, 72.4 / 80.5, 88.7 / 105; black box 25.2 / 15.0, 37.5 / 37.0, 56.0 / 51.9, 60.0 / 66.2, 84.6 / 94.9,
+// 101 / 124.  Between 32768 and 65536 rows neither side wins throughout: the blocks' time jumps by a walk
+// (16 to 22 us) where their CTAs (a block's four heads each) pass the 912 that run at once.
 constexpr long long kTokenRows = 32768;
 
 template <typename T, typename RP>
