@@ -36,6 +36,7 @@ witcert_status fail(witcert_status s, const char* fmt, ...) {
   return s;
 }
 witcert_status cuda_fail(cudaError_t e, const char* where) {
+  cudaGetLastError();                  // reported here: the next launch that asks must not find it
   return fail(e == cudaErrorMemoryAllocation ? WITCERT_ENOMEM : WITCERT_ECUDA, "%s: %s", where, cudaGetErrorString(e));
 }
 void ok() { g_err[0] = 0; }
@@ -1058,7 +1059,7 @@ witcert_status witcert_decode(witcert_cache* c, int layer, const void* q, double
     if (c->prof_free.empty()) {
       ProfPair n{};
       if (cudaEventCreate(&n.a) != cudaSuccess || cudaEventCreate(&n.b) != cudaSuccess)
-        return fail(WITCERT_ECUDA, "creating profiling events");
+        return cuda_fail(cudaGetLastError(), "creating profiling events");
       c->prof_free.push_back(n);
     }
     pp = c->prof_free.back();
