@@ -25,3 +25,30 @@ def test_calls_after_a_cache_that_does_not_fit():
         assert e.value.status == _lib.ENOMEM
         assert torch.equal(f(), w)
     torch.cuda.synchronize()
+
+
+def test_calls_after_polling_a_gate():
+    """witcert_gate_stats asks for the gate's event until it is there: "not ready" is no error of later calls."""
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    g = torch.Generator().manual_seed(2)
+    K = torch.randn(1, 64, 2, 128, generator=g).bfloat16().cuda()
+    q = torch.randn(1, 4, 128, generator=g).bfloat16().cuda()
+    pos, rope = torch.arange(64, device="cuda"), wc.Rope(128)
+    c = wc.Cache(1, 4, 2, 1, 64, "fp8_e4m3", max_repair_blocks=16)
+    c.witcert_write(0, K, K)
+    c.decode(0, q, 1e-2)
+    for f in (lambda: wc.witcert_rope(rope, pos, K[0]), lambda: c.read(0, [64]), lambda: c.attend(0, q, [1]),
+              lambda: K.float() + 1):
+        torch.cuda._sleep(100_000_000)                     # 50 ms that the gate waits for
+        c.witcert_gate(0, 0.0)
+        c.witcert_gate_stats()
+        f()
+        c.decode(0, q, 1e-2)
+    with pytest.raises(wc.WitcertError) as e:              # a deadline that runs out
+        torch.cuda._sleep(400_000_000)
+        c.witcert_gate(0, 0.0)
+        c.witcert_gate_stats(1)
+    assert e.value.status == _lib.ETIMEDOUT
+    wc.witcert_rope(rope, pos, K[0])
+    torch.cuda.synchronize()
