@@ -288,6 +288,9 @@ witcert_status witcert_reset_sequence(witcert_cache* cache, int seq, void* strea
  * measured, not by a worst-case bound.
  * A bound that no number holds (a witness above fp16's range, inputs that are not finite) is
  * +inf: 1 in meter_a and meter_b, +inf in the other meters and the block risks.
+ * out: the INT8 and KIVI2 schemes multiply a token's weight by its value scale in fp16, so products
+ * below 2^-14 are off by up to 2^-25: values under about 2^-10 in all come out less exact than from
+ * witcert_attend (output off by 0.5% of its size at |v| near 2^-10, 7% near 2^-14).
  * Any meter pointer may be NULL; if all five are NULL the meter work is
  * compiled out and `out` is bit-identical to the metered run's.
  * With the gate enabled, per-16-token-block risks of the gate's tier
