@@ -253,6 +253,21 @@ witcert_status witcert_attend(witcert_cache* cache, int layer, const void* q, co
  * lengths (host, no device work). */
 witcert_status witcert_attend_workspace(const witcert_cache* cache, int layer, const int32_t* n_tok, size_t* bytes);
 
+/* Sequences take each other's state (beams that change places, a prompt handed to several beams, a
+ * prefix that a new request shares): sequence i becomes, in every layer, the first lengths[i] tokens (all of
+ * them where that is more; lengths NULL: all) of what sequence parents[i] held before the call; -1: empty.
+ * parents and lengths are host [batch]; any map, in place.  A sequence that is its own parent is cut to its
+ * length, and in a paged cache gives back the pages behind it.  What the next tokens, decodes, attends, reads
+ * and exports of i see is what they would see of a sequence written with those tokens.
+ * Contiguous caches copy blocks; paged ones share pages: a page belongs to every sequence that refers to
+ * it, goes back to the pool when none does, and an append to a page that others hold first gives the
+ * sequence a copy of its own, in all layers (the append is ENOMEM if the pool has no page for it, with
+ * nothing written).  Value witnesses and the unfinished KIVI2 block's keys are each sequence's own, and
+ * copied.  Block risks become stale.  EINVAL for a bad parent, a negative length, a KIVI2 cut that would reopen a
+ * finished block (as for witcert_truncate), and for a gated cache: repairs and the backing store belong to
+ * one sequence.  Asynchronous on `stream`. */
+witcert_status witcert_fork(witcert_cache* cache, const int32_t* parents, const int32_t* lengths, void* stream);
+
 /* Empty sequence `seq` in every layer so the slot can serve a new request (continuous
  * batching).  Its repairs are dropped too (their slots in the exact-key pool are not
  * reused), a paged cache returns its pages to the pool, and its value witnesses are zeroed.
@@ -382,6 +397,52 @@ witcert_status witcert_merge_partials(const float* parts, int n_parts, int batch
  * Asynchronous on `stream`.  EINVAL for nblk outside [1, 16384] or bad shapes. */
 witcert_status witcert_gate_select(const float* risk, const uint8_t* repaired, int batch, int n_q_heads,
                                    int n_kv_heads, int nblk, float tau, uint32_t* selected, void* stream);
+
+/* Beam search over logits: each request's n_out best continuations.  Row r * n_beams + b is beam b of
+ * request r: logits at logits + r request_stride + b beam_stride (device, elements, tokens adjacent), its
+ * cumulative log-probability scores[row] and, if given, whether it has finished.  A row offers every token with
+ * the score scores[row] + x_token - log sum exp x; a finished one only itself, as token `eos` with its own
+ * score.  No candidates come from a row whose score is not finite (an absent beam), from one that has no
+ * softmax (+inf or NaN among its logits, or nothing but -inf), or of a logit of -inf.  Candidates
+ * are ordered by score (formed in 64 bits; sums of exponentials in fp32), then row, then token.
+ * rows, tokens, out_scores (device [n_requests][n_out]) take the row a candidate continues, its token and
+ * score; places for which there is no candidate get -1, -1 and -inf.  out_finished, if given, says whether a
+ * candidate's row had finished or its token is eos.  With n_out = n_beams, rows serve as witcert_fork's
+ * parents, and out_scores and out_finished may be scores and finished themselves. */
+typedef struct {
+  witcert_dtype dtype;               /* of the logits */
+  int n_requests, n_beams;           /* n_beams at most 128 */
+  int vocab;                         /* tokens, at most 2^27 */
+  int n_out;                         /* at most 256 */
+  int eos;                           /* -1: no token ends a beam (finished is NULL then) */
+  const void* logits;
+  long long request_stride, beam_stride;
+  const float* scores;               /* [n_requests][n_beams] */
+  const uint8_t* finished;           /* [n_requests][n_beams], 0 or 1, or NULL */
+  float* out_scores;
+  int32_t* rows;
+  int32_t* tokens;
+  uint8_t* out_finished;             /* or NULL */
+} witcert_beam_step;
+
+/* Bytes of device workspace that witcert_beam_select needs for this step's sizes, strides and logits'
+ * alignment (host, no device work). */
+witcert_status witcert_beam_workspace(const witcert_beam_step* step, size_t* bytes);
+
+/* One selection (see witcert_beam_step).  workspace: device, 16-byte aligned, at least what
+ * witcert_beam_workspace says; nothing in it is kept between calls, and calls that may run at the same time
+ * need one each.  Results do not depend on the order of execution.  EINVAL on bad arguments.  Asynchronous on
+ * `stream`; no cache is involved. */
+witcert_status witcert_beam_select(const witcert_beam_step* step, void* workspace, size_t workspace_bytes, void* stream);
+
+/* The token sequences of the last beams.  rows, tokens: device [n_steps][n_requests][n_beams], each step's
+ * choices as witcert_beam_select with n_out = n_beams writes them.  length: device [n_requests], how many steps of
+ * each request count (taken into [0, n_steps]); NULL: all.  out: device [n_requests][n_beams][n_steps]; beam
+ * b's sequence ends with its token of the last step and follows the rows back.  A row that is not one of
+ * its request's (-1: no candidate) ends the way back: that step and all before it are `pad`, as are the steps from
+ * length on.  n_beams at most 128.  EINVAL on bad arguments.  Asynchronous on `stream`; no cache is involved. */
+witcert_status witcert_beam_paths(const int32_t* rows, const int32_t* tokens, int n_steps, int n_requests, int n_beams,
+                                  const int32_t* length, int pad, int32_t* out, void* stream);
 
 typedef enum {
   WITCERT_FAULT_BACKING_LOST = 1   /* the layer's pinned backing store loses its exact keys, as

@@ -16,7 +16,8 @@ from . import _lib
 from ._lib import (BF16, BLACKBOX, EINVAL, ENOMEM, EPAGEIN, ESTATE, ETIMEDOUT, F32, FP8_E4M3, INT8_DITHER,  # noqa: F401
                    INT8_RTN, KIVI2, SCHEMES, WitcertError, check, load)
 
-__all__ = ["Cache", "Rope", "witcert_rope", "witcert_dither", "witcert_merge_partials", "witcert_gate_select", "WitcertError", "load", "SCHEMES", "PART_STRIDE"]
+__all__ = ["Cache", "Rope", "witcert_rope", "witcert_dither", "witcert_merge_partials", "witcert_gate_select", "witcert_beam_select",
+           "witcert_beam_paths", "BeamSearch", "WitcertError", "load", "SCHEMES", "PART_STRIDE"]
 
 _TORCH_DT = {F32: torch.float32, BF16: torch.bfloat16}
 
@@ -258,6 +259,13 @@ class Cache:
         _, arr = self._counts("lengths", lengths)
         check(load().witcert_truncate(self._h, layer, arr, _stream_ptr(stream)), "witcert_truncate")
 
+    def witcert_fork(self, parents, lengths=None, stream=None):
+        """Sequence i takes, in every layer, the first lengths[i] tokens (None: all) of what sequence parents[i]
+        holds (-1: none, it is empty then).  See witcert_fork in include/witcert.h."""
+        _, arr = self._counts("parents", parents)
+        cut = None if lengths is None else self._counts("lengths", lengths)[1]
+        check(load().witcert_fork(self._h, arr, cut, _stream_ptr(stream)), "witcert_fork")
+
     def witcert_read(self, layer, t0, n_tok, K, V, stream=None):
         """Tokens t0[i] .. t0[i] + n_tok[i] - 1 of every sequence (t0 None: the last n_tok[i]) as rows
         K, V [sum(n_tok), Hkv, 128] of the cache's dtype."""
@@ -466,6 +474,123 @@ def witcert_gate_select(risk, n_kv_heads, tau, repaired=None, selected=None, str
     check(load().witcert_gate_select(_ptr(risk), _ptr(repaired), B, Hq, n_kv_heads, nblk, float(tau), _ptr(selected),
                                      _stream_ptr(stream)), "witcert_gate_select")
     return selected
+
+
+def _here(name, t):
+    """Check that a tensor lies on the current device, where the library launches."""
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+
+
+def witcert_beam_select(logits, scores, n_out=None, finished=None, eos=-1, out=None, stream=None):
+    """Each request's n_out (None: as many as beams) best continuations: logits [R, W, V] bf16 or float32 (any
+    request and beam strides, tokens adjacent), cumulative log-probabilities scores [R, W] float32, finished
+    [R, W] bool or None.  Returns (scores float32, rows int32, tokens int32, finished bool), each [R, n_out]: a
+    row is request * W + beam, -1 where there is no candidate.  out: a tuple of four tensors to write, the
+    last of them or the input's own for scores and finished as witcert_beam_step in include/witcert.h allows."""
+    if not isinstance(logits, torch.Tensor) or logits.dim() != 3:
+        raise ValueError("logits must be a torch.Tensor [requests, beams, vocabulary]")
+    if logits.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"logits must be torch.bfloat16 or torch.float32, got {logits.dtype}")
+    R, W, V = logits.shape
+    if V != 1 and logits.stride(2) != 1:
+        raise ValueError(f"logits must have adjacent tokens (stride 1), got stride {logits.stride(2)}")
+    n = W if n_out is None else int(n_out)
+    _need(("scores", scores, torch.float32, (R, W)), ("finished", finished, torch.bool, (R, W), True))
+    if not logits.is_cuda:
+        raise ValueError("logits must be a CUDA tensor")
+    _here("logits", logits)
+    if out is None:
+        out = tuple(_empty(stream, (R, max(n, 0)), dt, logits.device)
+                    for dt in (torch.float32, torch.int32, torch.int32, torch.bool))
+    elif len(out) != 4:
+        raise ValueError(f"out needs four tensors (scores, rows, tokens, finished), got {len(out)}")
+    _need(*((name, t, dt, (R, n)) for name, t, dt in zip(("out scores", "rows", "tokens", "out finished"), out,
+                                                        (torch.float32, torch.int32, torch.int32, torch.bool))))
+    step = _lib.witcert_beam_step(BF16 if logits.dtype == torch.bfloat16 else F32, R, W, V, n, int(eos), logits.data_ptr(),
+                                  logits.stride(0), logits.stride(1), scores.data_ptr(), _ptr(finished),
+                                  *(t.data_ptr() for t in out))
+    size = ctypes.c_size_t()
+    check(load().witcert_beam_workspace(ctypes.addressof(step), ctypes.byref(size)), "witcert_beam_workspace")
+    workspace = _empty(stream, size.value, torch.uint8, logits.device)
+    check(load().witcert_beam_select(ctypes.addressof(step), workspace.data_ptr(), size.value, _stream_ptr(stream)),
+          "witcert_beam_select")
+    return tuple(out)
+
+
+def witcert_beam_paths(rows, tokens, length=None, pad=-1, out=None, stream=None):
+    """The token sequences [R, W, T] int32 of the last beams: rows, tokens [T, R, W] int32 as witcert_beam_select
+    chose them step by step, length [R] int32 steps that count (None: all), pad elsewhere (see
+    witcert_beam_paths in include/witcert.h)."""
+    T, R, W = (_extent(rows, i) for i in range(3))
+    _need(("rows", rows, torch.int32, (T, R, W)), ("tokens", tokens, torch.int32, (T, R, W)),
+          ("length", length, torch.int32, (R,), True))
+    _here("rows", rows)
+    if out is None:
+        out = _empty(stream, (R, W, T), torch.int32, rows.device)
+    _need(("out", out, torch.int32, (R, W, T)))
+    check(load().witcert_beam_paths(_ptr(rows), _ptr(tokens), T, R, W, _ptr(length), int(pad), _ptr(out),
+                                    _stream_ptr(stream)), "witcert_beam_paths")
+    return out
+
+
+class BeamSearch:
+    """A beam search of n_beams a request over a cache: sequence r * n_beams + b is beam b of request r.
+
+    Write each request's prompt to its first beam's sequence, then start(); every step() takes the logits of
+    all beams, chooses their continuations, and moves the cache's sequences to where the chosen beams are.
+    It returns the tokens [R, W] int32 (-1: the request has no beam there) that the next step appends.  A
+    finished beam keeps its score and goes on with eos; paths() gives the sequences so far, scores the
+    beams' log-probabilities, falling."""
+
+    def __init__(self, cache, n_beams, max_steps, eos=-1):
+        batch = cache.cfg.batch
+        if n_beams < 1 or batch % n_beams:
+            raise ValueError(f"the cache's batch ({batch}) must be a multiple of n_beams ({n_beams})")
+        if max_steps < 1:
+            raise ValueError(f"max_steps must be at least 1, got {max_steps}")
+        self.cache, self.eos, self.steps = cache, int(eos), 0
+        self.shape = R, W = batch // n_beams, int(n_beams)
+        dev = torch.device("cuda", torch.cuda.current_device())
+        self._rows = torch.empty((int(max_steps), R, W), dtype=torch.int32, device=dev)
+        self._tokens = torch.empty_like(self._rows)
+        self.scores = torch.empty((R, W), dtype=torch.float32, device=dev)
+        self.finished = torch.empty((R, W), dtype=torch.bool, device=dev)
+        self._restart()
+
+    def _restart(self):
+        self.steps = 0
+        self.scores.fill_(-math.inf)
+        self.scores[:, 0] = 0.0
+        self.finished.fill_(False)
+
+    def start(self, stream=None):
+        """Hand each request's prompt, in its first beam's sequence, to the other beams."""
+        W = self.shape[1]
+        self.cache.witcert_fork([i // W * W for i in range(self.cache.cfg.batch)], stream=stream)
+        with torch.cuda.stream(stream):
+            self._restart()
+
+    def step(self, logits, stream=None):
+        """Choose the continuations of all beams from logits [R, W, V] and move the cache's sequences."""
+        if self.steps == len(self._rows):
+            raise ValueError(f"the search was made for {len(self._rows)} steps")
+        if not isinstance(logits, torch.Tensor) or tuple(logits.shape[:2]) != self.shape:
+            raise ValueError(f"logits must be a torch.Tensor [{self.shape[0]}, {self.shape[1]}, vocabulary]")
+        rows, tokens = self._rows[self.steps], self._tokens[self.steps]
+        done = self.finished if self.eos >= 0 else None
+        witcert_beam_select(logits, self.scores, finished=done, eos=self.eos,
+                            out=(self.scores, rows, tokens, self.finished), stream=stream)
+        with torch.cuda.stream(stream):
+            parents = rows.flatten().tolist()
+        # a request with fewer candidates than beams leaves the others where they are
+        self.cache.witcert_fork([i if p < 0 else p for i, p in enumerate(parents)], stream=stream)
+        self.steps += 1
+        return tokens
+
+    def paths(self, pad=-1, stream=None):
+        """The beams' tokens so far, [R, W, steps] int32."""
+        return witcert_beam_paths(self._rows[:self.steps], self._tokens[:self.steps], pad=pad, stream=stream)
 
 
 def witcert_quotient_selftest(n_f32=4096, seed=0, stream=None):

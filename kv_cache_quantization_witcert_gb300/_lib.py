@@ -52,6 +52,14 @@ class witcert_rope_tensor(ctypes.Structure):
                 ("y_token_stride", ctypes.c_longlong), ("y_head_stride", ctypes.c_longlong)]
 
 
+class witcert_beam_step(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int), ("n_requests", ctypes.c_int), ("n_beams", ctypes.c_int), ("vocab", ctypes.c_int),
+                ("n_out", ctypes.c_int), ("eos", ctypes.c_int), ("logits", ctypes.c_void_p),
+                ("request_stride", ctypes.c_longlong), ("beam_stride", ctypes.c_longlong), ("scores", ctypes.c_void_p),
+                ("finished", ctypes.c_void_p), ("out_scores", ctypes.c_void_p), ("rows", ctypes.c_void_p),
+                ("tokens", ctypes.c_void_p), ("out_finished", ctypes.c_void_p)]
+
+
 _vp, _int, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
 _fp = ctypes.POINTER(ctypes.c_float)
 
@@ -66,6 +74,10 @@ SIGNATURES = {
     "witcert_write_rope": [_vp, _int, _vp, _vp, _vp, _vp, _int, _vp, _vp],
     "witcert_write_rope_ragged": [_vp, _int, _vp, _vp, _vp, _vp, ctypes.POINTER(ctypes.c_int32), _vp, _vp],
     "witcert_truncate": [_vp, _int, ctypes.POINTER(ctypes.c_int32), _vp],
+    "witcert_fork": [_vp, ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(ctypes.c_int32), _vp],
+    "witcert_beam_workspace": [_vp, ctypes.POINTER(_sz)],
+    "witcert_beam_select": [_vp, _vp, _sz, _vp],
+    "witcert_beam_paths": [_vp, _vp, _int, _int, _int, _vp, _int, _vp, _vp],
     "witcert_attend": [_vp, _int, _vp, ctypes.POINTER(ctypes.c_int32), _vp, _vp, _sz, _vp],
     "witcert_attend_workspace": [_vp, _int, ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(_sz)],
     "witcert_read": [_vp, _int, ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(ctypes.c_int32), _vp, _vp, _vp],

@@ -229,6 +229,73 @@ cudaError_t launch_attend_merge(const AttendArgs& a, cudaStream_t st);
 // Straight from the store, without images (units of kTileRows or kTinyRows rows).
 template <int SCH> cudaError_t launch_attend_few(const AttendArgs& a, cudaStream_t st);
 
+// Moves between the sequences of a cache (fork.cu), in an order in which none reads what an earlier one
+// wrote.  src: a sequence, kMoveKept (the row a kept move saved) or kMoveNone (an empty sequence); dst: a
+// sequence or kMoveKept (save the row).  Counts by what a stream counts in: [0] blocks, [1] rows of the
+// KIVI tail; load: the most of a run of moves from one source.
+constexpr int kMoveKept = -1, kMoveNone = -2;
+constexpr int kMovesPerLaunch = 256;
+struct MoveOp {
+  int src, dst;
+  int n[2], load[2];
+  int blocks;                // table entries that stay (a sequence that is only cut copies nothing)
+  int cap;                   // the most tokens the sequence keeps
+};
+struct MoveStream {          // rows of `unit` bytes counted by n[count], for each layer and head
+  uint8_t* base;
+  long long layer_pitch, seq_pitch, head_pitch;
+  int unit, count;
+  unsigned block0;           // filled by the launcher
+};
+struct MoveRows {
+  MoveStream s[3];
+  int n_streams, n;
+  MoveOp op[kMovesPerLaunch];
+};
+struct MoveInts {
+  int32_t *table, *lens;     // [B][nblk_max], [layers][B]; null: not kept on the device
+  int nblk_max, layers, B, n;
+  MoveOp op[kMovesPerLaunch];
+};
+// Pages src[k] (-1: nothing to copy) to dst[k] in every layer; table[idx[k]] = dst[k].
+struct CopyPages {
+  uint8_t* blocks;
+  long long layer_pitch, page_bytes;
+  int32_t* table;
+  int n;
+  int src[kRaggedPerLaunch], dst[kRaggedPerLaunch], idx[kRaggedPerLaunch];
+};
+cudaError_t launch_move_rows(MoveRows& a, int layers, int heads, cudaStream_t st);
+cudaError_t launch_move_ints(const MoveInts& a, cudaStream_t st);
+cudaError_t launch_copy_pages(const CopyPages& a, int layers, cudaStream_t st);
+
+// Beam search (beam.cu).  A row (request, beam) of logits is cut into chunks of kBeamChunk tokens, counted
+// from the 32-byte boundary at or before its start; part p of a row is chunks p chunks_per_part, ...
+constexpr int kBeamChunk = 512;
+constexpr int kBeamMaxBeams = 128, kBeamMaxOut = 256;
+struct BeamArgs {
+  const void* logits;
+  long long request_stride, beam_stride;   // elements
+  const float* scores;       // [requests][beams]
+  const uint8_t* finished;   // [requests][beams], or null
+  int requests, beams, vocab, n_out, eos, is_bf16;
+  int chunks, parts, chunks_per_part;
+  float2* records;           // [requests][beams][parts]: largest logit, sum of exp(x - it)
+  float* maxima;             // [requests][beams][chunks]
+  float* out_scores;         // [requests][n_out]
+  int32_t *rows, *tokens;
+  uint8_t* out_finished;     // or null
+};
+cudaError_t launch_beam_select(const BeamArgs& a, cudaStream_t st);
+struct PathArgs {
+  const int32_t *rows, *tokens;    // [steps][requests][beams]
+  const int32_t* n_steps;    // [requests], or null
+  int32_t* out;              // [requests][beams][steps]
+  int steps, requests, beams, pad;
+  int tile;                  // steps a CTA holds at a time; filled by the launcher
+};
+cudaError_t launch_beam_paths(PathArgs& a, cudaStream_t st);
+
 struct ExportArgs {
   const uint8_t* blocks;
   const int32_t* table;      // paged store, or null

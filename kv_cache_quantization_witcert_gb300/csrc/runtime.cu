@@ -75,11 +75,13 @@ struct witcert_cache {
   int32_t* table = nullptr;         // paged store: [B][nblk_max] page of each block (all layers), -1 = none
   std::vector<int32_t> table_host;  // host copy of the page table
   std::vector<int32_t> free_pages;  // paged store: pages no sequence holds
+  std::vector<int> page_refs;       // paged store: how many sequences hold each page (forks share them)
   std::vector<int> len;             // per layer: the longest sequence
   std::vector<std::vector<int>> slen;   // per layer and sequence
   std::vector<uint64_t> write_gen, risk_gen;   // per layer: writes / resets so far; at the last metered decode
   bool ragged = false;              // sequence lengths may differ: kernels read dlen
   bool lengths_last = false;        // the most recent launch on the cache's stream set dlen
+  bool forked = false;              // a fork was the last to change blocks: the next launch starts after its end
   std::vector<cudaEvent_t> gate_done;
   std::vector<char> gate_pending;
   std::vector<char> backing_lost;   // per layer: the backing store misses exact keys (gate -> EPAGEIN)
@@ -138,6 +140,14 @@ bool order_after_gate(witcert_cache* c, int layer, cudaStream_t st) {
   if (!c->gate_pending[layer]) return false;
   cudaStreamWaitEvent(st, c->gate_done[layer], 0);
   return true;
+}
+
+// Whether the next launch may start before its predecessor's end.  The kernels that overlap read older
+// blocks, lengths and pages before they wait; a fork writes all of those.
+bool may_overlap(witcert_cache* c, bool waited) {
+  const bool after_fork = c->forked;
+  c->forked = false;
+  return c->overlap && !waited && !after_fork;
 }
 
 // Turns per position of a frequency (see rope.cuh): f / (2 pi) mod 1 in units of 2^-64, to the nearest.
@@ -264,6 +274,7 @@ witcert_status witcert_create(const witcert_config* cfg, witcert_cache** out) tr
     TRY(cudaMemset(c->table, 0xFF, entries * sizeof(int32_t)), "clearing the page table");
     c->table_host.assign(entries, -1);
     for (int pg = f.max_pages - 1; pg >= 0; --pg) c->free_pages.push_back(pg);
+    c->page_refs.assign(f.max_pages, 0);
   }
   if (gate) {
     TRY(dalloc(&c->slots, L * layer_rows(c) * c->nblk_max * sizeof(int32_t)), "allocating repair slots");
@@ -365,35 +376,67 @@ static cudaError_t push_lengths(witcert_cache* c, const std::vector<std::pair<in
   return push_ints(c->dlen, upd, st, pdl);
 }
 
-// Paged store: pages for every block the appends of n touch that has none yet (the table is
-// shared by the layers, so the first layer to reach a block takes its page).  Fails, taking
-// back what it took, when the pool runs out.
-static witcert_status take_pages(witcert_cache* c, int layer, const std::vector<int>& n,
-                                 std::vector<std::pair<int, int>>& upd) {
+// A page that an append gives its sequence: entry idx of the table changes from `was` (-1: none) to `now`.
+// A page that other sequences hold too is left to them, and what the sequence keeps of it is copied.
+struct PageTaken { int idx, was, now; bool copy; };
+
+// Paged store: pages of its own for every block the appends of n touch (the table is shared by the
+// layers, so the first layer to reach a block takes its page).  Fails, taking back what it took, when
+// the pool runs out.
+static witcert_status take_pages(witcert_cache* c, int layer, const std::vector<int>& n, std::vector<PageTaken>& taken) {
   if (!c->table) return WITCERT_OK;
   size_t most = 0;
   for (int i = 0; i < c->cfg.batch; ++i) most += n[i] > 0 ? n[i] / kBlk + 2 : 0;
-  upd.reserve(std::min(most, c->free_pages.size()));           // no allocation once pages are being taken
+  taken.reserve(std::min(most, c->free_pages.size()));         // no allocation once pages are being taken
   for (int i = 0; i < c->cfg.batch; ++i) {
     if (n[i] == 0) continue;
     const int t0 = c->slen[layer][i];
+    int held = 0;                                              // tokens of the sequence in any layer
+    for (int l = 0; l < c->cfg.n_layers; ++l) held = std::max(held, c->slen[l][i]);
     for (int b = t0 / kBlk; b <= (t0 + n[i] - 1) / kBlk; ++b) {
       int32_t& e = c->table_host[(size_t)i * c->nblk_max + b];
-      if (e >= 0) continue;
+      if (e >= 0 && c->page_refs[e] == 1) continue;
       if (c->free_pages.empty()) {
-        for (auto& u : upd) {
-          c->free_pages.push_back(u.second);
-          c->table_host[u.first] = -1;
+        for (const PageTaken& u : taken) {
+          c->free_pages.push_back(u.now);
+          c->page_refs[u.now] = 0;
+          c->table_host[u.idx] = u.was;
+          if (u.was >= 0) ++c->page_refs[u.was];
         }
-        upd.clear();
+        taken.clear();
         return fail(WITCERT_ENOMEM, "the page pool (%d pages) is exhausted", c->cfg.max_pages);
       }
-      e = c->free_pages.back();
+      const PageTaken u{(int)((size_t)i * c->nblk_max + b), e, c->free_pages.back(), e >= 0 && b * kBlk < held};
+      taken.push_back(u);
       c->free_pages.pop_back();
-      upd.emplace_back((int)((size_t)i * c->nblk_max + b), e);
+      c->page_refs[u.now] = 1;
+      if (u.was >= 0) --c->page_refs[u.was];
+      e = u.now;
     }
   }
   return WITCERT_OK;
+}
+
+// The device's side of take_pages: copies and table entries.  Copies end before what follows starts.
+static cudaError_t push_pages(witcert_cache* c, const std::vector<PageTaken>& taken, cudaStream_t st, bool& pdl) {
+  CopyPages a{};
+  a.blocks = c->blocks;
+  a.layer_pitch = (long long)c->layer_blocks;
+  a.page_bytes = (long long)c->cfg.n_kv_heads * c->bblk;
+  a.table = c->table;
+  cudaError_t e = cudaSuccess;
+  std::vector<std::pair<int, int>> upd;
+  for (const PageTaken& u : taken) {
+    if (!u.copy) { upd.emplace_back(u.idx, u.now); continue; }
+    a.src[a.n] = u.was; a.dst[a.n] = u.now; a.idx[a.n] = u.idx;
+    pdl = false;
+    if (++a.n == kRaggedPerLaunch) {
+      if ((e = launch_copy_pages(a, c->cfg.n_layers, st)) != cudaSuccess) return e;
+      a.n = 0;
+    }
+  }
+  if ((e = launch_copy_pages(a, c->cfg.n_layers, st)) != cudaSuccess) return e;
+  return push_ints(c->table, upd, st, pdl);
 }
 
 // From now on the sequences' lengths may differ: the device gets every layer's lengths.
@@ -454,12 +497,12 @@ static witcert_status write_impl(witcert_cache* c, int layer, const void* K, con
     return fail(WITCERT_EINVAL, "K, V, K_hat and V_hat must be %d-byte aligned", 4 * c->elem);
   bool uniform = !c->ragged;
   for (int i = 1; i < B && uniform; ++i) uniform = n[i] == n[0];
-  std::vector<std::pair<int, int>> pages;
+  std::vector<PageTaken> pages;
   if (witcert_status ps = take_pages(c, layer, n, pages)) return ps;
   auto st = static_cast<cudaStream_t>(stream);
   const bool waited = order_after_gate(c, layer, st);
-  bool pdl = c->overlap && !waited;
-  cudaError_t e = push_ints(c->table, pages, st, pdl);
+  bool pdl = may_overlap(c, waited);
+  cudaError_t e = push_pages(c, pages, st, pdl);
   if (e != cudaSuccess) return cuda_fail(e, "page table");
   int first_blk = INT_MAX;
   if (uniform) {
@@ -626,14 +669,14 @@ witcert_status witcert_reset_sequence(witcert_cache* c, int seq, void* stream) t
   if (c->table) freed.reserve(c->nblk_max);
   bool waited = false;
   for (int l = 0; l < c->cfg.n_layers; ++l) waited |= order_after_gate(c, l, st);
-  bool pdl = c->overlap && !waited;
+  bool pdl = may_overlap(c, waited);
   cudaError_t e = enter_ragged(c, st, pdl);
   if (e == cudaSuccess) e = push_lengths(c, upd, st, pdl);
   if (c->table && e == cudaSuccess) {       // its pages go back to the pool
     for (int b = 0; b < c->nblk_max; ++b) {
       int32_t& pg = c->table_host[(size_t)seq * c->nblk_max + b];
       if (pg < 0) continue;
-      c->free_pages.push_back(pg);
+      if (--c->page_refs[pg] == 0) c->free_pages.push_back(pg);
       pg = -1;
       freed.emplace_back((int)((size_t)seq * c->nblk_max + b), -1);
     }
@@ -681,7 +724,7 @@ witcert_status witcert_truncate(witcert_cache* c, int layer, const int32_t* leng
   auto st = static_cast<cudaStream_t>(stream);
   bool waited = false;
   for (int l = l0; l < l1; ++l) waited |= order_after_gate(c, l, st);
-  bool pdl = c->overlap && !waited;
+  bool pdl = may_overlap(c, waited);
   // lengths that stay equal need no copy on the device
   bool uniform = !c->ragged;
   for (int l = l0; l < l1 && uniform; ++l)
@@ -708,6 +751,225 @@ witcert_status witcert_truncate(witcert_cache* c, int layer, const int32_t* leng
     c->len[l] = mx;
     if (moved) ++c->write_gen[l];          // block risks of the longer sequence are stale
   }
+  ok();
+  return WITCERT_OK;
+} WITCERT_NO_THROW
+
+// ------------------------------------------------------------------ forks
+// What every sequence of a fork becomes: its parent (itself: it stays, or is cut; -1: empty), the most
+// tokens it keeps, and how many blocks and KIVI tail rows that is, the longest layer's.
+struct ForkPlan {
+  std::vector<int> from, cap, blocks, tail;
+  std::vector<MoveOp> ops;
+  std::vector<size_t> launches;        // first move of each launch, and their end
+};
+
+static MoveOp fork_move(const ForkPlan& f, int src, int dst, int like, bool rows) {
+  MoveOp op{};
+  op.src = src; op.dst = dst;
+  op.n[0] = op.load[0] = rows ? f.blocks[like] : 0;
+  op.n[1] = op.load[1] = rows ? f.tail[like] : 0;
+  op.blocks = f.blocks[like];
+  op.cap = f.cap[like];
+  return op;
+}
+
+// The moves of a fork in an order in which none reads what an earlier one wrote.  First the sequences
+// that nobody reads any more, source by source, which frees their sources in turn; what is left are
+// cycles, each of which saves one row, moves the others up and hands the saved one out.  A launch holds
+// kMovesPerLaunch moves; a cycle that crosses its end is cut into two that share a sequence, the second
+// of which finds there what the first one saved.
+static void fork_moves(ForkPlan& f) {
+  const int B = (int)f.from.size();
+  std::vector<int> readers(B, 0), first(B + 1, 0), kids, ready, next(B, -1);
+  std::vector<char> done(B, 0);
+  for (int i = 0; i < B; ++i)
+    if (f.from[i] >= 0 && f.from[i] != i) ++readers[f.from[i]];
+  for (int i = 0; i < B; ++i) first[i + 1] = first[i] + readers[i];
+  kids.resize(first[B]);
+  std::vector<int> at(first.begin(), first.end() - 1);
+  for (int i = 0; i < B; ++i) {
+    if (f.from[i] >= 0 && f.from[i] != i) kids[at[f.from[i]]++] = i;
+    if (f.from[i] == i) done[i] = 1;
+  }
+  f.launches.push_back(0);
+  auto room = [&] {
+    if (f.ops.size() - f.launches.back() == kMovesPerLaunch) f.launches.push_back(f.ops.size());
+    return kMovesPerLaunch - (int)(f.ops.size() - f.launches.back());
+  };
+  auto emit = [&](int i) {
+    room();
+    f.ops.push_back(fork_move(f, f.from[i] >= 0 ? f.from[i] : kMoveNone, i, i, f.from[i] >= 0));
+    done[i] = 1;
+  };
+  for (int i = 0; i < B; ++i)
+    if (!done[i] && readers[i] == 0) ready.push_back(i);
+  while (!ready.empty()) {
+    const int i = ready.back(), src = f.from[i];
+    ready.pop_back();
+    if (done[i]) continue;
+    if (src < 0) { emit(i); continue; }
+    for (int k = first[src]; k < first[src + 1]; ++k)          // the source's other free children with it
+      if (!done[kids[k]] && readers[kids[k]] == 0) { emit(kids[k]); --readers[src]; }
+    if (!done[src] && readers[src] == 0) ready.push_back(src);
+  }
+  for (int i = 0; i < B; ++i) {
+    if (done[i]) continue;
+    int last = i;                                              // the sequence that takes i's row
+    for (int j = f.from[i]; j != i; j = f.from[j]) last = j;
+    int to = i;                                                // i <- from(i) <- ... <- last <- i
+    while (!done[last]) {
+      if (room() < 3) f.launches.push_back(f.ops.size());
+      f.ops.push_back(fork_move(f, to, kMoveKept, last, true));
+      f.ops.back().cap = INT_MAX;
+      while (to != last && room() > 1) {
+        emit(to);
+        to = f.from[to];
+      }
+      f.ops.push_back(fork_move(f, kMoveKept, to, last, true));
+      if (to == last) done[last] = 1; else f.ops.back().cap = INT_MAX;
+    }
+  }
+  for (int i = 0; i < B; ++i)                                  // sequences that are only cut, after their readers
+    if (f.from[i] == i && f.cap[i] >= 0) {
+      room();
+      f.ops.push_back(fork_move(f, i, i, i, false));
+    }
+  f.launches.push_back(f.ops.size());
+  // a run of moves from one source in one launch loads once what the largest of them takes
+  for (size_t l = 0; l + 1 < f.launches.size(); ++l)
+    for (size_t m = f.launches[l], to = m; m < f.launches[l + 1]; m = to) {
+      MoveOp most = f.ops[m];
+      for (to = m; to < f.launches[l + 1] && f.ops[to].src == f.ops[m].src; ++to)
+        for (int k = 0; k < 2; ++k) most.load[k] = std::max(most.load[k], f.ops[to].n[k]);
+      for (size_t j = m; j < to; ++j)
+        for (int k = 0; k < 2; ++k) f.ops[j].load[k] = most.load[k];
+    }
+}
+
+// The page table under the moves: the host's copy and the pages' holders.
+static void fork_table(witcert_cache* c, const ForkPlan& f, std::vector<int32_t>& kept) {
+  auto drop = [&](int32_t pg) { if (--c->page_refs[pg] == 0) c->free_pages.push_back(pg); };
+  const int nb = c->nblk_max;
+  int kept_blocks = 0;
+  for (const MoveOp& op : f.ops) {
+    const int32_t* src = op.src >= 0 ? c->table_host.data() + (size_t)op.src * nb : kept.data();
+    if (op.dst == kMoveKept) {
+      for (int b = 0; b < op.blocks; ++b) { kept[b] = src[b]; ++c->page_refs[src[b]]; }
+      kept_blocks = op.blocks;
+      continue;
+    }
+    int32_t* dst = c->table_host.data() + (size_t)op.dst * nb;
+    constexpr int kSpan = 64;                                  // beams share most of their pages
+    for (int b0 = 0; b0 < op.blocks; b0 += kSpan) {
+      const int b1 = std::min(op.blocks, b0 + kSpan);
+      if (memcmp(dst + b0, src + b0, (b1 - b0) * sizeof *dst) == 0) continue;
+      for (int b = b0; b < b1; ++b) {
+        if (dst[b] == src[b]) continue;
+        ++c->page_refs[src[b]];
+        if (dst[b] >= 0) drop(dst[b]);
+        dst[b] = src[b];
+      }
+    }
+    for (int b = op.blocks; b < nb && dst[b] >= 0; ++b) {       // a sequence holds its first blocks, without gaps
+      drop(dst[b]);
+      dst[b] = -1;
+    }
+    if (op.src == kMoveKept) {
+      for (int b = 0; b < kept_blocks; ++b) drop(kept[b]);
+      kept_blocks = 0;
+    }
+  }
+}
+
+witcert_status witcert_fork(witcert_cache* c, const int32_t* parents, const int32_t* lengths, void* stream) try {
+  if (!c || !parents) return fail(WITCERT_EINVAL, "cache and parents must not be NULL");
+  if (c->cfg.max_repair_blocks > 0)
+    return fail(WITCERT_EINVAL, "a gated cache cannot fork: repairs and the backing store belong to one sequence");
+  const int B = c->cfg.batch, L = c->cfg.n_layers;
+  ForkPlan f;
+  f.from.resize(B); f.cap.assign(B, -1); f.blocks.assign(B, 0); f.tail.assign(B, 0);
+  bool any = false, emptied = false;
+  for (int i = 0; i < B; ++i) {
+    const int p = parents[i];
+    if (p < -1 || p >= B) return fail(WITCERT_EINVAL, "the parent of sequence %d must be in [-1, %d) (got %d)", i, B, p);
+    if (lengths && p >= 0 && lengths[i] < 0) return fail(WITCERT_EINVAL, "lengths must be >= 0 (sequence %d: %d)", i, lengths[i]);
+    f.from[i] = p;
+    if (p < 0) { any = emptied = true; f.cap[i] = 0; continue; }
+    const int cap = lengths ? lengths[i] : INT_MAX;
+    bool cut = false;
+    for (int l = 0; l < L; ++l) {
+      const int now = c->slen[l][p], to = std::min(now, cap);
+      cut |= to < now;
+      if (c->scheme == kKivi && to < now && to % kBlk && to / kBlk < now / kBlk)
+        return fail(WITCERT_EINVAL, "layer %d sequence %d: the exact keys of a finished KIVI block are gone; keep a "
+                    "multiple of %d tokens or end within the unfinished block (at %d)", l, p, kBlk, now / kBlk * kBlk);
+      f.blocks[i] = std::max(f.blocks[i], (to + kBlk - 1) / kBlk);
+      f.tail[i] = std::max(f.tail[i], to % kBlk);
+    }
+    // a sequence that stays also gives back the pages past its last token
+    const bool spare = lengths && c->table && p == i && f.blocks[i] < c->nblk_max &&
+                       c->table_host[(size_t)i * c->nblk_max + f.blocks[i]] >= 0;
+    if (p != i || cut || spare) { any = true; f.cap[i] = cap; }
+  }
+  if (!any) { ok(); return WITCERT_OK; }
+  fork_moves(f);
+  // host memory first: nothing may fail between what the device and what the host is told
+  std::vector<std::vector<int>> slen(L, std::vector<int>(B));
+  bool equal = true;
+  for (int l = 0; l < L; ++l)
+    for (int i = 0; i < B; ++i) {
+      const int p = f.from[i], now = p < 0 ? 0 : c->slen[l][p];
+      slen[l][i] = f.cap[i] < 0 ? now : std::min(now, f.cap[i]);
+      equal &= slen[l][i] == slen[l][0];
+    }
+  std::vector<int32_t> kept(c->table ? c->nblk_max : 0);
+  auto st = static_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaSuccess;
+  bool pdl = false;
+  if (!equal) e = enter_ragged(c, st, pdl);
+  MoveRows rows{};
+  auto stream_of = [&](void* base, size_t layer_pitch, size_t head_pitch, int unit, int count) {
+    MoveStream& s = rows.s[rows.n_streams++];
+    s.base = static_cast<uint8_t*>(base);
+    s.layer_pitch = (long long)layer_pitch;
+    s.head_pitch = (long long)head_pitch;
+    s.seq_pitch = (long long)(head_pitch * c->cfg.n_kv_heads);
+    s.unit = unit; s.count = count;
+  };
+  if (!c->table) stream_of(c->blocks, c->layer_blocks, (size_t)c->nblk_max * c->bblk, c->bblk, 0);
+  if (c->vwit) stream_of(c->vwit, vwit_layer(c) * sizeof(__half), backing_rows(c) * sizeof(__half), kVwBytes, 0);
+  if (c->kivi_tail)
+    stream_of(c->kivi_tail, layer_rows(c) * kBlk * kD * sizeof(float), kBlk * kD * sizeof(float), kD * sizeof(float), 1);
+  MoveInts ints{};
+  ints.table = c->table;
+  ints.lens = equal ? nullptr : c->dlen;
+  ints.nblk_max = c->table ? c->nblk_max : 0;
+  ints.layers = equal ? 0 : L;
+  ints.B = B;
+  for (size_t k = 0; k + 1 < f.launches.size() && e == cudaSuccess; ++k) {
+    const size_t m0 = f.launches[k], n = f.launches[k + 1] - m0;
+    rows.n = ints.n = (int)n;
+    std::copy_n(f.ops.data() + m0, n, rows.op);
+    std::copy_n(f.ops.data() + m0, n, ints.op);
+    if (rows.n_streams) e = launch_move_rows(rows, L, c->cfg.n_kv_heads, st);
+    if (e == cudaSuccess && (ints.table || ints.lens)) e = launch_move_ints(ints, st);
+  }
+  // an export is as long as the longest sequence: no value witness of the old occupant shows in it
+  const size_t vrows = (size_t)c->cfg.n_kv_heads * backing_rows(c);
+  for (int i = 0; i < B && emptied && c->vwit; ++i)
+    for (int l = 0; l < L && f.from[i] < 0 && e == cudaSuccess; ++l)
+      e = cudaMemsetAsync(c->vwit + l * vwit_layer(c) + (size_t)i * vrows, 0, vrows * sizeof(__half), st);
+  if (e != cudaSuccess) return cuda_fail(e, "fork");
+  if (c->table) fork_table(c, f, kept);
+  c->slen.swap(slen);
+  c->ragged = !equal;
+  for (int l = 0; l < L; ++l) {
+    c->len[l] = *std::max_element(c->slen[l].begin(), c->slen[l].end());
+    ++c->write_gen[l];
+  }
+  c->last_write_layer = -1;
+  c->lengths_last = c->forked = true;
   ok();
   return WITCERT_OK;
 } WITCERT_NO_THROW
@@ -1066,7 +1328,7 @@ witcert_status witcert_decode(witcert_cache* c, int layer, const void* q, double
     c->prof_free.pop_back();
   }
   // the split kernel reads the sequence lengths before it waits for its predecessor
-  cudaError_t e = launch_decode(c->scheme, a, c->sm_count, st, pp.a, pp.b, c->overlap && !waited && !c->lengths_last);
+  cudaError_t e = launch_decode(c->scheme, a, c->sm_count, st, pp.a, pp.b, may_overlap(c, waited) && !c->lengths_last);
   if (pp.a) c->prof_pending.push_back(pp);
   if (e != cudaSuccess) return cuda_fail(e, "decode launch");
   c->lengths_last = false;
@@ -1109,7 +1371,7 @@ witcert_status witcert_decode_noalloc(witcert_cache* c, int layer, const void* q
     a.risk = c->risk + (size_t)layer * a.B * a.Hq * c->nblk_max;
   }
   a.out = out; a.meter_a = meter_a; a.meter_b = meter_b; a.raw_a = raw_a; a.raw_b = raw_b; a.meter_v = meter_v;
-  e = launch_decode(c->scheme, a, c->sm_count, st, nullptr, nullptr, c->overlap && !waited && !c->lengths_last);
+  e = launch_decode(c->scheme, a, c->sm_count, st, nullptr, nullptr, may_overlap(c, waited) && !c->lengths_last);
   if (e != cudaSuccess) return cuda_fail(e, "decode launch");
   c->lengths_last = false;
   if (gate && meter) c->risk_gen[layer] = c->write_gen[layer];
@@ -1135,7 +1397,7 @@ witcert_status witcert_decode_partial(witcert_cache* c, int layer, const void* q
   a.part = c->part;
   a.part_out = part;
   a.risk_raw = c->risk_raw;      // a gated cache's split kernel writes block risks; the merge keeps none (no a.risk)
-  cudaError_t e = launch_decode(c->scheme, a, c->sm_count, st, nullptr, nullptr, c->overlap && !waited);
+  cudaError_t e = launch_decode(c->scheme, a, c->sm_count, st, nullptr, nullptr, may_overlap(c, waited));
   if (e != cudaSuccess) return cuda_fail(e, "decode launch");
   c->last_write_layer = -1;
   c->last_n_splits = a.n_splits;
@@ -1218,6 +1480,84 @@ witcert_status witcert_gate_select(const float* risk, const uint8_t* repaired, i
   cudaError_t e = cudaMemsetAsync(selected, 0, (size_t)batch * n_kv_heads * (nblk / 32 + 1) * sizeof(uint32_t), st);
   if (e == cudaSuccess) e = launch_gate_select(a, st);
   if (e != cudaSuccess) return cuda_fail(e, "gate selection");
+  ok();
+  return WITCERT_OK;
+}
+
+// ------------------------------------------------------------------ beam search
+// Checks a step and lays out its scan: a warp takes chunks_per_part chunks of a row, one where the rows are
+// few (latency), more where the GPU is full anyway.
+static witcert_status beam_args(const witcert_beam_step* s, BeamArgs& a, size_t& bytes) {
+  if (!s) return fail(WITCERT_EINVAL, "step must not be NULL");
+  if (s->dtype != WITCERT_F32 && s->dtype != WITCERT_BF16) return fail(WITCERT_EINVAL, "unknown dtype %d", (int)s->dtype);
+  if (s->n_requests < 0) return fail(WITCERT_EINVAL, "n_requests must be >= 0");
+  if (s->n_beams < 1 || s->n_beams > kBeamMaxBeams) return fail(WITCERT_EINVAL, "n_beams must be in [1, %d] (got %d)", kBeamMaxBeams, s->n_beams);
+  if (s->vocab < 1 || s->vocab > 1 << 27) return fail(WITCERT_EINVAL, "vocab must be in [1, 2^27] (got %d)", s->vocab);
+  if (s->n_out < 1 || s->n_out > kBeamMaxOut) return fail(WITCERT_EINVAL, "n_out must be in [1, %d] (got %d)", kBeamMaxOut, s->n_out);
+  if (s->eos < -1 || s->eos >= s->vocab) return fail(WITCERT_EINVAL, "eos must be in [-1, %d) (got %d)", s->vocab, s->eos);
+  if (s->finished && s->eos < 0) return fail(WITCERT_EINVAL, "finished beams need eos");
+  const int elem = s->dtype == WITCERT_BF16 ? 2 : 4;
+  const long long rows = (long long)s->n_requests * s->n_beams;
+  if (rows > INT_MAX || (long long)s->n_requests * s->n_out > INT_MAX) return fail(WITCERT_EINVAL, "too many rows (%lld)", rows);
+  const uintptr_t at = (uintptr_t)s->logits;
+  if (at % elem) return fail(WITCERT_EINVAL, "logits must be aligned to their elements");
+  // a row's chunks begin at a 32-byte boundary at or before it
+  const bool even = at % 32 == 0 && (s->n_requests < 2 || s->request_stride * elem % 32 == 0) &&
+                    (s->n_beams < 2 || s->beam_stride * elem % 32 == 0);
+  a.chunks = (int)((s->vocab + (even ? 0 : 32 / elem - 1) + (long long)kBeamChunk - 1) / kBeamChunk);
+  const long long warps = (long long)sm_count_now() * 32;
+  a.chunks_per_part = (int)std::min<long long>(8, std::max<long long>(1, rows * a.chunks / warps));
+  a.parts = (a.chunks + a.chunks_per_part - 1) / a.chunks_per_part;
+  if (rows * a.parts > INT_MAX) return fail(WITCERT_EINVAL, "too many logits (%lld rows of %d)", rows, s->vocab);
+  bytes = (size_t)rows * (a.parts * sizeof(float2) + a.chunks * sizeof(float));
+  a.logits = s->logits;
+  a.request_stride = s->request_stride; a.beam_stride = s->beam_stride;
+  a.scores = s->scores; a.finished = s->finished;
+  a.requests = s->n_requests; a.beams = s->n_beams; a.vocab = s->vocab; a.n_out = s->n_out; a.eos = s->eos;
+  a.is_bf16 = s->dtype == WITCERT_BF16;
+  a.out_scores = s->out_scores; a.rows = s->rows; a.tokens = s->tokens; a.out_finished = s->out_finished;
+  return WITCERT_OK;
+}
+
+witcert_status witcert_beam_workspace(const witcert_beam_step* step, size_t* bytes) {
+  BeamArgs a{};
+  size_t need = 0;
+  if (witcert_status s = beam_args(step, a, need)) return s;
+  if (!bytes) return fail(WITCERT_EINVAL, "bytes must not be NULL");
+  *bytes = need;
+  ok();
+  return WITCERT_OK;
+}
+
+witcert_status witcert_beam_select(const witcert_beam_step* step, void* workspace, size_t workspace_bytes, void* stream) {
+  BeamArgs a{};
+  size_t need = 0;
+  if (witcert_status s = beam_args(step, a, need)) return s;
+  if (a.requests == 0) { ok(); return WITCERT_OK; }
+  if (!a.logits || !a.scores || !a.out_scores || !a.rows || !a.tokens)
+    return fail(WITCERT_EINVAL, "logits, scores, out_scores, rows and tokens must not be NULL");
+  if (a.n_out != a.beams && a.requests > 1 && (a.out_scores == a.scores || (a.finished && a.out_finished == a.finished)))
+    return fail(WITCERT_EINVAL, "outputs may be the inputs only with n_out = n_beams");
+  if (!workspace || workspace_bytes < need || (uintptr_t)workspace % 16)
+    return fail(WITCERT_EINVAL, "the workspace needs %zu bytes, 16-byte aligned, got %zu", need, workspace ? workspace_bytes : 0);
+  a.records = static_cast<float2*>(workspace);
+  a.maxima = reinterpret_cast<float*>(a.records + (size_t)a.requests * a.beams * a.parts);
+  cudaError_t e = launch_beam_select(a, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "beam selection launch");
+  ok();
+  return WITCERT_OK;
+}
+
+witcert_status witcert_beam_paths(const int32_t* rows, const int32_t* tokens, int n_steps, int n_requests, int n_beams,
+                                  const int32_t* length, int pad, int32_t* out, void* stream) {
+  if (n_steps < 0 || n_requests < 0) return fail(WITCERT_EINVAL, "n_steps and n_requests must be >= 0");
+  if (n_beams < 1 || n_beams > kBeamMaxBeams) return fail(WITCERT_EINVAL, "n_beams must be in [1, %d] (got %d)", kBeamMaxBeams, n_beams);
+  if ((long long)n_requests * n_beams > INT_MAX) return fail(WITCERT_EINVAL, "too many rows");
+  if (n_steps == 0 || n_requests == 0) { ok(); return WITCERT_OK; }
+  if (!rows || !tokens || !out) return fail(WITCERT_EINVAL, "rows, tokens and out must not be NULL");
+  PathArgs a{rows, tokens, length, out, n_steps, n_requests, n_beams, pad, 0};
+  cudaError_t e = launch_beam_paths(a, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "beam paths launch");
   ok();
   return WITCERT_OK;
 }
