@@ -1,7 +1,7 @@
 // Beam search: the best continuations of each request, and the token sequences of its beams.
 //
-// Selection.  A live row (request, beam) of logits x and score c offers s_v = c + x_v - lse, lse = log sum
-// exp x.  Two launches:
+// Selection.  A live row (request, beam) of logits x and score c offers s_v = c + x_v - log sum exp x, formed
+// as (c - log sum exp(x - m)) + (x_v - m) with the row's maximum m.  Two launches:
 //
 //   scan   one pass over the logits: for every chunk of kChunk tokens its maximum, for every warp's run of
 //          chunks the maximum m and sum exp(x - m).  Bound by HBM; five lane operations an element.
@@ -10,8 +10,9 @@
 //          chunks' maxima, reads those n chunks again and ranks their elements.  Bound by latency.
 //
 // Ranking goes by a key in 64 bits, (s, lower row, lower token).  Most of the work is a filter in 32 bits:
-// a lower bound of the n-th best key comes from the threads' own maxima, every key that its rounding
-// does not put below that bound is listed, and only the list is formed in 64 bits and ranked by counting.
+// a lower bound of the n-th best key comes from the largest keys of groups of threads, every key that its
+// rounding does not put below that bound is listed, and only the list is formed in 64 bits (whose rate is a
+// 64th of fp32's) and ranked by counting.
 #include <cfloat>
 
 #include "common.cuh"
@@ -23,9 +24,10 @@ namespace {
 
 constexpr int kChunk = kBeamChunk;
 constexpr int kLane = kChunk / 32;               // elements of a chunk a lane holds: 16
-constexpr int kScanWarps = 8;
+constexpr int kScanWarps = 4;
 constexpr int kPickThreads = 1024;
 constexpr int kList = 1024;                      // candidates that are ranked exactly
+constexpr int kMaxGroups = 512;
 constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ float redux_max(float x) {
@@ -36,6 +38,7 @@ __device__ __forceinline__ float redux_max(float x) {
 
 template <typename T>
 struct Row {
+  static constexpr int kWords = kLane * sizeof(T) / 4;         // registers a lane's part of a chunk takes
   const T* x;
   int lead;                  // elements between the 32-byte boundary before the row and the row
   int vocab;
@@ -44,322 +47,545 @@ struct Row {
     lead = (int)((reinterpret_cast<uintptr_t>(x) & 31) / sizeof(T));
     vocab = a.vocab;
   }
-  // First token of lane `lane`'s part of chunk c (may lie outside the row at either end).
-  __device__ int first(int c, int lane) const { return c * kChunk + lane * kLane - lead; }
-  // The lane's sixteen elements; -inf outside the row.
-  __device__ void load(int c, int lane, float (&v)[kLane]) const {
-    const int e0 = first(c, lane);
-    if (e0 >= 0 && e0 <= vocab - kLane) {
-      if constexpr (sizeof(T) == 2) {
-        uint32_t w[8];
-        load8(x + e0, w);
+  // Token of element e of chunk c (may lie outside the row at either end).
+  __device__ int token(int c, int e) const { return c * kChunk + e - lead; }
+  // N words of elements from e of chunk c on, as they lie; -inf outside the row.
+  template <int N>
+  __device__ void load(int c, int e, uint32_t (&w)[N]) const { load_at(x, vocab, token(c, e), w); }
+  template <int N>
+  static __device__ __forceinline__ void load_at(const T* x, int vocab, int t, uint32_t (&w)[N]) {
+    constexpr int n = N * 4 / sizeof(T);
+    if (t >= 0 && t <= vocab - n) {
+      if constexpr (N == 2)
+        asm("ld.global.nc.v2.b32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(x + t));
+      else if constexpr (N == 4)
+        asm("ld.global.nc.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "l"(x + t));
+      else
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          v[2 * k] = __uint_as_float(w[k] << 16);
-          v[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
-        }
-      } else {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t w[8];
-          load8(x + e0 + 8 * h, w);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) v[8 * h + k] = __uint_as_float(w[k]);
-        }
-      }
+        for (int h = 0; h < N; h += 8)
+          asm("ld.global.nc.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+              : "=r"(w[h]), "=r"(w[h + 1]), "=r"(w[h + 2]), "=r"(w[h + 3]), "=r"(w[h + 4]), "=r"(w[h + 5]), "=r"(w[h + 6]), "=r"(w[h + 7])
+              : "l"(x + t + h * 4 / sizeof(T)));
     } else {
 #pragma unroll
-      for (int k = 0; k < kLane; ++k) {
-        const int e = e0 + k;
-        v[k] = e >= 0 && e < vocab ? to_f32(x[e]) : -INFINITY;
+      for (int k = 0; k < N; ++k) {
+        if constexpr (sizeof(T) == 2) w[k] = bits(x, vocab, t + 2 * k) | bits(x, vocab, t + 2 * k + 1) << 16;
+        else w[k] = bits(x, vocab, t + k);
       }
     }
   }
-  static __device__ __forceinline__ void load8(const T* p, uint32_t (&w)[8]) {
-    asm volatile("ld.global.nc.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7]) : "l"(p));
+  static __device__ __forceinline__ uint32_t bits(const T* x, int vocab, int t) {
+    const bool in = t >= 0 && t < vocab;
+    if constexpr (sizeof(T) == 2) return in ? reinterpret_cast<const uint16_t*>(x)[t] : 0xFF80u;
+    else return in ? reinterpret_cast<const uint32_t*>(x)[t] : 0xFF800000u;
+  }
+  // Element k of loaded words.
+  template <int N>
+  static __device__ __forceinline__ float value(const uint32_t (&w)[N], int k) {
+    if constexpr (sizeof(T) == 2) return __uint_as_float(k & 1 ? w[k / 2] & 0xFFFF0000u : w[k / 2] << 16);
+    else return __uint_as_float(w[k]);
   }
 };
 
 // A row takes part while its score is finite; a finished one offers only itself.
 __device__ __forceinline__ bool live(float score) { return fabsf(score) <= FLT_MAX; }
 
+// s + x as a rounded sum and what the rounding dropped.
+__device__ __forceinline__ void two_sum(float& s, float& lost, float x) {
+  const float t = s + x, back = t - s;
+  lost += (s - (t - back)) + (x - back);
+  s = t;
+}
+
+// A warp's chunks on their way: each lane copies its own pieces of a chunk to shared memory and reads them back
+// itself, so that a wait for the lane's own copies is all there is to wait for.
+constexpr int kRing = 4 * 1024;                  // bytes of a warp's chunks in shared memory
 template <typename T>
-__global__ void __launch_bounds__(kScanWarps * 32) beam_scan_kernel(const __grid_constant__ BeamArgs a) {
-  pdl_trigger();
+struct Ring {
+  static constexpr int kBytes = kChunk * sizeof(T), kPieces = kBytes / 512, kStages = kRing / kBytes, kPiece = 16 / sizeof(T);
+  uint32_t at;               // shared address of the lane's first piece
+  int lane;
+  // Copies chunk c of the row; from = where the lane's first piece lies in it.
+  __device__ __forceinline__ void fetch(const Row<T>& row, const T* from, int c, int stage) const {
+    const uint32_t to = at + stage * kBytes;
+    if (c > 0 && row.token(c, kChunk) <= row.vocab) {          // all of it in the row
+#pragma unroll
+      for (int k = 0; k < kPieces; ++k)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + k * 512), "l"(from + k * 32 * kPiece) : "memory");
+    } else {
+#pragma unroll 1
+      for (int k = 0; k < kPieces; ++k) {
+        uint32_t w[4];
+        Row<T>::load_at(row.x, row.vocab, row.token(c, (k * 32 + lane) * kPiece), w);
+        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(to + k * 512), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
+      }
+    }
+  }
+  __device__ static void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+  __device__ __forceinline__ void take(int stage, uint32_t (&w)[Row<T>::kWords]) const {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+#pragma unroll
+    for (int k = 0; k < kPieces; ++k)
+      asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(w[4 * k]), "=r"(w[4 * k + 1]), "=r"(w[4 * k + 2]),
+                   "=r"(w[4 * k + 3]) : "r"(at + stage * kBytes + k * 512) : "memory");
+  }
+};
+
+// Two floats in a register pair.
+using f32x2 = unsigned long long;
+__device__ __forceinline__ f32x2 pair(float lo, float hi) {
+  f32x2 p;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(lo), "f"(hi));
+  return p;
+}
+__device__ __forceinline__ float low(f32x2 p) { return __uint_as_float((uint32_t)p); }
+__device__ __forceinline__ float high(f32x2 p) { return __uint_as_float((uint32_t)(p >> 32)); }
+__device__ __forceinline__ f32x2 fma_pair(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ f32x2 add_pair(f32x2 a, f32x2 b) {
+  f32x2 d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ f32x2 ex2_pair(f32x2 a) { return pair(ex2(low(a)), ex2(high(a))); }
+
+// The largest of a lane's words of logits (NaN where there is nothing else).
+template <typename T, int N>
+__device__ __forceinline__ float largest(const uint32_t (&w)[N]) {
+  if constexpr (sizeof(T) == 2) {
+    auto bf = [](uint32_t x) { return *reinterpret_cast<__nv_bfloat162*>(&x); };
+    __nv_bfloat162 m = bf(w[0]);
+#pragma unroll
+    for (int k = 1; k < N; ++k) m = __hmax2(m, bf(w[k]));
+    return fmaxf(__low2float(m), __high2float(m));
+  } else {
+    float m = __uint_as_float(w[0]);
+#pragma unroll
+    for (int k = 1; k < N; ++k) m = fmaxf(m, __uint_as_float(w[k]));
+    return m;
+  }
+}
+
+// A lane's part of the sum of exp(x - m), m the largest logit its warp has seen.  The exponents are x log2 e - R
+// with R = m log2 e rounded once: a fused product loses nothing, and what R lost, below 2^-8 and the same for
+// every term, goes back in at the end.
+struct LaneSum {
+  float m = -INFINITY, R = 0.f, sum = 0.f, lost = 0.f;         // sum + lost = sum 2^(x log2 e - R)
+  bool far = false;                                            // a huge maximum: differences instead
+  __device__ __forceinline__ void raise(float top) {
+    const bool now = !(fabsf(top) < 0x1p16f);
+    const float to = now ? 0.f : top * kLog2e;
+    const float f = m == -INFINITY ? 1.f : far || now ? ex2((m - top) * kLog2e) : ex2(R - to);
+    sum *= f; lost *= f;                                       // before any maximum the sum is 0 (or NaN)
+    m = top; R = to; far = now;
+  }
+  // Pairs of logits at a time: one instruction for two products, and for two sums.
+  template <int N>
+  __device__ __forceinline__ void add(const f32x2 (&v)[N]) {
+    f32x2 e[N];
+    const f32x2 scale = pair(kLog2e, kLog2e);
+    if (far) {                                                 // inf - inf is NaN, and so is the row's sum
+#pragma unroll
+      for (int k = 0; k < N; ++k) e[k] = ex2_pair(fma_pair(add_pair(v[k], pair(-m, -m)), scale, pair(0.f, 0.f)));
+    } else {                                                   // zeros, or NaN, while there is nothing but -inf
+#pragma unroll
+      for (int k = 0; k < N; ++k) e[k] = ex2_pair(fma_pair(v[k], scale, pair(-R, -R)));
+    }
+#pragma unroll
+    for (int h = N / 2; h > 0; h /= 2)
+#pragma unroll
+      for (int k = 0; k < h; ++k) e[k] = add_pair(e[k], e[k + h]);
+    two_sum(sum, lost, low(e[0]) + high(e[0]));
+  }
+  __device__ __forceinline__ float total() const {
+    return (sum + lost) * (far || m == -INFINITY ? 1.f : ex2(-__fmaf_rn(m, kLog2e, -R)));
+  }
+};
+
+template <typename T>
+__global__ void __launch_bounds__(kScanWarps * 32, kBeamScanWarps / kScanWarps) beam_scan_kernel(const __grid_constant__ BeamArgs a) {
+  __shared__ __align__(16) uint8_t held[kScanWarps * kRing];
   const int lane = threadIdx.x & 31;
-  const long long wid = (long long)blockIdx.x * kScanWarps + (threadIdx.x >> 5);
-  const long long row = wid / a.parts;
-  if (row >= (long long)a.requests * a.beams) return;
-  const int part = (int)(wid - row * a.parts), r = (int)(row / a.beams), w = (int)(row % a.beams);
+  const uint32_t wid = blockIdx.x * kScanWarps + (threadIdx.x >> 5), row = wid / (uint32_t)a.parts;
+  if (row >= (uint32_t)a.requests * a.beams) return;
+  const int part = (int)(wid - row * a.parts), r = (int)(row / (uint32_t)a.beams), w = (int)(row - r * (uint32_t)a.beams);
   if (!live(a.scores[row]) || (a.finished && a.finished[row])) return;
   const Row<T> x(a, r, w);
-  float* maxima = a.maxima + row * a.chunks;
-  float m = -INFINITY, sum = 0.f, lost = 0.f;                  // of this lane: sum + lost = sum exp(x - m)
-  const int c1 = min(a.chunks, (part + 1) * a.chunks_per_part);
-  for (int c = part * a.chunks_per_part; c < c1; ++c) {
-    float v[kLane];
-    x.load(c, lane, v);
-    float top = v[0];
+  float* maxima = a.maxima + (size_t)row * a.chunks;
+  LaneSum l;
+  // every parts-th chunk: the row's warps read side by side
+  const Ring<T> ring{smem_addr(held) + (threadIdx.x >> 5) * kRing + lane * 16, lane};
+  constexpr int kStages = Ring<T>::kStages;
+  const T* from = x.x + x.token(part, lane * Ring<T>::kPiece);
+  const long long step = (long long)a.parts * kChunk;
+  int ahead = part;
+  auto fetch = [&](int stage) {
+    if (ahead < a.chunks) ring.fetch(x, from, ahead, stage);
+    ring.commit();
+    ahead += a.parts;
+    from += step;
+  };
 #pragma unroll
-    for (int k = 1; k < kLane; ++k) top = fmaxf(top, v[k]);
-    const float most = redux_max(top);
-    if (lane == 0) maxima[c] = most;
-    if (top > m) {
-      const float f = ex2((m - top) * kLog2e);                 // 0 for the first
-      sum *= f; lost *= f;
-      m = top;
+  for (int u = 0; u < kStages - 1; ++u) fetch(u);
+  for (int c = part; c < a.chunks;) {
+#pragma unroll
+    for (int stage = 0; stage < kStages; ++stage) {
+      fetch(stage ? stage - 1 : kStages - 1);                  // the stage read last
+      uint32_t raw[Row<T>::kWords];
+      ring.take(stage, raw);
+      const float most = redux_max(largest<T>(raw));
+      if (lane == 0) maxima[c] = most;
+      if (most > l.m) l.raise(most);
+      f32x2 v[kLane / 2];
+#pragma unroll
+      for (int k = 0; k < kLane / 2; ++k) v[k] = pair(Row<T>::value(raw, 2 * k), Row<T>::value(raw, 2 * k + 1));
+      l.add(v);
+      c += a.parts;
+      if (c >= a.chunks) break;
     }
-    // exponents relative to the lane's maximum: differences of logits, which lose nothing next to it; a
-    // lane that has seen only -inf adds zeros, and +inf or NaN anywhere makes the row's sum NaN
-    const float ref = m == -INFINITY ? 0.f : m;
-    float e[kLane];
-#pragma unroll
-    for (int k = 0; k < kLane; ++k) e[k] = ex2((v[k] - ref) * kLog2e);
-#pragma unroll
-    for (int h = kLane / 2; h > 0; h /= 2)
-#pragma unroll
-      for (int k = 0; k < h; ++k) e[k] += e[k + h];
-    const float s = sum + e[0], back = s - sum;                // two-sum: the running sum keeps its rounding
-    lost += (sum - (s - back)) + (e[0] - back);
-    sum = s;
   }
-  const float top = redux_max(m), ref = top == -INFINITY ? 0.f : top;
-  sum = (sum + lost) * (m == -INFINITY ? (sum == 0.f ? 0.f : NAN) : ex2((m - ref) * kLog2e));
+  // not before: the next kernel's blocks would take registers that scan blocks still to come need
+  pdl_trigger();
+  float sum = l.total();
 #pragma unroll
   for (int o = 16; o > 0; o /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (lane == 0) a.records[wid] = make_float2(top, sum);
+  if (lane == 0) a.records[wid] = make_float2(l.m, sum);
 }
 
 // ------------------------------------------------------------------ pick
-__device__ __forceinline__ uint32_t ordered(float x) {
-  const uint32_t b = __float_as_uint(x);
-  return b & 0x80000000u ? ~b : b | 0x80000000u;
-}
 __device__ __forceinline__ unsigned long long ordered(double x) {
-  const unsigned long long b = (unsigned long long)__double_as_longlong(x + 0.0);   // one zero
+  const unsigned long long b = (unsigned long long)__double_as_longlong(x);
   return b >> 63 ? ~b : b | 1ull << 63;
 }
-
-struct Key {                 // larger s first, then lower place (row << 32 | token, or chunk)
-  unsigned long long s, place;
-};
-__device__ __forceinline__ bool before(const Key& x, const Key& y) { return x.s != y.s ? x.s > y.s : x.place < y.place; }
-
-struct PickShared {
-  Key key[kList];
-  uint32_t id[kList];
-  uint32_t best[kBeamMaxOut];          // chosen ids, in order
-  Key best_key[kBeamMaxOut];
-  double lse[kBeamMaxBeams];
-  float score[kBeamMaxBeams];
-  uint8_t state[kBeamMaxBeams];        // 0 no candidates, 1 live, 2 finished
-  int count, got;
-  uint32_t top;
-  float size;                          // bound of |score| + |lse| over the rows
-};
-
-// The n first of the keys that Keys::each(visit) gives this thread as visit(s, id), s within Keys' rounding
-// of the key's score; Keys::exact(id) is the key.  They end up in sh.best in order; returns how many there
-// are.  Called by the whole CTA.
-template <class Keys>
-__device__ int pick_best(PickShared& sh, const Keys& keys, int n) {
-  const int tid = threadIdx.x, lane = tid & 31;
-  float mine = -INFINITY;
-  keys.each([&](float s, uint32_t) { mine = fmaxf(mine, s); });
-  const uint32_t my = mine == -INFINITY ? 0u : ordered(mine);
-  if (tid == 0) { sh.count = 0; sh.top = 0u; }
-  __syncthreads();
-  const uint32_t wtop = __reduce_max_sync(0xffffffffu, my);
-  if (lane == 0 && wtop) atomicMax(&sh.top, wtop);
-  // the largest bound that n threads' maxima reach (all keys, if fewer threads have one), by halving
-  uint32_t lo = 1u;
-  if (__syncthreads_count(my != 0u) > n) {
-    uint32_t hi = sh.top;                                      // count(>= lo) >= n, sought in [lo, hi]
-    while (lo < hi) {
-      const uint32_t mid = lo + (hi - lo + 1) / 2;
-      const int c = __syncthreads_count(my >= mid);
-      if (c >= n) lo = mid; else hi = mid - 1;
-      if (c == n) break;
-    }
-  }
-  // keys within twice the rounding of the bound may still be first
-  const float bound = lo == 1u ? -INFINITY : __uint_as_float(lo & 0x80000000u ? lo & 0x7FFFFFFFu : ~lo);
-  const float off = 0x1p-20f * (fabsf(bound) + 2.f * sh.size);
-  const float from = bound - off > -INFINITY ? bound - off : -FLT_MAX;     // also where that is no number
-  keys.each([&](float s, uint32_t id) {
-    if (s >= from) {
-      const int at = atomicAdd(&sh.count, 1);
-      if (at < kList) sh.id[at] = id;
-    }
-  });
-  __syncthreads();
-  int listed = sh.count;
-  if (listed > kList) {
-    // Very many equal or nearly equal keys: halve the space of the keys themselves, which are distinct.
-    unsigned __int128 low = 0, high = ~(unsigned __int128)0;   // count(>= low) > kList, count(> high) < n
-    for (;;) {
-      const unsigned __int128 mid = low + (high - low) / 2 + 1;
-      __syncthreads();
-      if (tid == 0) sh.count = 0;
-      __syncthreads();
-      int c = 0;
-      keys.each([&](float s, uint32_t id) {
-        if (s < from) return;
-        const Key k = keys.exact(id);
-        c += ((unsigned __int128)k.s << 64 | ~k.place) >= mid;
-      });
-      c = __reduce_add_sync(0xffffffffu, c);
-      if (lane == 0 && c) atomicAdd(&sh.count, c);
-      __syncthreads();
-      c = sh.count;
-      if (c < n) high = mid - 1; else low = mid;
-      if (c >= n && c <= kList) break;
-    }
-    __syncthreads();
-    if (tid == 0) sh.count = 0;
-    __syncthreads();
-    keys.each([&](float s, uint32_t id) {
-      if (s < from) return;
-      const Key k = keys.exact(id);
-      if (((unsigned __int128)k.s << 64 | ~k.place) >= low) sh.id[atomicAdd(&sh.count, 1)] = id;
-    });
-    __syncthreads();
-    listed = sh.count;
-  }
-  for (int i = tid; i < listed; i += kPickThreads) sh.key[i] = keys.exact(sh.id[i]);
-  __syncthreads();
-  // a key's rank is the number of keys before it: a warp counts for one key at a time
-  for (int i = tid >> 5; i < listed; i += kPickThreads / 32) {
-    const Key k = sh.key[i];
-    int rank = 0;
-    for (int j = lane; j < listed; j += 32) rank += before(sh.key[j], k);
-    rank = __reduce_add_sync(0xffffffffu, rank);
-    if (lane == 0 && rank < n) {
-      sh.best[rank] = sh.id[i];
-      sh.best_key[rank] = k;
-    }
-  }
-  __syncthreads();
-  return min(listed, n);
+__device__ __forceinline__ double unordered(unsigned long long k) {
+  return __longlong_as_double((long long)(k >> 63 ? k & ~(1ull << 63) : ~k));
 }
 
-// Chunk maxima of a request: id = beam * chunks + chunk.
-struct ChunkKeys {
-  const BeamArgs& a;
-  const PickShared& sh;
-  const float* maxima;
-  __device__ float value(int w, int c) const { return sh.state[w] == 2 ? (c == 0 ? 0.f : -INFINITY) : maxima[(size_t)w * a.chunks + c]; }
-  template <class V> __device__ void each(V&& visit) const {
-    for (int w = 0; w < a.beams; ++w) {
-      if (sh.state[w] == 0) continue;
-      const float score = sh.score[w], lse = (float)sh.lse[w];
-      const int end = sh.state[w] == 2 ? 1 : a.chunks;
-      // rows start at different threads, so that the threads' shares are alike
-      for (int c = (threadIdx.x + w * 416) % kPickThreads; c < end; c += kPickThreads) {
-        const float x = value(w, c);
-        if (x > -INFINITY) visit(fmaxf(score + (x - lse), -FLT_MAX), (uint32_t)w * a.chunks + c);
-      }
-    }
-  }
-  __device__ Key exact(uint32_t id) const {
-    const int w = id / a.chunks, c = id % a.chunks;
-    return {ordered((double)sh.score[w] + ((double)value(w, c) - sh.lse[w])), id};
-  }
+constexpr int kPickWarps = kPickThreads / 32;
+constexpr int kPer = 4;                          // keys a thread looks at together
+constexpr int kAhead = 4;                        // such rounds whose loads are in flight together, where there are more
+
+template <typename T>
+struct alignas(16) Chosen {  // a chosen chunk
+  const T* x;                // its row
+  int first;                 // the token of its element 0, which may lie before the row
+  float least;               // logits below this are no candidates; +inf: a finished row
+};
+template <typename T>
+struct PickShared {
+  unsigned __int128 key[kList];                  // listed: a logit's bits above its place; then the score above ~place
+  Chosen<T> chunk[kBeamMaxOut];
+  int row[kBeamMaxOut];                          // the chosen chunks' beams
+  double base[kBeamMaxBeams];                    // score - log sum exp(x - top): a logit's key is base + (x - top)
+  float mine[kPickThreads + kPickWarps];         // threads' largest keys, a warp's behind the other at 33 words
+  float group[kMaxGroups];
+  float base32[kBeamMaxBeams], score[kBeamMaxBeams], top[kBeamMaxBeams], log_sum[kBeamMaxBeams];
+  int exponent[kBeamMaxBeams], state[kBeamMaxBeams];     // state: 0 no candidates, 1 live, 2 finished
+  int count;
+  float bound, size;                             // size: the largest |base|
 };
 
-// Elements of the chosen chunks: id = place among the chosen * kChunk + element.
 template <typename T>
-struct TokenKeys {
+struct Pick {
   const BeamArgs& a;
-  const PickShared& sh;
-  const uint32_t* chunk;               // the chosen chunks' ids
-  int n, r;
-  template <class V> __device__ void each(V&& visit) const {
-    const int lane = threadIdx.x & 31;
-    for (int k = threadIdx.x >> 5; k < n; k += kPickThreads / 32) {
-      const int w = chunk[k] / a.chunks, c = chunk[k] % a.chunks;
-      const float score = sh.score[w], lse = (float)sh.lse[w];
-      if (sh.state[w] == 2) {
-        if (lane == 0) visit(score, (uint32_t)k * kChunk);
-        continue;
+  PickShared<T>& sh;
+  int r, n;
+  int tid, warp, lane;
+
+  // The least key in 32 bits that may belong to a key which reaches the bound: either is off by at most 2^-23 of
+  // |key| + size.
+  __device__ __forceinline__ float from() const {
+    const float f = sh.bound - 0x1p-20f * (fabsf(sh.bound) + sh.size);
+    return f > -INFINITY ? f : -FLT_MAX;                       // also where that is no number
+  }
+  __device__ __forceinline__ static float key32(float base, float top, float x) { return fmaxf(base + (x - top), -FLT_MAX); }
+  __device__ __forceinline__ unsigned long long key(float x, int w) const { return ordered(sh.base[w] + ((double)x - (double)sh.top[w])); }
+
+  // A bound that n keys reach, from the threads' largest ones: groups of threads, a third more of them than n,
+  // have their largest key each, and the n-th largest of these is the bound (-inf if fewer groups than n have
+  // one).  About G log(G / (G - n)) keys reach it when they are spread at random: 9 for n = 8, 89 for n = 64.
+  // The threads of a group are of different warps, so that few keys fill many groups.
+  __device__ __forceinline__ void bound(float mine) const {
+    sh.mine[tid + warp] = mine;
+    __syncthreads();
+    float g = sh.mine[lane * 33 + warp];
+    if (n <= 24) {                                             // 32 groups, one a warp
+      g = redux_max(g);
+      if (lane == 0) sh.group[warp] = g;
+      __syncthreads();
+      const float o = sh.group[lane], v = sh.group[warp];
+      if (__popc(__ballot_sync(0xffffffffu, o > v || (o == v && lane < warp))) == n - 1 && lane == 0) sh.bound = v;
+    } else {
+      const int width = n <= 96 ? 8 : 2, groups = kPickThreads / width, k = tid / width;
+      for (int o = width / 2; o > 0; o /= 2) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
+      if (lane % width == 0) sh.group[k] = g;
+      __syncthreads();
+      int rank = 0;                                            // the group's own threads count for it
+#pragma unroll 4
+      for (int j = tid % width; j < groups; j += width) {
+        const float o = sh.group[j];
+        rank += (int)(o > g) | ((int)(o == g) & (int)(j < k));
       }
-      float v[kLane];
-      Row<T>(a, r, w).load(c, lane, v);
+      for (int o = width / 2; o > 0; o /= 2) rank += __shfl_xor_sync(0xffffffffu, rank, o);
+      if (rank == n - 1 && lane % width == 0) sh.bound = g;
+    }
+    __syncthreads();
+  }
+
+  // Lists a candidate: its logit x, and place = beam << 32 | chunk's number or token.
+  __device__ __forceinline__ void add(float x, unsigned long long place) const {
+    const int at = atomicAdd(&sh.count, 1);
+    if (at < kList) sh.key[at] = (unsigned __int128)__float_as_uint(x) << 64 | place;
+  }
+  __device__ __forceinline__ unsigned __int128 exact(unsigned __int128 k) const {
+    const unsigned long long place = (unsigned long long)k;
+    return (unsigned __int128)key(__uint_as_float((uint32_t)(k >> 64)), (int)(place >> 32)) << 64 | ~place;
+  }
+
+  // Ranks the listed keys and calls put(rank, s, place) on one thread for each of the n first; each(visit) visits
+  // all candidates again, where more were listed than fit.  Returns how many there are.
+  template <class Each, class Put>
+  __device__ __forceinline__ int rank(Each&& each, Put&& put) const {
+    __syncthreads();
+    int listed = sh.count;
+    if (listed > kList) {
+      // Very many equal or nearly equal keys: halve the space of the keys themselves, which are distinct.
+      unsigned __int128 low = 0, high = ~(unsigned __int128)0; // count(>= low) > kList, count(> high) < n
+      do {
+        const unsigned __int128 mid = low + (high - low) / 2 + 1;
+        __syncthreads();
+        if (tid == 0) sh.count = 0;
+        __syncthreads();
+        each([&](float x, unsigned long long place) {
+          if (exact((unsigned __int128)__float_as_uint(x) << 64 | place) >= mid) add(x, place);
+        });
+        __syncthreads();
+        listed = sh.count;
+        if (listed < n) high = mid - 1; else low = mid;
+      } while (listed < n || listed > kList);
+    }
+    for (int i = tid; i < listed; i += kPickThreads) sh.key[i] = exact(sh.key[i]);
+    __syncthreads();
+    // a key's rank is the number of keys before it: eight lanes count for one key at a time
+    for (int i = tid / 8; i - tid % 32 / 8 < listed; i += kPickThreads / 8) {
+      const unsigned __int128 k = i < listed ? sh.key[i] : 0;
+      int rank = 0;
+#pragma unroll 2
+      for (int j = tid % 8; j < listed; j += 8) rank += sh.key[j] > k;
 #pragma unroll
-      for (int e = 0; e < kLane; ++e)
-        if (v[e] > -INFINITY) visit(fmaxf(score + (v[e] - lse), -FLT_MAX), (uint32_t)k * kChunk + lane * kLane + e);
+      for (int o = 4; o > 0; o /= 2) rank += __shfl_xor_sync(0xffffffffu, rank, o);
+      if (tid % 8 == 0 && i < listed && rank < n) put(rank, (unsigned long long)(k >> 64), ~(unsigned long long)k);
+    }
+    return min(listed, n);
+  }
+
+  // ---- the chunks' maxima: number beam * chunks + chunk, a thread takes every kPickThreads-th
+  __device__ __forceinline__ int row_of(uint32_t i) const {    // i / chunks
+    const uint32_t q = __umulhi(i, a.chunks_inv);
+    return q + (i - q * a.chunks >= (uint32_t)a.chunks);
+  }
+  __device__ __forceinline__ void load_maxima(const float* maxima, int keys, int i0, float (&x)[kPer]) const {
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) x[e] = i0 + e * kPickThreads < keys ? maxima[i0 + e * kPickThreads] : -INFINITY;
+  }
+  // visit(key32, logit, place) of those among x that count.
+  template <class V>
+  __device__ __forceinline__ void each_chunk(int keys, int i0, const float (&x)[kPer], V&& visit) const {
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+      const int i = i0 + e * kPickThreads;
+      if (i >= keys) break;
+      const int w = row_of(i), state = sh.state[w];
+      float v = x[e];
+      if (state == 2) v = i == w * a.chunks ? 0.f : -INFINITY; // a finished row has one candidate: itself
+      if (state == 0 || !(v > -INFINITY)) continue;
+      visit(key32(sh.base32[w], sh.top[w], v), v, (unsigned long long)w << 32 | (uint32_t)i);
     }
   }
-  __device__ Key exact(uint32_t id) const {
-    const int k = id / kChunk, w = chunk[k] / a.chunks, c = chunk[k] % a.chunks;
-    if (sh.state[w] == 2) return {ordered((double)sh.score[w]), (unsigned long long)w << 32 | (uint32_t)a.eos};
-    const Row<T> x(a, r, w);
-    const int token = x.first(c, 0) + (int)(id % kChunk);
-    return {ordered((double)sh.score[w] + ((double)to_f32(x.x[token]) - sh.lse[w])), (unsigned long long)w << 32 | (uint32_t)token};
+
+  // ---- elements of the chosen chunks; a thread takes four adjacent ones, a warp a quarter of a chunk
+  static constexpr int kWords = kPer * sizeof(T) / 4;
+  // visit(raw, i, chunk) for the thread's elements i .. i + 3 of the chosen chunks (i counts through all of them).
+  template <class V>
+  __device__ __forceinline__ void each_four(int chosen, V&& visit) const {
+    for (int i0 = tid * kPer; i0 < chosen * kChunk; i0 += kAhead * kPer * kPickThreads) {
+      uint32_t raw[kAhead][kWords];
+      Chosen<T> c[kAhead];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int i = i0 + u * kPer * kPickThreads;
+        if (i >= chosen * kChunk) break;
+        c[u] = sh.chunk[i / kChunk];
+        if (c[u].least < INFINITY) Row<T>::load_at(c[u].x, a.vocab, c[u].first + i % kChunk, raw[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int i = i0 + u * kPer * kPickThreads;
+        if (i >= chosen * kChunk) break;
+        if (c[u].least < INFINITY) visit(raw[u], i, c[u]);
+      }
+    }
+  }
+  // Logits of chunk k below this are below `from` whatever was rounded; next to huge logits none are.
+  __device__ __forceinline__ float least(int k, float from) const {
+    const int w = sh.row[k];
+    const float d = from - sh.base32[w], l = (d + sh.top[w]) - 0x1p-21f * (fabsf(d) + fabsf(sh.top[w]));
+    return sh.state[w] == 2 ? INFINITY : l >= -FLT_MAX ? fminf(l, FLT_MAX) : -FLT_MAX;
+  }
+  // visit(logit, place) of the tokens that reach their chunk's least logit.
+  template <class V>
+  __device__ __forceinline__ void each_token(int chosen, V&& visit) const {
+    each_four(chosen, [&](const uint32_t (&raw)[kWords], int i, const Chosen<T>& c) {
+      float v[kPer];
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) v[e] = Row<T>::value(raw, e);
+      if (!(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])) >= c.least)) return;
+      const unsigned long long w = (unsigned long long)sh.row[i / kChunk] << 32;
+#pragma unroll
+      for (int e = 0; e < kPer; ++e)
+        if (v[e] >= c.least) visit(v[e], w | (uint32_t)(c.first + i % kChunk + e));
+    });
+    if (tid < chosen && sh.state[sh.row[tid]] == 2) visit(0.f, (unsigned long long)sh.row[tid] << 32 | (uint32_t)a.eos);
   }
 };
 
 template <typename T>
-__global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_constant__ BeamArgs a) {
-  extern __shared__ __align__(16) uint8_t smem[];
-  PickShared& sh = *reinterpret_cast<PickShared*>(smem);
-  uint32_t* chunk = reinterpret_cast<uint32_t*>(smem + sizeof(PickShared));
-  const int r = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
-  if (tid == 0) sh.size = 0.f;
+__global__ void __launch_bounds__(kPickThreads, 1) beam_pick_kernel(const __grid_constant__ BeamArgs a) {
+  __shared__ __align__(16) PickShared<T> sh;
+  const int r = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, n = a.n_out;
+  const Pick<T> p{a, sh, r, n, tid, warp, lane};
+  if (tid == 0) { sh.size = 0.f; sh.bound = -INFINITY; sh.count = 0; }
+  if (tid < a.beams) {
+    const long long row = (long long)r * a.beams + tid;
+    sh.score[tid] = a.scores[row];
+    sh.state[tid] = !live(a.scores[row]) ? 0 : a.finished && a.finished[row] ? 2 : 1;
+  }
+  if (tid < n) {                                               // places that no candidate takes
+    const long long to = (long long)r * n + tid;
+    a.rows[to] = -1;
+    a.tokens[to] = -1;
+  }
   __syncthreads();
   pdl_wait();
-  // the rows' sums: a warp a row
-  for (int w = tid >> 5; w < a.beams; w += kPickThreads / 32) {
-    const long long row = (long long)r * a.beams + w;
-    const float score = a.scores[row];
-    int state = !live(score) ? 0 : a.finished && a.finished[row] ? 2 : 1;
-    double lse = 0.0;
-    if (state == 1) {
-      const float2* rec = a.records + row * a.parts;
-      float top = -INFINITY;
-      for (int p = lane; p < a.parts; p += 32) top = fmaxf(top, rec[p].x);
-      top = redux_max(top);
-      double sum = 0.0;
-      for (int p = lane; p < a.parts; p += 32)
-        sum += (double)(rec[p].x > -INFINITY ? rec[p].y * ex2((rec[p].x - top) * kLog2e) : rec[p].y);
+  const float* maxima = a.maxima + (size_t)r * a.beams * a.chunks;
+  const int keys = a.beams * a.chunks;
+  float x[kPer];                                               // a thread's first keys stay in registers
+  p.load_maxima(maxima, keys, tid, x);
+  // the rows' sums, a warp a row
+  for (int w = warp; w < a.beams; w += kPickWarps) {
+    const float2* rec = a.records + ((long long)r * a.beams + w) * a.parts;
+    float2 v = lane < a.parts ? rec[lane] : make_float2(-INFINITY, 0.f);     // not written for rows that do not count
+    float top = v.x, sum = 0.f, lost = 0.f;
+    for (int k = lane + 32; k < a.parts; k += 32) top = fmaxf(top, rec[k].x);
+    top = redux_max(top);
+    for (int k = lane;;) {
+      two_sum(sum, lost, v.x > -INFINITY ? v.y * ex2((v.x - top) * kLog2e) : v.y);
+      k += 32;
+      if (k >= a.parts) break;
+      v = rec[k];
+    }
 #pragma unroll
-      for (int o = 16; o > 0; o /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      // no softmax: nothing but -inf, or +inf or NaN among the logits
-      if (!(sum > 0.0) || !(fabsf(top) <= FLT_MAX)) state = 0;
-      else lse = (double)top + log(sum);
+    for (int o = 16; o > 0; o /= 2) {
+      const float s = __shfl_xor_sync(0xffffffffu, sum, o);
+      lost += __shfl_xor_sync(0xffffffffu, lost, o);
+      two_sum(sum, lost, s);
     }
-    if (lane == 0) {
-      sh.score[w] = score;
-      sh.lse[w] = lse;
-      sh.state[w] = (uint8_t)state;
+    // log sum = exponent log 2 + log of a fraction about 1 (2^-25 off) + the sum's dropped part
+    const int e = (int)(__float_as_uint(sum * 1.41421356f) >> 23) - 127;
+    const float log_f = logf(__uint_as_float(__float_as_uint(sum) - ((uint32_t)e << 23))) + __fdividef(lost, sum);
+    int state = sh.state[w];
+    // no softmax: nothing but -inf, or +inf or NaN among the logits
+    if (state == 1 && (!(sum > 0.f) || !(fabsf(top) <= FLT_MAX))) state = 0;
+    if (lane == 0 && state) {
+      const bool done = state == 2;
+      const float base = done ? sh.score[w] : sh.score[w] - ((float)e * 0.693147181f + log_f);
+      sh.top[w] = done ? 0.f : top;
+      sh.exponent[w] = done ? 0 : e;
+      sh.log_sum[w] = done ? 0.f : log_f;
+      sh.base32[w] = base;
       // non-negative floats order like their bits
-      if (state) atomicMax(reinterpret_cast<int*>(&sh.size), __float_as_int(fminf(fabsf(score) + (float)fabs(lse), FLT_MAX)));
+      atomicMax(reinterpret_cast<int*>(&sh.size), __float_as_int(fminf(fabsf(base), FLT_MAX)));
     }
+    __syncwarp();
+    if (lane == 0) sh.state[w] = state;
   }
   __syncthreads();
-  const int n_chunks = pick_best(sh, ChunkKeys{a, sh, a.maxima + (size_t)r * a.beams * a.chunks}, a.n_out);
-  if (tid < n_chunks) chunk[tid] = sh.best[tid];
-  __syncthreads();
-  const TokenKeys<T> tokens{a, sh, chunk, n_chunks, r};
-  const int n = pick_best(sh, tokens, a.n_out);
-  if (tid >= a.n_out) return;
-  const long long at = (long long)r * a.n_out + tid;
-  float score = -INFINITY;
-  int row = -1, token = -1;
-  bool ended = false;
-  if (tid < n) {
-    const Key k = sh.best_key[tid];
-    const int w = (int)(k.place >> 32);
-    token = (int)(uint32_t)k.place;
-    row = r * a.beams + w;
-    score = (float)__longlong_as_double((long long)(k.s >> 63 ? k.s & ~(1ull << 63) : ~k.s));
-    ended = sh.state[w] == 2 || token == a.eos;
+  // 64-bit bases, while the others look for the bound
+  if (tid >= kPickThreads - kBeamMaxBeams && tid - (kPickThreads - kBeamMaxBeams) < a.beams) {
+    const int w = tid - (kPickThreads - kBeamMaxBeams);
+    if (sh.state[w]) sh.base[w] = (double)sh.score[w] - ((double)sh.exponent[w] * 0.69314718055994531 + (double)sh.log_sum[w]) + 0.0;   // one zero
   }
-  a.out_scores[at] = score;
-  a.rows[at] = row;
-  a.tokens[at] = token;
-  if (a.out_finished) a.out_finished[at] = ended;
+
+  // the n best chunks
+  float mine = -INFINITY;
+  auto most = [&](float s, float, unsigned long long) { mine = fmaxf(mine, s); };
+  p.each_chunk(keys, tid, x, most);
+  for (int i0 = tid + kPer * kPickThreads; i0 < keys; i0 += kPer * kPickThreads) {
+    float y[kPer];
+    p.load_maxima(maxima, keys, i0, y);
+    p.each_chunk(keys, i0, y, most);
+  }
+  p.bound(mine);
+  auto chunks = [&](auto&& visit) {
+    const float from = p.from();
+    auto reach = [&](float s, float v, unsigned long long place) {
+      if (s >= from) visit(v, place);
+    };
+    p.each_chunk(keys, tid, x, reach);
+    for (int i0 = tid + kPer * kPickThreads; i0 < keys; i0 += kPer * kPickThreads) {
+      float y[kPer];
+      p.load_maxima(maxima, keys, i0, y);
+      p.each_chunk(keys, i0, y, reach);
+    }
+  };
+  auto add = [&](float v, unsigned long long place) { p.add(v, place); };
+  chunks(add);
+  const int chosen = p.rank(chunks, [&](int rank, unsigned long long s, unsigned long long place) {
+    const int w = (int)(place >> 32);
+    const Row<T> row(a, r, w);
+    sh.chunk[rank] = Chosen<T>{row.x, row.token((int)(uint32_t)place - w * a.chunks, 0), 0.f};
+    sh.row[rank] = w;
+    if (rank == n - 1) sh.bound = (float)unordered(s);         // n chunks' maxima are n tokens
+  });
+  __syncthreads();
+
+  // the n best tokens in them
+  if (chosen < n) {                                            // fewer chunks than n: another bound
+    if (tid < chosen) sh.chunk[tid].least = sh.state[sh.row[tid]] == 2 ? INFINITY : 0.f;
+    __syncthreads();
+    if (tid == 0) sh.bound = -INFINITY;
+    mine = -INFINITY;
+    p.each_four(chosen, [&](const uint32_t (&raw)[Pick<T>::kWords], int i, const Chosen<T>&) {
+      const int w = sh.row[i / kChunk];
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) {
+        const float v = Row<T>::value(raw, e);
+        if (v > -INFINITY) mine = fmaxf(mine, p.key32(sh.base32[w], sh.top[w], v));
+      }
+    });
+    if (tid < chosen && sh.state[sh.row[tid]] == 2) mine = fmaxf(mine, sh.score[sh.row[tid]]);
+    p.bound(mine);
+  }
+  if (tid == 0) sh.count = 0;
+  if (tid < chosen) sh.chunk[tid].least = p.least(tid, p.from());
+  __syncthreads();
+  auto tokens = [&](auto&& visit) { p.each_token(chosen, visit); };
+  tokens(add);
+  const long long to = (long long)r * n;
+  const int found = p.rank(tokens, [&](int rank, unsigned long long s, unsigned long long place) {
+    const int w = (int)(place >> 32), token = (int)(uint32_t)place;
+    a.out_scores[to + rank] = (float)unordered(s);
+    a.rows[to + rank] = r * a.beams + w;
+    a.tokens[to + rank] = token;
+    if (a.out_finished) a.out_finished[to + rank] = sh.state[w] == 2 || token == a.eos;
+  });
+  if (tid >= found && tid < n) {
+    a.out_scores[to + tid] = -INFINITY;
+    if (a.out_finished) a.out_finished[to + tid] = 0;
+  }
 }
 
 // ------------------------------------------------------------------ paths
@@ -448,7 +674,6 @@ cudaError_t select_t(const BeamArgs& a, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.requests);
   cfg.blockDim = dim3(kPickThreads);
-  cfg.dynamicSmemBytes = sizeof(PickShared) + kBeamMaxOut * sizeof(uint32_t);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

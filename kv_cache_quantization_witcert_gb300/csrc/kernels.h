@@ -270,8 +270,9 @@ cudaError_t launch_move_ints(const MoveInts& a, cudaStream_t st);
 cudaError_t launch_copy_pages(const CopyPages& a, int layers, cudaStream_t st);
 
 // Beam search (beam.cu).  A row (request, beam) of logits is cut into chunks of kBeamChunk tokens, counted
-// from the 32-byte boundary at or before its start; part p of a row is chunks p chunks_per_part, ...
+// from the 32-byte boundary at or before its start; part p of a row is its chunks p, p + parts, ...
 constexpr int kBeamChunk = 512;
+constexpr int kBeamScanWarps = 48;               // warps of the scan on an SM
 constexpr int kBeamMaxBeams = 128, kBeamMaxOut = 256;
 struct BeamArgs {
   const void* logits;
@@ -279,7 +280,8 @@ struct BeamArgs {
   const float* scores;       // [requests][beams]
   const uint8_t* finished;   // [requests][beams], or null
   int requests, beams, vocab, n_out, eos, is_bf16;
-  int chunks, parts, chunks_per_part;
+  int chunks, parts;
+  uint32_t chunks_inv;       // floor((2^32 - 1) / chunks)
   float2* records;           // [requests][beams][parts]: largest logit, sum of exp(x - it)
   float* maxima;             // [requests][beams][chunks]
   float* out_scores;         // [requests][n_out]

@@ -1485,8 +1485,7 @@ witcert_status witcert_gate_select(const float* risk, const uint8_t* repaired, i
 }
 
 // ------------------------------------------------------------------ beam search
-// Checks a step and lays out its scan: a warp takes chunks_per_part chunks of a row, one where the rows are
-// few (latency), more where the GPU is full anyway.
+// Checks a step and lays out its scan.
 static witcert_status beam_args(const witcert_beam_step* s, BeamArgs& a, size_t& bytes) {
   if (!s) return fail(WITCERT_EINVAL, "step must not be NULL");
   if (s->dtype != WITCERT_F32 && s->dtype != WITCERT_BF16) return fail(WITCERT_EINVAL, "unknown dtype %d", (int)s->dtype);
@@ -1505,9 +1504,10 @@ static witcert_status beam_args(const witcert_beam_step* s, BeamArgs& a, size_t&
   const bool even = at % 32 == 0 && (s->n_requests < 2 || s->request_stride * elem % 32 == 0) &&
                     (s->n_beams < 2 || s->beam_stride * elem % 32 == 0);
   a.chunks = (int)((s->vocab + (even ? 0 : 32 / elem - 1) + (long long)kBeamChunk - 1) / kBeamChunk);
-  const long long warps = (long long)sm_count_now() * 32;
-  a.chunks_per_part = (int)std::min<long long>(8, std::max<long long>(1, rows * a.chunks / warps));
-  a.parts = (a.chunks + a.chunks_per_part - 1) / a.chunks_per_part;
+  // a warp a chunk where the rows are few; one wave of warps, then more waves of at most nine chunks a warp
+  const long long warps = (long long)sm_count_now() * kBeamScanWarps;
+  a.parts = (int)std::min<long long>(a.chunks, std::max(warps / std::max(rows, 1ll), (a.chunks + 8ll) / 9));
+  a.chunks_inv = UINT32_MAX / (uint32_t)a.chunks;
   if (rows * a.parts > INT_MAX) return fail(WITCERT_EINVAL, "too many logits (%lld rows of %d)", rows, s->vocab);
   bytes = (size_t)rows * (a.parts * sizeof(float2) + a.chunks * sizeof(float));
   a.logits = s->logits;

@@ -49,9 +49,10 @@ def check(x, scores, got, n, done=None, eos=-1):
                 m = row.max() if not np.isnan(row).any() else np.nan
                 if not np.isfinite(m):
                     continue
-                lse = m + math.log(np.exp(row - m).sum())
+                # in this order nothing is lost next to a maximum of any size
+                c = sc[r, w] - math.log(np.exp(row - m).sum())
                 first = np.lexsort((np.arange(V), -row))[:n]
-                offers[w] = [(sc[r, w] + (row[t] - lse), int(t)) for t in first if row[t] > -INF]
+                offers[w] = [(c + (row[t] - m), int(t)) for t in first if row[t] > -INF]
             best += [s for s, _ in offers[w]]
         best = sorted(best, reverse=True)[:n]
         taken = dict.fromkeys(offers, 0)
