@@ -426,7 +426,7 @@ typedef struct {
 } witcert_beam_step;
 
 /* Bytes of device workspace that witcert_beam_select needs for this step's sizes, strides and logits'
- * alignment (host, no device work). */
+ * alignment (host, no device work); at most 12 n_requests n_beams (vocab / 512 + 2). */
 witcert_status witcert_beam_workspace(const witcert_beam_step* step, size_t* bytes);
 
 /* One selection (see witcert_beam_step).  workspace: device, 16-byte aligned, at least what

@@ -57,6 +57,16 @@ def _need(*specs):
     optional]) with None in shape for any extent: contiguous tensors of that dtype and shape,
     then all on a CUDA device.  The C ABI takes bare pointers, so a host tensor or a short
     buffer would reach a kernel; the binding raises ValueError instead."""
+    for spec in specs:                          # what nearly every call passes: nothing to complain about
+        t = spec[1]
+        if t is None:
+            if len(spec) > 4 and spec[4]:
+                continue
+            break
+        if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == spec[2] and t.shape == spec[3] and t.is_contiguous()):
+            break
+    else:
+        return
     given = []
     for name, t, dtype, shape, *opt in specs:
         if t is None:
@@ -477,8 +487,10 @@ def witcert_gate_select(risk, n_kv_heads, tau, repaired=None, selected=None, str
 
 
 def _here(name, t):
-    """Check that a tensor lies on the current device, where the library launches."""
-    if t.device.index != torch.cuda.current_device():
+    """Check that a tensor lies on the current CUDA device, where the library launches."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.get_device() != torch._C._cuda_getDevice():
         raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
 
 
@@ -490,30 +502,29 @@ def witcert_beam_select(logits, scores, n_out=None, finished=None, eos=-1, out=N
     last of them or the input's own for scores and finished as witcert_beam_step in include/witcert.h allows."""
     if not isinstance(logits, torch.Tensor) or logits.dim() != 3:
         raise ValueError("logits must be a torch.Tensor [requests, beams, vocabulary]")
+    R, W, V = logits.shape
+    xs, dev = logits.stride(), logits.device
+    n = W if n_out is None else int(n_out)
     if logits.dtype not in (torch.bfloat16, torch.float32):
         raise ValueError(f"logits must be torch.bfloat16 or torch.float32, got {logits.dtype}")
-    R, W, V = logits.shape
-    if V != 1 and logits.stride(2) != 1:
-        raise ValueError(f"logits must have adjacent tokens (stride 1), got stride {logits.stride(2)}")
-    n = W if n_out is None else int(n_out)
+    if V != 1 and xs[2] != 1:
+        raise ValueError(f"logits must have adjacent tokens (stride 1), got stride {xs[2]}")
     _need(("scores", scores, torch.float32, (R, W)), ("finished", finished, torch.bool, (R, W), True))
-    if not logits.is_cuda:
-        raise ValueError("logits must be a CUDA tensor")
     _here("logits", logits)
     if out is None:
-        out = tuple(_empty(stream, (R, max(n, 0)), dt, logits.device)
-                    for dt in (torch.float32, torch.int32, torch.int32, torch.bool))
-    elif len(out) != 4:
-        raise ValueError(f"out needs four tensors (scores, rows, tokens, finished), got {len(out)}")
-    _need(*((name, t, dt, (R, n)) for name, t, dt in zip(("out scores", "rows", "tokens", "out finished"), out,
-                                                        (torch.float32, torch.int32, torch.int32, torch.bool))))
+        shape = (R, max(n, 0))
+        out = (_empty(stream, shape, torch.float32, dev), _empty(stream, shape, torch.int32, dev),
+               _empty(stream, shape, torch.int32, dev), _empty(stream, shape, torch.bool, dev))
+    else:
+        if len(out) != 4:
+            raise ValueError(f"out needs four tensors (scores, rows, tokens, finished), got {len(out)}")
+        _need(*((name, t, dt, (R, n)) for name, t, dt in zip(("out scores", "rows", "tokens", "out finished"), out,
+                                                            (torch.float32, torch.int32, torch.int32, torch.bool))))
     step = _lib.witcert_beam_step(BF16 if logits.dtype == torch.bfloat16 else F32, R, W, V, n, int(eos), logits.data_ptr(),
-                                  logits.stride(0), logits.stride(1), scores.data_ptr(), _ptr(finished),
-                                  *(t.data_ptr() for t in out))
-    size = ctypes.c_size_t()
-    check(load().witcert_beam_workspace(ctypes.addressof(step), ctypes.byref(size)), "witcert_beam_workspace")
-    workspace = _empty(stream, size.value, torch.uint8, logits.device)
-    check(load().witcert_beam_select(ctypes.addressof(step), workspace.data_ptr(), size.value, _stream_ptr(stream)),
+                                  xs[0], xs[1], scores.data_ptr(), _ptr(finished), *[t.data_ptr() for t in out])
+    size = 12 * R * W * (V // 512 + 2)                     # what witcert_beam_workspace says is at most this
+    workspace = _empty(stream, size, torch.uint8, dev)
+    check(load().witcert_beam_select(ctypes.addressof(step), workspace.data_ptr(), size, _stream_ptr(stream)),
           "witcert_beam_select")
     return tuple(out)
 

@@ -13,6 +13,7 @@
 // a lower bound of the n-th best key comes from the largest keys of groups of threads, every key that its
 // rounding does not put below that bound is listed, and only the list is formed in 64 bits (whose rate is a
 // 64th of fp32's) and ranked by counting.
+#include <algorithm>
 #include <cfloat>
 
 #include "common.cuh"
@@ -26,7 +27,8 @@ constexpr int kChunk = kBeamChunk;
 constexpr int kLane = kChunk / 32;               // elements of a chunk a lane holds: 16
 constexpr int kScanWarps = 4;
 constexpr int kPickThreads = 1024;
-constexpr int kList = 1024;                      // candidates that are ranked exactly
+constexpr int kList = 4096;                      // candidates that are ranked exactly, a power of two
+constexpr int kCounted = 256;                    // lists up to this are ranked by counting, longer ones sorted
 constexpr int kMaxGroups = 512;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -345,39 +347,101 @@ struct Pick {
     return (unsigned __int128)key(__uint_as_float((uint32_t)(k >> 64)), (int)(place >> 32)) << 64 | ~place;
   }
 
-  // Ranks the listed keys and calls put(rank, s, place) on one thread for each of the n first; each(visit) visits
-  // all candidates again, where more were listed than fit.  Returns how many there are.
-  template <class Each, class Put>
-  __device__ __forceinline__ int rank(Each&& each, Put&& put) const {
+  // The q first of a warp's candidates of one row, by logit and then in order: value(j), j = 0 .. m - 1, are the
+  // lane's logits (-inf: none), those of lower lanes come first.  Calls visit(j, logit) for each.
+  template <class Value, class Visit>
+  __device__ __forceinline__ void first_of(int m, int q, Value&& value, Visit&& visit) const {
+    auto rank_of = [](float x) {                               // orders like the logits, one zero
+      const uint32_t b = __float_as_uint(x + 0.f);
+      return b & 0x80000000u ? ~b : b | 0x80000000u;
+    };
+    auto count = [&](uint32_t least) {
+      int c = 0;
+      for (int j = 0; j < m; ++j) c += rank_of(value(j)) >= least;
+      return (int)__reduce_add_sync(0xffffffffu, c);
+    };
+    uint32_t lo = rank_of(-FLT_MAX), hi = rank_of(FLT_MAX);
+    if (count(lo) > q)
+      while (lo < hi) {                                        // the largest that q of them reach
+        const uint32_t mid = lo + (hi - lo) / 2 + 1;
+        if (count(mid) >= q) lo = mid; else hi = mid - 1;
+      }
+    int same = 0;
+    for (int j = 0; j < m; ++j) same += rank_of(value(j)) == lo;
+    int before = same;                                         // those equal to it in lower lanes
+    for (int o = 1; o < 32; o *= 2) {
+      const int v = __shfl_up_sync(0xffffffffu, before, o);
+      before += lane >= o ? v : 0;
+    }
+    before -= same;
+    const int room = q - count(lo + 1);
+    for (int j = 0; j < m; ++j) {
+      const float x = value(j);
+      const uint32_t k = rank_of(x);
+      if (k > lo || (k == lo && before++ < room)) visit(j, x);
+    }
+  }
+
+  // Ranks the listed keys and calls put(rank, s, place) on one thread for each of the n first.  If more were listed
+  // than fit (very many equal or nearly equal keys), few() lists only those that their row's or chunk's own order
+  // leaves, at most `at_most` of them; if these may be too many as well, each(visit) visits all candidates again,
+  // and a bound is found by halving the space of the keys, which are distinct.  Returns how many there are.
+  template <class Each, class Few, class Put>
+  __device__ __forceinline__ int rank(Each&& each, int at_most, Few&& few, Put&& put) const {
     __syncthreads();
     int listed = sh.count;
     if (listed > kList) {
-      // Very many equal or nearly equal keys: halve the space of the keys themselves, which are distinct.
-      unsigned __int128 low = 0, high = ~(unsigned __int128)0; // count(>= low) > kList, count(> high) < n
-      do {
-        const unsigned __int128 mid = low + (high - low) / 2 + 1;
-        __syncthreads();
-        if (tid == 0) sh.count = 0;
-        __syncthreads();
-        each([&](float x, unsigned long long place) {
-          if (exact((unsigned __int128)__float_as_uint(x) << 64 | place) >= mid) add(x, place);
-        });
+      __syncthreads();
+      if (tid == 0) sh.count = 0;
+      __syncthreads();
+      if (at_most <= kList) {
+        few();
         __syncthreads();
         listed = sh.count;
-        if (listed < n) high = mid - 1; else low = mid;
-      } while (listed < n || listed > kList);
+      } else {
+        unsigned __int128 low = 0, high = ~(unsigned __int128)0;         // count(>= low) > kList, count(> high) < n
+        do {
+          const unsigned __int128 mid = low + (high - low) / 2 + 1;
+          __syncthreads();
+          if (tid == 0) sh.count = 0;
+          __syncthreads();
+          each([&](float x, unsigned long long place) {
+            if (exact((unsigned __int128)__float_as_uint(x) << 64 | place) >= mid) add(x, place);
+          });
+          __syncthreads();
+          listed = sh.count;
+          if (listed < n) high = mid - 1; else low = mid;
+        } while (listed < n || listed > kList);
+      }
     }
     for (int i = tid; i < listed; i += kPickThreads) sh.key[i] = exact(sh.key[i]);
     __syncthreads();
-    // a key's rank is the number of keys before it: eight lanes count for one key at a time
-    for (int i = tid / 8; i - tid % 32 / 8 < listed; i += kPickThreads / 8) {
-      const unsigned __int128 k = i < listed ? sh.key[i] : 0;
-      int rank = 0;
+    if (listed <= kCounted) {
+      // a key's rank is the number of keys before it: eight lanes count for one key at a time
+      for (int i = tid / 8; i - tid % 32 / 8 < listed; i += kPickThreads / 8) {
+        const unsigned __int128 k = i < listed ? sh.key[i] : 0;
+        int rank = 0;
 #pragma unroll 2
-      for (int j = tid % 8; j < listed; j += 8) rank += sh.key[j] > k;
+        for (int j = tid % 8; j < listed; j += 8) rank += sh.key[j] > k;
 #pragma unroll
-      for (int o = 4; o > 0; o /= 2) rank += __shfl_xor_sync(0xffffffffu, rank, o);
-      if (tid % 8 == 0 && i < listed && rank < n) put(rank, (unsigned long long)(k >> 64), ~(unsigned long long)k);
+        for (int o = 4; o > 0; o /= 2) rank += __shfl_xor_sync(0xffffffffu, rank, o);
+        if (tid % 8 == 0 && i < listed && rank < n) put(rank, (unsigned long long)(k >> 64), ~(unsigned long long)k);
+      }
+    } else {                                                   // sorted by exchanges, the largest first
+      int size = 2 * kCounted;
+      while (size < listed) size *= 2;
+      for (int i = listed + tid; i < size; i += kPickThreads) sh.key[i] = 0;
+      for (int run = 2; run <= size; run *= 2)
+        for (int d = run / 2; d > 0; d /= 2) {
+          __syncthreads();
+          for (int i = tid; i < size / 2; i += kPickThreads) {
+            const int x = 2 * i - (i & (d - 1)), y = x + d;    // the i-th pair d apart
+            const unsigned __int128 u = sh.key[x], v = sh.key[y];
+            if ((u < v) == ((x & run) == 0)) { sh.key[x] = v; sh.key[y] = u; }
+          }
+        }
+      __syncthreads();
+      if (tid < min(listed, n)) put(tid, (unsigned long long)(sh.key[tid] >> 64), ~(unsigned long long)sh.key[tid]);
     }
     return min(listed, n);
   }
@@ -454,7 +518,8 @@ struct Pick {
 
 template <typename T>
 __global__ void __launch_bounds__(kPickThreads, 1) beam_pick_kernel(const __grid_constant__ BeamArgs a) {
-  __shared__ __align__(16) PickShared<T> sh;
+  extern __shared__ __align__(16) uint8_t smem[];
+  PickShared<T>& sh = *reinterpret_cast<PickShared<T>*>(smem);
   const int r = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, n = a.n_out;
   const Pick<T> p{a, sh, r, n, tid, warp, lane};
   if (tid == 0) { sh.size = 0.f; sh.bound = -INFINITY; sh.count = 0; }
@@ -543,7 +608,18 @@ __global__ void __launch_bounds__(kPickThreads, 1) beam_pick_kernel(const __grid
   };
   auto add = [&](float v, unsigned long long place) { p.add(v, place); };
   chunks(add);
-  const int chosen = p.rank(chunks, [&](int rank, unsigned long long s, unsigned long long place) {
+  auto few_chunks = [&] {                                      // n of a row's chunks at most
+    for (int w = warp; w < a.beams; w += kPickWarps) {
+      const int state = sh.state[w], m = (a.chunks + 31) / 32, c0 = lane * m;
+      const float from = p.from(), base = sh.base32[w], top = sh.top[w];
+      p.first_of(state ? m : 0, n, [&](int j) {
+        const int c = c0 + j;
+        const float v = c >= a.chunks ? -INFINITY : state == 2 ? (c ? -INFINITY : 0.f) : maxima[(size_t)w * a.chunks + c];
+        return v > -INFINITY && p.key32(base, top, v) >= from ? v : -INFINITY;
+      }, [&](int j, float v) { p.add(v, (unsigned long long)w << 32 | (uint32_t)(w * a.chunks + c0 + j)); });
+    }
+  };
+  const int chosen = p.rank(chunks, a.beams * n, few_chunks, [&](int rank, unsigned long long s, unsigned long long place) {
     const int w = (int)(place >> 32);
     const Row<T> row(a, r, w);
     sh.chunk[rank] = Chosen<T>{row.x, row.token((int)(uint32_t)place - w * a.chunks, 0), 0.f};
@@ -575,7 +651,28 @@ __global__ void __launch_bounds__(kPickThreads, 1) beam_pick_kernel(const __grid
   auto tokens = [&](auto&& visit) { p.each_token(chosen, visit); };
   tokens(add);
   const long long to = (long long)r * n;
-  const int found = p.rank(tokens, [&](int rank, unsigned long long s, unsigned long long place) {
+  auto few_tokens = [&] {          // k chunks' maxima are before any token of chunk k: n - k of its tokens at most
+    for (int k = warp; k < chosen; k += kPickWarps) {
+      const Chosen<T> c = sh.chunk[k];
+      const unsigned long long w = (unsigned long long)sh.row[k] << 32;
+      if (c.least == INFINITY) {
+        if (lane == 0) p.add(0.f, w | (uint32_t)a.eos);
+        continue;
+      }
+      uint32_t part[Row<T>::kWords];
+      Row<T>::load_at(c.x, a.vocab, c.first + lane * kLane, part);
+      float v[kLane];
+#pragma unroll
+      for (int e = 0; e < kLane; ++e) v[e] = Row<T>::value(part, e);
+      p.first_of(kLane, n - k, [&](int j) {
+        float x = -INFINITY;
+#pragma unroll
+        for (int e = 0; e < kLane; ++e) x = e == j ? v[e] : x;
+        return x >= c.least ? x : -INFINITY;
+      }, [&](int j, float x) { p.add(x, w | (uint32_t)(c.first + lane * kLane + j)); });
+    }
+  };
+  const int found = p.rank(tokens, chosen * (2 * n - chosen + 1) / 2, few_tokens, [&](int rank, unsigned long long s, unsigned long long place) {
     const int w = (int)(place >> 32), token = (int)(uint32_t)place;
     a.out_scores[to + rank] = (float)unordered(s);
     a.rows[to + rank] = r * a.beams + w;
@@ -589,80 +686,108 @@ __global__ void __launch_bounds__(kPickThreads, 1) beam_pick_kernel(const __grid
 }
 
 // ------------------------------------------------------------------ paths
-// The beam that step t's choice for the last beam w came from is a chain of maps, which are put together in
-// any grouping: a CTA a request takes a tile of steps from the end, each warp forms the map of its share of
-// the tile (a walk for every beam), takes over the maps after its own, and walks its share again, writing
-// for each step which entry the last beams chose.  The tile's entries and tokens lie in shared memory, so
-// that a step of a walk is one shared-memory load, and the sequences go out along time.
-constexpr int kPathThreads = 1024, kPathWarps = kPathThreads / 32;
-constexpr int kPathPerLane = (kBeamMaxBeams + 31) / 32;
-constexpr int kPathShared = 160 * 1024;
+// The way back from the last beams is a chain of maps, which may be put together in any grouping.  A cluster of
+// CTAs a request takes a tile of steps from the end, each of its threads a share of them for one beam: they walk
+// through their shares from every beam (a map a share), put the maps of all later shares together in
+// log2(shares) rounds within a CTA and one after another across the cluster, and walk again from where the
+// last beams come in.  Parents and tokens of the tile lie in shared memory, so that a step is one shared-memory
+// load, and the sequences leave along time.  Bound by the latency of that chain: load, two walks, the
+// rounds between.
+constexpr int kPathThreads = 1024;
+constexpr int kPathShared = 200 * 1024;
+constexpr int kNoBeam = 255;
 
-__global__ void __launch_bounds__(kPathThreads) beam_paths_kernel(const __grid_constant__ PathArgs a) {
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n barrier.cluster.wait.acquire;" ::: "memory");
+}
+// A byte of CTA `rank`'s shared memory, at the same place as p in this one.
+__device__ __forceinline__ int of_cta(const uint8_t* p, int rank) {
+  uint32_t at, v;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.u8 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+  return (int)v;
+}
+
+__global__ void __launch_bounds__(kPathThreads, 1) beam_paths_kernel(const __grid_constant__ PathArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ uint8_t map[kPathWarps][kBeamMaxBeams + 1];
-  __shared__ uint8_t carry[kBeamMaxBeams];
-  const int W = a.beams, r = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  __shared__ uint8_t map[2][kPathThreads];
+  __shared__ uint8_t whole[2][kBeamMaxBeams];                  // this CTA's steps as one map, of this tile and the next
+  const int W = a.beams, ctas = a.ctas, cta = blockIdx.x % ctas, r = blockIdx.x / ctas, tid = threadIdx.x, lw = a.log_beams;
+  const int shares = kPathThreads >> lw, share = tid >> lw, w = tid & ((1 << lw) - 1);
+  const bool here = w < W;
+  const int pitch = a.tile | 1;                                // of the sequences: odd, beams on different banks
   int32_t* tok = reinterpret_cast<int32_t*>(smem);             // [tile][W]
-  uint8_t* rel = smem + (size_t)a.tile * W * 4;                // [tile][W]: the parent beam, W for none
+  int32_t* seq = tok + (size_t)a.tile * W;                     // [W][pitch]
+  uint8_t* par = reinterpret_cast<uint8_t*>(seq + (size_t)W * pitch);      // [tile][W]
   int n = a.steps;
   if (a.n_steps) n = min(max(a.n_steps[r], 0), a.steps);
   const size_t step = (size_t)a.requests * W;
   int32_t* out = a.out + (size_t)r * W * a.steps;
-  for (int w = 0; w < W; ++w)
-    for (int t = n + tid; t < a.steps; t += kPathThreads) out[(size_t)w * a.steps + t] = a.pad;
-  if (tid < W) carry[tid] = (uint8_t)tid;
-  for (int t1 = n; t1 > 0; t1 -= a.tile) {
-    const int t0 = max(0, t1 - a.tile), len = t1 - t0;
+  // 32 steps of a beam a warp at a time: fn(beam, step in 0 .. count - 1)
+  auto along_time = [&](int count, auto&& fn) {
+    const int tasks = (count + 31) / 32 * W;
+#pragma unroll 4
+    for (int k = tid / 32; k < tasks; k += kPathThreads / 32) {
+      const int t = k / W * 32 + tid % 32;
+      if (t < count) fn(k % W, t);
+    }
+  };
+  if (cta == 0) along_time(a.steps - n, [&](int k, int t) { out[(size_t)k * a.steps + n + t] = a.pad; });
+  int carry = here ? w : kNoBeam;                              // where last beam w is when the tile begins (at its end)
+  for (int t2 = n, turn = 0; t2 > 0; t2 -= ctas * a.tile, turn ^= 1) {
+    // the CTAs take equal parts of the tile, the last one the last steps
+    const int all = min(t2, ctas * a.tile), part = (all + ctas - 1) / ctas;
+    const int t0 = t2 - all + min(all, cta * part), len = t2 - all + min(all, (cta + 1) * part) - t0;
     __syncthreads();
-    for (int i = tid; i < len * W; i += kPathThreads) {
-      const size_t at = (t0 + i / W) * step + (size_t)r * W + i % W;
-      const long long p = (long long)a.rows[at] - (long long)r * W;
-      rel[i] = p >= 0 && p < W ? (uint8_t)p : (uint8_t)W;
-      tok[i] = a.tokens[at];
+    if (here) {
+      const size_t from = t0 * step + (size_t)r * W + w;
+#pragma unroll 8
+      for (int t = share; t < len; t += shares) {
+        const long long p = (long long)a.rows[from + t * step] - (long long)r * W;
+        const int32_t x = a.tokens[from + t * step];
+        par[t * W + w] = p >= 0 && p < W ? (uint8_t)p : (uint8_t)kNoBeam;
+        tok[t * W + w] = x;
+      }
     }
     __syncthreads();
-    const int share = (len + kPathWarps - 1) / kPathWarps, b = min(len, warp * share), e = min(len, b + share);
-    int at[kPathPerLane];
-#pragma unroll
-    for (int k = 0; k < kPathPerLane; ++k) at[k] = min(lane + 32 * k, W);
-    for (int t = e - 1; t >= b; --t)
-#pragma unroll
-      for (int k = 0; k < kPathPerLane; ++k)
-        if (at[k] < W) at[k] = rel[t * W + at[k]];
-#pragma unroll
-    for (int k = 0; k < kPathPerLane; ++k)
-      if (lane + 32 * k < W) map[warp][lane + 32 * k] = (uint8_t)at[k];
+    const int each = (len + shares - 1) >> (10 - lw), b = min(len, share * each), e = min(len, b + each);
+    int at = here ? w : kNoBeam;
+    for (int t = e - 1; t >= b && at != kNoBeam; --t) at = par[t * W + at];
+    map[0][tid] = (uint8_t)at;
     __syncthreads();
-#pragma unroll
-    for (int k = 0; k < kPathPerLane; ++k) at[k] = lane + 32 * k < W ? carry[lane + 32 * k] : W;
-    for (int j = kPathWarps - 1; j > warp; --j)
-#pragma unroll
-      for (int k = 0; k < kPathPerLane; ++k)
-        if (at[k] < W) at[k] = map[j][at[k]];
-    for (int t = e - 1; t >= b; --t) {
-      int to[kPathPerLane];
-#pragma unroll
-      for (int k = 0; k < kPathPerLane; ++k) to[k] = at[k] < W ? rel[t * W + at[k]] : W;
-      __syncwarp();                                            // the step's parents are read: its choices replace them
-#pragma unroll
-      for (int k = 0; k < kPathPerLane; ++k) {
-        if (lane + 32 * k < W) rel[t * W + lane + 32 * k] = (uint8_t)(to[k] < W ? at[k] : W);
-        at[k] = to[k];
-      }
-      __syncwarp();
+    int now = 0;                                               // map[now][share]: through this share and all later ones
+    for (int d = 1; d < shares; d *= 2, now ^= 1) {
+      int v = w;
+      if (share + d < shares) v = map[now][tid + (d << lw)];
+      map[now ^ 1][tid] = v == kNoBeam ? kNoBeam : map[now][(share << lw) + v];
+      __syncthreads();
     }
-    __syncthreads();                                           // every warp has read the carry
-    if (warp == 0)
-#pragma unroll
-      for (int k = 0; k < kPathPerLane; ++k)
-        if (lane + 32 * k < W) carry[lane + 32 * k] = (uint8_t)at[k];
-    for (int w = 0; w < W; ++w)
-      for (int t = tid; t < len; t += kPathThreads) {
-        const int c = rel[t * W + w];
-        out[(size_t)w * a.steps + t0 + t] = c < W ? tok[t * W + c] : a.pad;
+    at = carry;
+    if (ctas > 1) {
+      if (share == 0 && here) whole[turn][w] = map[now][tid];
+      cluster_sync();
+      for (int c = ctas - 1; c >= 0; --c) {                    // through the later CTAs, and then through the others
+        if (c == cta) at = carry;
+        if (carry != kNoBeam) carry = of_cta(&whole[turn][carry], c);
       }
+    } else if (carry != kNoBeam) {
+      carry = map[now][carry];
+    }
+    if (share + 1 < shares && at != kNoBeam) at = map[now][((share + 1) << lw) + at];
+    if (here)
+      for (int t = e - 1; t >= b; --t) {
+        int x = a.pad;
+        if (at != kNoBeam) {
+          const int to = par[t * W + at];
+          if (to != kNoBeam) x = tok[t * W + at];
+          at = to;
+        }
+        seq[w * pitch + t] = x;
+      }
+    __syncthreads();
+    along_time(len, [&](int k, int t) { out[(size_t)k * a.steps + t0 + t] = seq[k * pitch + t]; });
   }
+  if (ctas > 1) cluster_sync();                                // nobody leaves while its maps are read
 }
 
 template <typename T>
@@ -670,10 +795,12 @@ cudaError_t select_t(const BeamArgs& a, cudaStream_t st) {
   const long long warps = (long long)a.requests * a.beams * a.parts;
   beam_scan_kernel<T><<<(unsigned)((warps + kScanWarps - 1) / kScanWarps), kScanWarps * 32, 0, st>>>(a);
   cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(beam_pick_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(PickShared<T>));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.requests);
   cfg.blockDim = dim3(kPickThreads);
+  cfg.dynamicSmemBytes = sizeof(PickShared<T>);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -689,16 +816,32 @@ cudaError_t launch_beam_select(const BeamArgs& a, cudaStream_t st) {
   return a.is_bf16 ? select_t<__nv_bfloat16>(a, st) : select_t<float>(a, st);
 }
 
-cudaError_t launch_beam_paths(PathArgs& a, cudaStream_t st) {
-  a.tile = kPathShared / (a.beams * 5);
-  if (a.tile > a.steps) a.tile = a.steps;
-  const int bytes = a.tile * a.beams * 5;
-  if (bytes > 47 * 1024) {
+cudaError_t launch_beam_paths(PathArgs& a, int sm_count, cudaStream_t st) {
+  a.log_beams = 0;
+  while (1 << a.log_beams < a.beams) ++a.log_beams;
+  // CTAs a request while they have an SM each and four steps a share.  By 1, 2, 4 and 8 of them, us: 5 requests
+  // of 33 beams and 777 steps (4 a share by 8) 23.2, 13.4, 9.7, 8.4; 64 of 8 beams and 2048 steps (8 by 2) 12.8, 9.2, 14.5
+  // by 4 (256 CTAs); 16 of 4 beams and 512 steps (2 by 1) 5.3, 5.6, 5.6, 11.1
+  a.ctas = 1;
+  while (a.ctas < 8 && 2 * a.ctas * (long long)a.requests <= sm_count && 2 * a.ctas * 4 * (kPathThreads >> a.log_beams) <= a.steps) a.ctas *= 2;
+  a.tile = std::min(kPathShared / (a.beams * 9) - 1, (a.steps + a.ctas - 1) / a.ctas);
+  const int bytes = a.tile * a.beams * 5 + a.beams * (a.tile | 1) * 4;
+  if (bytes > 44 * 1024) {
     cudaError_t e = cudaFuncSetAttribute(beam_paths_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPathShared);
     if (e != cudaSuccess) return e;
   }
-  beam_paths_kernel<<<a.requests, kPathThreads, bytes, st>>>(a);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)a.requests * a.ctas);
+  cfg.blockDim = dim3(kPathThreads);
+  cfg.dynamicSmemBytes = bytes;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = a.ctas;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, beam_paths_kernel, (const PathArgs)a);
 }
 
 }  // namespace witcert

@@ -70,12 +70,20 @@ __global__ void __launch_bounds__(128) move_ints_kernel(const __grid_constant__ 
   if (table ? !a.table : !a.lens) return;
   const size_t pitch = table ? a.nblk_max : 1;
   int32_t kept = table ? -1 : 0;
-  for (int m = 0; m < a.n; ++m) {
-    const MoveOp& op = a.op[m];
-    int32_t v = op.src >= 0 ? base[op.src * pitch] : op.src == kMoveKept ? kept : table ? -1 : 0;
-    if (op.dst == kMoveKept) { kept = v; continue; }
-    v = table ? (c < op.blocks ? v : -1) : min(v, op.cap);
-    base[op.dst * pitch] = v;
+  constexpr int kTogether = 8;                                 // loads in flight; no move reads what an earlier one wrote
+  for (int m = 0; m < a.n; m += kTogether) {
+    int32_t v[kTogether];
+#pragma unroll
+    for (int u = 0; u < kTogether; ++u)
+      if (m + u < a.n && a.op[m + u].src >= 0) v[u] = base[a.op[m + u].src * pitch];
+#pragma unroll
+    for (int u = 0; u < kTogether; ++u) {
+      if (m + u >= a.n) break;
+      const MoveOp& op = a.op[m + u];
+      const int32_t x = op.src >= 0 ? v[u] : op.src == kMoveKept ? kept : table ? -1 : 0;
+      if (op.dst == kMoveKept) kept = x;
+      else base[op.dst * pitch] = table ? (c < op.blocks ? x : -1) : min(x, op.cap);
+    }
   }
 }
 

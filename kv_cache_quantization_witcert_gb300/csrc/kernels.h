@@ -294,9 +294,10 @@ struct PathArgs {
   const int32_t* n_steps;    // [requests], or null
   int32_t* out;              // [requests][beams][steps]
   int steps, requests, beams, pad;
-  int tile;                  // steps a CTA holds at a time; filled by the launcher
+  // filled by the launcher: CTAs a request, steps a CTA holds at a time, log2 of beams rounded up
+  int ctas, tile, log_beams;
 };
-cudaError_t launch_beam_paths(PathArgs& a, cudaStream_t st);
+cudaError_t launch_beam_paths(PathArgs& a, int sm_count, cudaStream_t st);
 
 struct ExportArgs {
   const uint8_t* blocks;

@@ -1555,8 +1555,8 @@ witcert_status witcert_beam_paths(const int32_t* rows, const int32_t* tokens, in
   if ((long long)n_requests * n_beams > INT_MAX) return fail(WITCERT_EINVAL, "too many rows");
   if (n_steps == 0 || n_requests == 0) { ok(); return WITCERT_OK; }
   if (!rows || !tokens || !out) return fail(WITCERT_EINVAL, "rows, tokens and out must not be NULL");
-  PathArgs a{rows, tokens, length, out, n_steps, n_requests, n_beams, pad, 0};
-  cudaError_t e = launch_beam_paths(a, static_cast<cudaStream_t>(stream));
+  PathArgs a{rows, tokens, length, out, n_steps, n_requests, n_beams, pad, 0, 0, 0};
+  cudaError_t e = launch_beam_paths(a, sm_count_now(), static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "beam paths launch");
   ok();
   return WITCERT_OK;

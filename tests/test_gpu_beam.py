@@ -184,6 +184,22 @@ def test_ties_and_orders(kind, dt):
             assert (rows[r] == r * W + order // V).all() and (tokens[r] == order % V).all()
 
 
+@pytest.mark.parametrize("R, W, V, n", [(2, 4, 140001, 200), (1, 64, 40000, 128), (2, 8, 131072, 16), (1, 32, 50001, 64), (3, 16, 9000, 44),
+                                        (1, 2, 1500, 256)])
+@pytest.mark.parametrize("kind", ["equal", "mask", "levels"])
+def test_many_alike(R, W, V, n, kind):
+    """More equal or nearly equal keys than any list holds, at both stages, by chunks' and rows' order and by halving."""
+    x, s = inputs(R, W, V)
+    if kind == "equal":
+        x, s = torch.full_like(x, 0.25), torch.full_like(s, -3.0)
+    elif kind == "mask":                                    # the type's lowest value everywhere but in a few places
+        keep = torch.rand(x.shape, device="cuda") < 4 / V
+        x = x.masked_fill(~keep, torch.finfo(x.dtype).min)
+    else:                                                   # a few distinct values, rows that start alike
+        x, s = x.round().clamp(-2, 2), s.round()
+    check(x, s, wc.witcert_beam_select(x, s, n), n)
+
+
 @pytest.mark.parametrize("size", [1e4, 1e20, 3e38])
 def test_far_apart(size):
     """Scores and logits of any size: what 32 bits cannot tell apart, 64 do."""
