@@ -235,11 +235,17 @@ template <int SCH> cudaError_t launch_attend_few(const AttendArgs& a, cudaStream
 // KIVI tail; load: the most of a run of moves from one source.
 constexpr int kMoveKept = -1, kMoveNone = -2;
 constexpr int kMovesPerLaunch = 256;
-struct MoveOp {
+struct alignas(32) MoveOp {
   int src, dst;
   int n[2], load[2];
   int blocks;                // table entries that stay (a sequence that is only cut copies nothing)
   int cap;                   // the most tokens the sequence keeps
+};
+// Moves first[g] .. first[g + 1] - 1 have nothing to do with those of other groups.
+constexpr int kMoveGroups = 16;
+struct MoveGroups {
+  int n;
+  int first[kMoveGroups + 1];
 };
 struct MoveStream {          // rows of `unit` bytes counted by n[count], for each layer and head
   uint8_t* base;
@@ -250,11 +256,13 @@ struct MoveStream {          // rows of `unit` bytes counted by n[count], for ea
 struct MoveRows {
   MoveStream s[3];
   int n_streams, n;
+  MoveGroups group;
   MoveOp op[kMovesPerLaunch];
 };
 struct MoveInts {
   int32_t *table, *lens;     // [B][nblk_max], [layers][B]; null: not kept on the device
   int nblk_max, layers, B, n;
+  MoveGroups group;
   MoveOp op[kMovesPerLaunch];
 };
 // Pages src[k] (-1: nothing to copy) to dst[k] in every layer; table[idx[k]] = dst[k].

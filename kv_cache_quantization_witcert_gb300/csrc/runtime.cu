@@ -13,6 +13,7 @@
 #include <exception>
 #include <memory>
 #include <new>
+#include <numeric>
 #include <thread>
 #include <vector>
 
@@ -762,6 +763,7 @@ struct ForkPlan {
   std::vector<int> from, cap, blocks, tail;
   std::vector<MoveOp> ops;
   std::vector<size_t> launches;        // first move of each launch, and their end
+  std::vector<size_t> groups;          // first move of each set of sequences that have nothing to do with the others
 };
 
 static MoveOp fork_move(const ForkPlan& f, int src, int dst, int like, bool rows) {
@@ -774,14 +776,14 @@ static MoveOp fork_move(const ForkPlan& f, int src, int dst, int like, bool rows
   return op;
 }
 
-// The moves of a fork in an order in which none reads what an earlier one wrote.  First the sequences
-// that nobody reads any more, source by source, which frees their sources in turn; what is left are
+// The moves of a fork in an order in which none reads what an earlier one wrote, one connected set of
+// sequences (a request's beams) after another.  First the sequences that nobody reads any more, source by source, which frees their sources in turn; what is left are
 // cycles, each of which saves one row, moves the others up and hands the saved one out.  A launch holds
 // kMovesPerLaunch moves; a cycle that crosses its end is cut into two that share a sequence, the second
 // of which finds there what the first one saved.
 static void fork_moves(ForkPlan& f) {
   const int B = (int)f.from.size();
-  std::vector<int> readers(B, 0), first(B + 1, 0), kids, ready, next(B, -1);
+  std::vector<int> readers(B, 0), first(B + 1, 0), kids, ready;
   std::vector<char> done(B, 0);
   for (int i = 0; i < B; ++i)
     if (f.from[i] >= 0 && f.from[i] != i) ++readers[f.from[i]];
@@ -792,6 +794,20 @@ static void fork_moves(ForkPlan& f) {
     if (f.from[i] >= 0 && f.from[i] != i) kids[at[f.from[i]]++] = i;
     if (f.from[i] == i) done[i] = 1;
   }
+  // connected sets: each sequence points towards its set's representative
+  std::vector<int> set(B), member(B), start(B + 1, 0);
+  std::iota(set.begin(), set.end(), 0);
+  auto find = [&](int i) {
+    while (set[i] != i) i = set[i] = set[set[i]];
+    return i;
+  };
+  for (int i = 0; i < B; ++i)
+    if (f.from[i] >= 0) set[find(i)] = find(f.from[i]);
+  for (int i = 0; i < B; ++i) ++start[find(i) + 1];
+  for (int i = 0; i < B; ++i) start[i + 1] += start[i];
+  std::vector<int> fill(start.begin(), start.end() - 1);
+  for (int i = 0; i < B; ++i) member[fill[find(i)]++] = i;
+
   f.launches.push_back(0);
   auto room = [&] {
     if (f.ops.size() - f.launches.back() == kMovesPerLaunch) f.launches.push_back(f.ops.size());
@@ -802,40 +818,45 @@ static void fork_moves(ForkPlan& f) {
     f.ops.push_back(fork_move(f, f.from[i] >= 0 ? f.from[i] : kMoveNone, i, i, f.from[i] >= 0));
     done[i] = 1;
   };
-  for (int i = 0; i < B; ++i)
-    if (!done[i] && readers[i] == 0) ready.push_back(i);
-  while (!ready.empty()) {
-    const int i = ready.back(), src = f.from[i];
-    ready.pop_back();
-    if (done[i]) continue;
-    if (src < 0) { emit(i); continue; }
-    for (int k = first[src]; k < first[src + 1]; ++k)          // the source's other free children with it
-      if (!done[kids[k]] && readers[kids[k]] == 0) { emit(kids[k]); --readers[src]; }
-    if (!done[src] && readers[src] == 0) ready.push_back(src);
-  }
-  for (int i = 0; i < B; ++i) {
-    if (done[i]) continue;
-    int last = i;                                              // the sequence that takes i's row
-    for (int j = f.from[i]; j != i; j = f.from[j]) last = j;
-    int to = i;                                                // i <- from(i) <- ... <- last <- i
-    while (!done[last]) {
-      if (room() < 3) f.launches.push_back(f.ops.size());
-      f.ops.push_back(fork_move(f, to, kMoveKept, last, true));
-      f.ops.back().cap = INT_MAX;
-      while (to != last && room() > 1) {
-        emit(to);
-        to = f.from[to];
+  for (int g = 0; g < B; ++g) {
+    f.groups.push_back(f.ops.size());
+    for (int m = start[g]; m < start[g + 1]; ++m)
+      if (!done[member[m]] && readers[member[m]] == 0) ready.push_back(member[m]);
+    while (!ready.empty()) {
+      const int i = ready.back(), src = f.from[i];
+      ready.pop_back();
+      if (done[i]) continue;
+      if (src < 0) { emit(i); continue; }
+      for (int k = first[src]; k < first[src + 1]; ++k)        // the source's other free children with it
+        if (!done[kids[k]] && readers[kids[k]] == 0) { emit(kids[k]); --readers[src]; }
+      if (!done[src] && readers[src] == 0) ready.push_back(src);
+    }
+    for (int m = start[g]; m < start[g + 1]; ++m) {
+      const int i = member[m];
+      if (done[i]) continue;
+      int last = i;                                            // the sequence that takes i's row
+      for (int j = f.from[i]; j != i; j = f.from[j]) last = j;
+      int to = i;                                              // i <- from(i) <- ... <- last <- i
+      while (!done[last]) {
+        if (room() < 3) f.launches.push_back(f.ops.size());
+        f.ops.push_back(fork_move(f, to, kMoveKept, last, true));
+        f.ops.back().cap = INT_MAX;
+        while (to != last && room() > 1) {
+          emit(to);
+          to = f.from[to];
+        }
+        f.ops.push_back(fork_move(f, kMoveKept, to, last, true));
+        if (to == last) done[last] = 1; else f.ops.back().cap = INT_MAX;
       }
-      f.ops.push_back(fork_move(f, kMoveKept, to, last, true));
-      if (to == last) done[last] = 1; else f.ops.back().cap = INT_MAX;
     }
+    for (int m = start[g]; m < start[g + 1]; ++m)              // sequences that are only cut, after their readers
+      if (f.from[member[m]] == member[m] && f.cap[member[m]] >= 0) {
+        room();
+        f.ops.push_back(fork_move(f, member[m], member[m], member[m], false));
+      }
   }
-  for (int i = 0; i < B; ++i)                                  // sequences that are only cut, after their readers
-    if (f.from[i] == i && f.cap[i] >= 0) {
-      room();
-      f.ops.push_back(fork_move(f, i, i, i, false));
-    }
   f.launches.push_back(f.ops.size());
+  f.groups.push_back(f.ops.size());
   // a run of moves from one source in one launch loads once what the largest of them takes
   for (size_t l = 0; l + 1 < f.launches.size(); ++l)
     for (size_t m = f.launches[l], to = m; m < f.launches[l + 1]; m = to) {
@@ -949,6 +970,15 @@ witcert_status witcert_fork(witcert_cache* c, const int32_t* parents, const int3
   ints.B = B;
   for (size_t k = 0; k + 1 < f.launches.size() && e == cudaSuccess; ++k) {
     const size_t m0 = f.launches[k], n = f.launches[k + 1] - m0;
+    // up to kMoveGroups groups of about as many moves, each run down by threads of its own
+    MoveGroups split{};
+    split.first[0] = 0;
+    for (size_t g : f.groups) {
+      if (g <= m0 || g >= m0 + n || split.n + 1 == kMoveGroups) continue;
+      if (g - m0 - split.first[split.n] >= (n + kMoveGroups - 1) / kMoveGroups) split.first[++split.n] = (int)(g - m0);
+    }
+    split.first[++split.n] = (int)n;
+    rows.group = ints.group = split;
     rows.n = ints.n = (int)n;
     std::copy_n(f.ops.data() + m0, n, rows.op);
     std::copy_n(f.ops.data() + m0, n, ints.op);
