@@ -32,14 +32,18 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+def _torch_stream(stream):
+    """The torch stream of a call's stream argument (None for the current one)."""
+    return stream if stream is None or isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(stream.cuda_stream)
+
+
 def _empty(stream, shape, dtype, device="cuda"):
     """An output or workspace of a call on `stream` (None: the current stream).  It comes from that
     stream's memory: a block freed on the current stream may still be in use by work queued there, which
     another stream does not wait for.  It may be used on the current stream too (ordering is the caller's)."""
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(stream.cuda_stream)
+    stream = _torch_stream(stream)
     here = torch.cuda.current_stream(stream.device)
     with torch.cuda.stream(stream):
         t = torch.empty(shape, dtype=dtype, device=device)
@@ -579,7 +583,7 @@ class BeamSearch:
         """Hand each request's prompt, in its first beam's sequence, to the other beams."""
         W = self.shape[1]
         self.cache.witcert_fork([i // W * W for i in range(self.cache.cfg.batch)], stream=stream)
-        with torch.cuda.stream(stream):
+        with torch.cuda.stream(_torch_stream(stream)):
             self._restart()
 
     def step(self, logits, stream=None):
@@ -592,7 +596,7 @@ class BeamSearch:
         done = self.finished if self.eos >= 0 else None
         witcert_beam_select(logits, self.scores, finished=done, eos=self.eos,
                             out=(self.scores, rows, tokens, self.finished), stream=stream)
-        with torch.cuda.stream(stream):
+        with torch.cuda.stream(_torch_stream(stream)):
             parents = rows.flatten().tolist()
         # a request with fewer candidates than beams leaves the others where they are
         self.cache.witcert_fork([i if p < 0 else p for i, p in enumerate(parents)], stream=stream)

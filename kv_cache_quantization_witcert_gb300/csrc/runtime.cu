@@ -420,6 +420,7 @@ static witcert_status take_pages(witcert_cache* c, int layer, const std::vector<
 
 // The device's side of take_pages: copies and table entries.  Copies end before what follows starts.
 static cudaError_t push_pages(witcert_cache* c, const std::vector<PageTaken>& taken, cudaStream_t st, bool& pdl) {
+  if (taken.empty()) return cudaSuccess;
   CopyPages a{};
   a.blocks = c->blocks;
   a.layer_pitch = (long long)c->layer_blocks;
@@ -725,7 +726,6 @@ witcert_status witcert_truncate(witcert_cache* c, int layer, const int32_t* leng
   auto st = static_cast<cudaStream_t>(stream);
   bool waited = false;
   for (int l = l0; l < l1; ++l) waited |= order_after_gate(c, l, st);
-  bool pdl = may_overlap(c, waited);
   // lengths that stay equal need no copy on the device
   bool uniform = !c->ragged;
   for (int l = l0; l < l1 && uniform; ++l)
@@ -733,6 +733,7 @@ witcert_status witcert_truncate(witcert_cache* c, int layer, const int32_t* leng
       uniform = std::min(c->slen[l][i], (int)lengths[i]) == std::min(c->slen[l][0], (int)lengths[0]);
   cudaError_t e = cudaSuccess;
   if (!uniform) {
+    bool pdl = may_overlap(c, waited);
     e = enter_ragged(c, st, pdl);
     std::vector<std::pair<int, int>> upd;
     for (int l = l0; l < l1; ++l)
