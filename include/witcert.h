@@ -265,7 +265,8 @@ witcert_status witcert_attend_workspace(const witcert_cache* cache, int layer, c
  * nothing written).  Value witnesses and the unfinished KIVI2 block's keys are each sequence's own, and
  * copied.  Block risks become stale.  EINVAL for a bad parent, a negative length, a KIVI2 cut that would reopen a
  * finished block (as for witcert_truncate), and for a gated cache: repairs and the backing store belong to
- * one sequence.  Asynchronous on `stream`. */
+ * one sequence; ESTATE on a stream that is being captured (a replay would move the device's sequences
+ * alone).  Asynchronous on `stream`. */
 witcert_status witcert_fork(witcert_cache* cache, const int32_t* parents, const int32_t* lengths, void* stream);
 
 /* Empty sequence `seq` in every layer so the slot can serve a new request (continuous

@@ -427,9 +427,8 @@ static cudaError_t push_pages(witcert_cache* c, const std::vector<PageTaken>& ta
   a.page_bytes = (long long)c->cfg.n_kv_heads * c->bblk;
   a.table = c->table;
   cudaError_t e = cudaSuccess;
-  std::vector<std::pair<int, int>> upd;
   for (const PageTaken& u : taken) {
-    if (!u.copy) { upd.emplace_back(u.idx, u.now); continue; }
+    if (!u.copy) continue;
     a.src[a.n] = u.was; a.dst[a.n] = u.now; a.idx[a.n] = u.idx;
     pdl = false;
     if (++a.n == kRaggedPerLaunch) {
@@ -438,7 +437,17 @@ static cudaError_t push_pages(witcert_cache* c, const std::vector<PageTaken>& ta
     }
   }
   if ((e = launch_copy_pages(a, c->cfg.n_layers, st)) != cudaSuccess) return e;
-  return push_ints(c->table, upd, st, pdl);
+  LengthArgs t{};                                              // no host allocation: the pages are taken
+  t.dst = c->table;
+  for (const PageTaken& u : taken) {
+    if (u.copy) continue;
+    t.idx[t.n] = u.idx; t.len[t.n] = u.now;
+    if (++t.n == kRaggedPerLaunch) {
+      if ((e = launch_set_lengths(t, st, pdl)) != cudaSuccess) return e;
+      t.n = 0;
+    }
+  }
+  return launch_set_lengths(t, st, pdl);
 }
 
 // From now on the sequences' lengths may differ: the device gets every layer's lengths.
@@ -935,6 +944,11 @@ witcert_status witcert_fork(witcert_cache* c, const int32_t* parents, const int3
     if (p != i || cut || spare) { any = true; f.cap[i] = cap; }
   }
   if (!any) { ok(); return WITCERT_OK; }
+  auto st = static_cast<cudaStream_t>(stream);
+  cudaStreamCaptureStatus capturing = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(st, &capturing) != cudaSuccess) cudaGetLastError();
+  if (capturing != cudaStreamCaptureStatusNone)
+    return fail(WITCERT_ESTATE, "a fork cannot be captured: the lengths and pages on the host would not follow a replay");
   fork_moves(f);
   // host memory first: nothing may fail between what the device and what the host is told
   std::vector<std::vector<int>> slen(L, std::vector<int>(B));
@@ -946,7 +960,6 @@ witcert_status witcert_fork(witcert_cache* c, const int32_t* parents, const int3
       equal &= slen[l][i] == slen[l][0];
     }
   std::vector<int32_t> kept(c->table ? c->nblk_max : 0);
-  auto st = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
   bool pdl = false;
   if (!equal) e = enter_ragged(c, st, pdl);

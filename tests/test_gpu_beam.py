@@ -248,6 +248,20 @@ def test_first_step_and_in_place():
                                for t in (torch.int32, torch.int32, torch.bool))))
 
 
+def test_logits_beyond_32_bits():
+    """More than 2^31 elements, and strides as large: the requests at both ends as by themselves."""
+    R, W, V = 130, 128, 131073
+    x = torch.empty(R, W, V, dtype=torch.bfloat16, device="cuda").normal_(0, 3)
+    s = -torch.rand(R, W, device="cuda")
+    got = wc.witcert_beam_select(x, s, 16)
+    for r in (0, R - 1):
+        one = wc.witcert_beam_select(x[r:r + 1].clone(), s[r:r + 1].clone(), 16)
+        assert torch.equal(got[2][r], one[2][0]) and torch.equal(got[1][r], one[1][0] + r * W)
+        assert (got[0][r] - one[0][0]).abs().max() <= 2.0 ** -18      # the rows' parts are summed in other places
+    far = x.view(-1)[:V * 2].as_strided((2, 1, V), (V * 16000, V, 1))
+    check(far, s[:2, :1].contiguous(), wc.witcert_beam_select(far, s[:2, :1].contiguous(), 4), 4)
+
+
 def test_no_requests():
     got = wc.witcert_beam_select(torch.empty(0, 4, 100, device="cuda"), torch.empty(0, 4, device="cuda"), 7)
     assert [tuple(t.shape) for t in got] == [(0, 7)] * 4

@@ -245,3 +245,42 @@ def test_refusals():
     with pytest.raises(wc.WitcertError, match="gated") as e:
         gated.witcert_fork([0, 0])
     assert e.value.status == _lib.EINVAL
+
+
+def test_a_fork_is_not_captured():
+    c = wc.Cache(1, 4, 2, 2, 64, "fp8_e4m3")
+    k = rows(40)
+    write(c, 0, [20, 20], k, k)
+    want = [x.clone() for x in c.read(0, [20, 20])]
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        x = k + 1
+        with pytest.raises(wc.WitcertError, match="captured") as e:
+            c.witcert_fork([1, 0])
+    assert e.value.status == _lib.ESTATE and x.shape == k.shape
+    assert all(torch.equal(a, b) for a, b in zip(want, c.read(0, [20, 20])))
+    c.witcert_fork([1, 0])
+    assert all(torch.equal(a, b.view(2, 20, 2, 128).flip(0).flatten(0, 1)) for a, b in zip(want, c.read(0, [20, 20])))
+
+
+@pytest.mark.parametrize("pages", [0, 8 * 8200])
+def test_stores_beyond_32_bits(pages):
+    """4.5 GB: the last rows of every sequence, forked, shared and appended to."""
+    B, S, H = 8, 131000, 8
+    c = wc.Cache(1, H, H, B, S + 8, "blackbox", max_pages=pages)
+    n = [S - 7 * i for i in range(B)]
+    for i in range(B):
+        m = [0] * B
+        m[i] = n[i]
+        k = torch.randn(n[i], H, 128, device="cuda").bfloat16()
+        c.witcert_write_ragged(0, k, k, m, k, k)
+    at = lambda lens: [x - 40 for x in lens]
+    last = [x.split(40) for x in c.read(0, [40] * B, at(n))]
+    parents = [7, 5, 1, 0, 2, 3, 4, 0]
+    c.witcert_fork(parents)
+    n = [n[p] for p in parents]
+    new = torch.randn(B, H, 128, device="cuda").bfloat16()
+    c.witcert_write_ragged(0, new, new, [1] * B, new, new)
+    for got, want in zip(c.read(0, [41] * B, at(n)), last):
+        assert torch.equal(got, torch.cat([x for i, p in enumerate(parents) for x in (want[p], new[i:i + 1])]))
