@@ -405,7 +405,7 @@ witcert_status witcert_gate_select(const float* risk, const uint8_t* repaired, i
  * the score scores[row] + x_token - log sum exp x; a finished one only itself, as token `eos` with its own
  * score.  No candidates come from a row whose score is not finite (an absent beam), from one that has no
  * softmax (+inf or NaN among its logits, or nothing but -inf), or of a logit of -inf.  Candidates
- * are ordered by score (formed in 64 bits; sums of exponentials in fp32), then row, then token.
+ * are ordered by score (formed in 64 bits; sums of exponentials in fp32), then row, then logit, then token.
  * rows, tokens, out_scores (device [n_requests][n_out]) take the row a candidate continues, its token and
  * score; places for which there is no candidate get -1, -1 and -inf.  out_finished, if given, says whether a
  * candidate's row had finished or its token is eos.  With n_out = n_beams, rows serve as witcert_fork's
@@ -413,7 +413,7 @@ witcert_status witcert_gate_select(const float* risk, const uint8_t* repaired, i
 typedef struct {
   witcert_dtype dtype;               /* of the logits */
   int n_requests, n_beams;           /* n_beams at most 128 */
-  int vocab;                         /* tokens, at most 2^27 */
+  int vocab;                         /* tokens, at most 2^25 */
   int n_out;                         /* at most 256 */
   int eos;                           /* -1: no token ends a beam (finished is NULL then) */
   const void* logits;

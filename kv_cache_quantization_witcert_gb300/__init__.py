@@ -587,9 +587,12 @@ class BeamSearch:
             self._restart()
 
     def step(self, logits, stream=None):
-        """Choose the continuations of all beams from logits [R, W, V] and move the cache's sequences."""
+        """Choose the continuations of all beams from logits [R, W, V] (or [R * W, V], a row a sequence of the
+        cache) and move the cache's sequences."""
         if self.steps == len(self._rows):
             raise ValueError(f"the search was made for {len(self._rows)} steps")
+        if isinstance(logits, torch.Tensor) and logits.dim() == 2 and logits.shape[0] == self.shape[0] * self.shape[1]:
+            logits = logits.unflatten(0, self.shape)
         if not isinstance(logits, torch.Tensor) or tuple(logits.shape[:2]) != self.shape:
             raise ValueError(f"logits must be a torch.Tensor [{self.shape[0]}, {self.shape[1]}, vocabulary]")
         rows, tokens = self._rows[self.steps], self._tokens[self.steps]

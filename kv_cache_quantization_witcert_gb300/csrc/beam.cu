@@ -3,13 +3,15 @@
 // Selection.  A live row (request, beam) of logits x and score c offers s_v = c + x_v - log sum exp x, formed
 // as (c - log sum exp(x - m)) + (x_v - m) with the row's maximum m.  Two launches:
 //
-//   scan   one pass over the logits: for every chunk of kChunk tokens its maximum, for every warp's run of
-//          chunks the maximum m and sum exp(x - m).  Bound by HBM; five lane operations an element.
+//   scan   one pass over the logits: for every chunk of kChunk tokens its maximum, for every warp's chunks the
+//          maximum m and sum exp(x - m).  Bound by HBM and, at both ends of the launch, by latency: 64 x 8 rows of
+//          131072 bf16 tokens 22 us, 6.1 TB/s (a bare read of them 20.5).
 //   pick   one CTA a request.  The n best candidates lie in the n chunks with the best maxima (ordered as
 //          candidates are: a candidate in any other chunk is beaten by n chunk maxima), so it ranks the
-//          chunks' maxima, reads those n chunks again and ranks their elements.  Bound by latency.
+//          chunks' maxima, reads those n chunks again and ranks their elements.  Bound by the latency of
+//          its phases: about 5 us for 4 beams and 8 out, 6 for 8 and 16, 13 for 32 and 64.
 //
-// Ranking goes by a key in 64 bits, (s, lower row, lower token).  Most of the work is a filter in 32 bits:
+// Ranking goes by (s in 64 bits, lower row, larger logit, lower token).  Most of the work is a filter in 32 bits:
 // a lower bound of the n-th best key comes from the largest keys of groups of threads, every key that its
 // rounding does not put below that bound is listed, and only the list is formed in 64 bits (whose rate is a
 // 64th of fp32's) and ranked by counting.
@@ -101,6 +103,7 @@ __device__ __forceinline__ void two_sum(float& s, float& lost, float x) {
 
 // A warp's chunks on their way: each lane copies its own pieces of a chunk to shared memory and reads them back
 // itself, so that a wait for the lane's own copies is all there is to wait for.
+// 48 warps of 4 KB, loops of launches, us: 26.2 by 28 parts a row, 26.5 by 9; 32 warps of 6 KB 26.6, 30.0.
 constexpr int kRing = 4 * 1024;                  // bytes of a warp's chunks in shared memory
 template <typename T>
 struct Ring {
@@ -278,7 +281,7 @@ struct alignas(16) Chosen {  // a chosen chunk
 };
 template <typename T>
 struct PickShared {
-  unsigned __int128 key[kList];                  // listed: a logit's bits above its place; then the score above ~place
+  unsigned __int128 key[kList];                  // listed: a logit's bits above its place; then its key (Pick::exact)
   Chosen<T> chunk[kBeamMaxOut];
   int row[kBeamMaxOut];                          // the chosen chunks' beams
   double base[kBeamMaxBeams];                    // score - log sum exp(x - top): a logit's key is base + (x - top)
@@ -342,32 +345,36 @@ struct Pick {
     const int at = atomicAdd(&sh.count, 1);
     if (at < kList) sh.key[at] = (unsigned __int128)__float_as_uint(x) << 64 | place;
   }
+  // Orders like the logits, one zero.
+  __device__ __forceinline__ static uint32_t ordered32(float x) {
+    const uint32_t b = __float_as_uint(x + 0.f);
+    return b & 0x80000000u ? ~b : b | 0x80000000u;
+  }
+  // The key of a listed candidate, larger ones first: the score, ~beam (7 bits), the logit (32), ~number (25).
   __device__ __forceinline__ unsigned __int128 exact(unsigned __int128 k) const {
-    const unsigned long long place = (unsigned long long)k;
-    return (unsigned __int128)key(__uint_as_float((uint32_t)(k >> 64)), (int)(place >> 32)) << 64 | ~place;
+    const unsigned long long w = (unsigned long long)k >> 32, number = (uint32_t)k;
+    const float x = __uint_as_float((uint32_t)(k >> 64));
+    const unsigned long long place = w << 57 | (unsigned long long)~ordered32(x) << 25 | number;
+    return (unsigned __int128)key(x, (int)w) << 64 | ~place;
   }
 
   // The q first of a warp's candidates of one row, by logit and then in order: value(j), j = 0 .. m - 1, are the
   // lane's logits (-inf: none), those of lower lanes come first.  Calls visit(j, logit) for each.
   template <class Value, class Visit>
   __device__ __forceinline__ void first_of(int m, int q, Value&& value, Visit&& visit) const {
-    auto rank_of = [](float x) {                               // orders like the logits, one zero
-      const uint32_t b = __float_as_uint(x + 0.f);
-      return b & 0x80000000u ? ~b : b | 0x80000000u;
-    };
     auto count = [&](uint32_t least) {
       int c = 0;
-      for (int j = 0; j < m; ++j) c += rank_of(value(j)) >= least;
+      for (int j = 0; j < m; ++j) c += ordered32(value(j)) >= least;
       return (int)__reduce_add_sync(0xffffffffu, c);
     };
-    uint32_t lo = rank_of(-FLT_MAX), hi = rank_of(FLT_MAX);
+    uint32_t lo = ordered32(-FLT_MAX), hi = ordered32(FLT_MAX);
     if (count(lo) > q)
       while (lo < hi) {                                        // the largest that q of them reach
         const uint32_t mid = lo + (hi - lo) / 2 + 1;
         if (count(mid) >= q) lo = mid; else hi = mid - 1;
       }
     int same = 0;
-    for (int j = 0; j < m; ++j) same += rank_of(value(j)) == lo;
+    for (int j = 0; j < m; ++j) same += ordered32(value(j)) == lo;
     int before = same;                                         // those equal to it in lower lanes
     for (int o = 1; o < 32; o *= 2) {
       const int v = __shfl_up_sync(0xffffffffu, before, o);
@@ -377,12 +384,12 @@ struct Pick {
     const int room = q - count(lo + 1);
     for (int j = 0; j < m; ++j) {
       const float x = value(j);
-      const uint32_t k = rank_of(x);
+      const uint32_t k = ordered32(x);
       if (k > lo || (k == lo && before++ < room)) visit(j, x);
     }
   }
 
-  // Ranks the listed keys and calls put(rank, s, place) on one thread for each of the n first.  If more were listed
+  // Ranks the listed keys and calls put(rank, score, beam, number) on one thread for each of the n first.  If more were listed
   // than fit (very many equal or nearly equal keys), few() lists only those that their row's or chunk's own order
   // leaves, at most `at_most` of them; if these may be too many as well, each(visit) visits all candidates again,
   // and a bound is found by halving the space of the keys, which are distinct.  Returns how many there are.
@@ -414,6 +421,10 @@ struct Pick {
         } while (listed < n || listed > kList);
       }
     }
+    auto put_key = [&](int rank, unsigned __int128 k) {
+      const unsigned long long place = ~(unsigned long long)k;
+      put(rank, unordered((unsigned long long)(k >> 64)), (int)(place >> 57), (int)(place & 0x1FFFFFF));
+    };
     for (int i = tid; i < listed; i += kPickThreads) sh.key[i] = exact(sh.key[i]);
     __syncthreads();
     if (listed <= kCounted) {
@@ -425,7 +436,7 @@ struct Pick {
         for (int j = tid % 8; j < listed; j += 8) rank += sh.key[j] > k;
 #pragma unroll
         for (int o = 4; o > 0; o /= 2) rank += __shfl_xor_sync(0xffffffffu, rank, o);
-        if (tid % 8 == 0 && i < listed && rank < n) put(rank, (unsigned long long)(k >> 64), ~(unsigned long long)k);
+        if (tid % 8 == 0 && i < listed && rank < n) put_key(rank, k);
       }
     } else {                                                   // sorted by exchanges, the largest first
       int size = 2 * kCounted;
@@ -441,7 +452,7 @@ struct Pick {
           }
         }
       __syncthreads();
-      if (tid < min(listed, n)) put(tid, (unsigned long long)(sh.key[tid] >> 64), ~(unsigned long long)sh.key[tid]);
+      if (tid < min(listed, n)) put_key(tid, sh.key[tid]);
     }
     return min(listed, n);
   }
@@ -619,12 +630,11 @@ __global__ void __launch_bounds__(kPickThreads, 1) beam_pick_kernel(const __grid
       }, [&](int j, float v) { p.add(v, (unsigned long long)w << 32 | (uint32_t)(w * a.chunks + c0 + j)); });
     }
   };
-  const int chosen = p.rank(chunks, a.beams * n, few_chunks, [&](int rank, unsigned long long s, unsigned long long place) {
-    const int w = (int)(place >> 32);
+  const int chosen = p.rank(chunks, a.beams * n, few_chunks, [&](int rank, double s, int w, int i) {
     const Row<T> row(a, r, w);
-    sh.chunk[rank] = Chosen<T>{row.x, row.token((int)(uint32_t)place - w * a.chunks, 0), 0.f};
+    sh.chunk[rank] = Chosen<T>{row.x, row.token(i - w * a.chunks, 0), 0.f};
     sh.row[rank] = w;
-    if (rank == n - 1) sh.bound = (float)unordered(s);         // n chunks' maxima are n tokens
+    if (rank == n - 1) sh.bound = (float)s;                    // n chunks' maxima are n tokens
   });
   __syncthreads();
 
@@ -672,9 +682,8 @@ __global__ void __launch_bounds__(kPickThreads, 1) beam_pick_kernel(const __grid
       }, [&](int j, float x) { p.add(x, w | (uint32_t)(c.first + lane * kLane + j)); });
     }
   };
-  const int found = p.rank(tokens, chosen * (2 * n - chosen + 1) / 2, few_tokens, [&](int rank, unsigned long long s, unsigned long long place) {
-    const int w = (int)(place >> 32), token = (int)(uint32_t)place;
-    a.out_scores[to + rank] = (float)unordered(s);
+  const int found = p.rank(tokens, chosen * (2 * n - chosen + 1) / 2, few_tokens, [&](int rank, double s, int w, int token) {
+    a.out_scores[to + rank] = (float)s;
     a.rows[to + rank] = r * a.beams + w;
     a.tokens[to + rank] = token;
     if (a.out_finished) a.out_finished[to + rank] = sh.state[w] == 2 || token == a.eos;

@@ -1535,7 +1535,7 @@ static witcert_status beam_args(const witcert_beam_step* s, BeamArgs& a, size_t&
   if (s->dtype != WITCERT_F32 && s->dtype != WITCERT_BF16) return fail(WITCERT_EINVAL, "unknown dtype %d", (int)s->dtype);
   if (s->n_requests < 0) return fail(WITCERT_EINVAL, "n_requests must be >= 0");
   if (s->n_beams < 1 || s->n_beams > kBeamMaxBeams) return fail(WITCERT_EINVAL, "n_beams must be in [1, %d] (got %d)", kBeamMaxBeams, s->n_beams);
-  if (s->vocab < 1 || s->vocab > 1 << 27) return fail(WITCERT_EINVAL, "vocab must be in [1, 2^27] (got %d)", s->vocab);
+  if (s->vocab < 1 || s->vocab > 1 << 25) return fail(WITCERT_EINVAL, "vocab must be in [1, 2^25] (got %d)", s->vocab);
   if (s->n_out < 1 || s->n_out > kBeamMaxOut) return fail(WITCERT_EINVAL, "n_out must be in [1, %d] (got %d)", kBeamMaxOut, s->n_out);
   if (s->eos < -1 || s->eos >= s->vocab) return fail(WITCERT_EINVAL, "eos must be in [-1, %d) (got %d)", s->vocab, s->eos);
   if (s->finished && s->eos < 0) return fail(WITCERT_EINVAL, "finished beams need eos");

@@ -23,11 +23,11 @@ GOOD = dict(dtype=_lib.BF16, n_requests=2, n_beams=4, vocab=1000, n_out=4, eos=7
 
 @pytest.mark.parametrize("change, text", [
     (dict(dtype=7), b"dtype"), (dict(n_requests=-1), b"n_requests"), (dict(n_beams=0), b"n_beams"), (dict(n_beams=129), b"n_beams"),
-    (dict(vocab=0), b"vocab"), (dict(vocab=2 ** 27 + 1), b"vocab"), (dict(n_out=0), b"n_out"), (dict(n_out=257), b"n_out"),
+    (dict(vocab=0), b"vocab"), (dict(vocab=2 ** 25 + 1), b"vocab"), (dict(n_out=0), b"n_out"), (dict(n_out=257), b"n_out"),
     (dict(eos=1000), b"eos"), (dict(eos=-2), b"eos"), (dict(eos=-1), b"eos"), (dict(n_requests=2 ** 30), b"rows"),
     (dict(logits=4097), b"aligned"), (dict(logits=None), b"NULL"), (dict(scores=None), b"NULL"), (dict(out_scores=None), b"NULL"),
     (dict(rows=None), b"NULL"), (dict(tokens=None), b"NULL"), (dict(n_out=8, out_scores=4096), b"n_out = n_beams"),
-    (dict(n_out=8, out_finished=4096), b"n_out = n_beams"), (dict(n_requests=2 ** 24, vocab=2 ** 27), b"logits"), ({}, b"workspace")])
+    (dict(n_out=8, out_finished=4096), b"n_out = n_beams"), (dict(n_requests=2 ** 24, vocab=2 ** 25), b"logits"), ({}, b"workspace")])
 def test_steps(lib, change, text):
     step = _lib.witcert_beam_step(**{**GOOD, **change})
     assert lib.witcert_beam_select(ctypes.addressof(step), None, 1 << 40, None) == _lib.EINVAL

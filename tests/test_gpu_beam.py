@@ -200,6 +200,17 @@ def test_many_alike(R, W, V, n, kind):
     check(x, s, wc.witcert_beam_select(x, s, n), n)
 
 
+@pytest.mark.parametrize("V, n", [(900, 4), (120001, 24), (140001, 200)])
+def test_logits_that_the_score_does_not_tell_apart(V, n):
+    """Next to a score of -1e12 (2^-13 apart in 64 bits) logits 1e-7 apart vanish, but still order their row."""
+    x, s = inputs(1, 3, V, torch.float32, scale=1e-3)
+    s.fill_(-1e12)
+    x[0, 0, 5:400] = 0.5 + 1e-7 * (torch.arange(395, device="cuda") // 2)     # pairs of equal ones among them
+    rows, tokens = (t[0].cpu().numpy() for t in wc.witcert_beam_select(x, s, n)[1:3])
+    order = np.lexsort((np.arange(V), -x[0, 0].cpu().numpy()))[:n]
+    assert (rows == 0).all() and (tokens == order).all()
+
+
 @pytest.mark.parametrize("size", [1e4, 1e20, 3e38])
 def test_far_apart(size):
     """Scores and logits of any size: what 32 bits cannot tell apart, 64 do."""
@@ -422,3 +433,31 @@ def test_search_with_fewer_candidates_than_beams():
     x[1] = math.nan
     assert search.step(x).tolist() == [[4, -1, -1], [-1] * 3]
     assert search.paths(pad=9).tolist() == [[[4, 4], [9, 9], [9, 9]], [[9, 9]] * 3]
+
+
+def test_search_on_a_stream():
+    """All of it on another stream than the current one, logits a row a sequence, as on the current stream."""
+    side, out = torch.cuda.Stream(), []
+    k = torch.randn(2 * 70, 2, 128, device="cuda").bfloat16()
+    xs = [inputs(2, 3, 999, seed=i)[0].flatten(0, 1) for i in range(5)]
+    torch.cuda.synchronize()
+    for stream in (None, side):
+        cache = wc.Cache(1, 4, 2, 6, 80, "int8_rtn", max_pages=30)
+        cache.witcert_write_ragged(0, k, k, [70, 0, 0, 70, 0, 0], stream=stream)
+        search = wc.BeamSearch(cache, 3, 5, eos=1)
+        torch.cuda.synchronize()                            # what the search keeps was made on the current stream
+        search.start(stream=stream)
+        for x in xs:
+            tokens = search.step(x, stream=stream)
+            new = k[:6] * 0.5
+            torch.cuda.synchronize()
+            cache.witcert_write_ragged(0, new, new, [1] * 6, stream=stream)
+        paths = search.paths(stream=stream)
+        torch.cuda.synchronize()
+        assert torch.equal(paths[..., -1], tokens)
+        out.append([paths, search.scores, *cache.read(0, [75] * 6)])
+    assert all(torch.equal(a, b) for a, b in zip(*out))
+    for bad in (xs[0][:5], xs[0].unflatten(0, (3, 2)), None):
+        fresh = wc.BeamSearch(cache, 3, 1)
+        with pytest.raises(ValueError, match="logits"):
+            fresh.step(bad)
