@@ -238,8 +238,14 @@ class Cache:
 
     def _counts(self, name, values):
         """One host integer per sequence, as the library takes them."""
-        counts = [int(x) for x in values]
         batch = self.cfg.batch
+        if type(values) is list and len(values) == batch:
+            try:                                # whole numbers that fit: what nearly every call passes
+                arr = array.array("i", values)
+                return arr.tolist(), (ctypes.c_int32 * batch).from_buffer(arr)
+            except (TypeError, OverflowError):
+                pass
+        counts = [int(x) for x in values]
         if len(counts) != batch:
             raise ValueError(f"{name} needs one count per sequence ({batch}), got {len(counts)}")
         try:
