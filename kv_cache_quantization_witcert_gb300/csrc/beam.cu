@@ -1,7 +1,8 @@
 // Beam search: the best continuations of each request, and the token sequences of its beams.
 //
 // Selection.  A live row (request, beam) of logits x and score c offers s_v = c + x_v - log sum exp x, formed
-// as (c - log sum exp(x - m)) + (x_v - m) with the row's maximum m.  Two launches:
+// as (c - log sum exp(x - m)) + (x_v - m) with the row's maximum m.  Two steps, a launch each, or for few small
+// requests one launch of clusters:
 //
 //   scan   one pass over the logits: for every chunk of kChunk tokens its maximum, for every warp's chunks the
 //          maximum m and sum exp(x - m).  Bound by HBM and, at both ends of the launch, by latency: 64 x 8 rows of
@@ -40,6 +41,9 @@ __device__ __forceinline__ float redux_max(float x) {
   return y;
 }
 
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n barrier.cluster.wait.acquire;" ::: "memory");
+}
 template <typename T>
 struct Row {
   static constexpr int kWords = kLane * sizeof(T) / 4;         // registers a lane's part of a chunk takes
@@ -210,19 +214,18 @@ struct LaneSum {
   }
 };
 
-template <typename T>
-__global__ void __launch_bounds__(kScanWarps * 32, kBeamScanWarps / kScanWarps) beam_scan_kernel(const __grid_constant__ BeamArgs a) {
-  __shared__ __align__(16) uint8_t held[kScanWarps * kRing];
+// A warp's part of beam w of request r; `held`, kRing bytes of shared memory, is the warp's.  after(): behind the last
+// load, before the sums are written.
+template <typename T, class After>
+__device__ __forceinline__ void scan_part(const BeamArgs& a, uint8_t* held, int r, int w, int part, After&& after) {
   const int lane = threadIdx.x & 31;
-  const uint32_t wid = blockIdx.x * kScanWarps + (threadIdx.x >> 5), row = wid / (uint32_t)a.parts;
-  if (row >= (uint32_t)a.requests * a.beams) return;
-  const int part = (int)(wid - row * a.parts), r = (int)(row / (uint32_t)a.beams), w = (int)(row - r * (uint32_t)a.beams);
+  const uint32_t row = (uint32_t)r * a.beams + w;
   if (!live(a.scores[row]) || (a.finished && a.finished[row])) return;
   const Row<T> x(a, r, w);
   float* maxima = a.maxima + (size_t)row * a.chunks;
   LaneSum l;
   // every parts-th chunk: the row's warps read side by side
-  const Ring<T> ring{smem_addr(held) + (threadIdx.x >> 5) * kRing + lane * 16, lane};
+  const Ring<T> ring{smem_addr(held) + lane * 16, lane};
   constexpr int kStages = Ring<T>::kStages;
   const T* from = x.x + x.token(part, lane * Ring<T>::kPiece);
   const long long step = (long long)a.parts * kChunk;
@@ -252,12 +255,21 @@ __global__ void __launch_bounds__(kScanWarps * 32, kBeamScanWarps / kScanWarps) 
       if (c >= a.chunks) break;
     }
   }
-  // not before: the next kernel's blocks would take registers that scan blocks still to come need
-  pdl_trigger();
+  after();
   float sum = l.total();
 #pragma unroll
   for (int o = 16; o > 0; o /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (lane == 0) a.records[wid] = make_float2(l.m, sum);
+  if (lane == 0) a.records[row * a.parts + part] = make_float2(l.m, sum);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kScanWarps * 32, kBeamScanWarps / kScanWarps) beam_scan_kernel(const __grid_constant__ BeamArgs a) {
+  __shared__ __align__(16) uint8_t held[kScanWarps * kRing];
+  const uint32_t warp = threadIdx.x >> 5, wid = blockIdx.x * kScanWarps + warp, row = wid / (uint32_t)a.parts;
+  if (row >= (uint32_t)a.requests * a.beams) return;
+  const uint32_t r = row / (uint32_t)a.beams;
+  // the next kernel's blocks not before the end: they would take registers that scan blocks still to come need
+  scan_part<T>(a, held + warp * kRing, (int)r, (int)(row - r * a.beams), (int)(wid - row * a.parts), [] { pdl_trigger(); });
 }
 
 // ------------------------------------------------------------------ pick
@@ -527,11 +539,10 @@ struct Pick {
   }
 };
 
-template <typename T>
-__global__ void __launch_bounds__(kPickThreads, 1) beam_pick_kernel(const __grid_constant__ BeamArgs a) {
-  extern __shared__ __align__(16) uint8_t smem[];
-  PickShared<T>& sh = *reinterpret_cast<PickShared<T>*>(smem);
-  const int r = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, n = a.n_out;
+// Ranks request r's candidates, one CTA; scanned(): waits for the scan.
+template <typename T, class Scanned>
+__device__ __forceinline__ void pick_request(const BeamArgs& a, PickShared<T>& sh, int r, Scanned&& scanned) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, n = a.n_out;
   const Pick<T> p{a, sh, r, n, tid, warp, lane};
   if (tid == 0) { sh.size = 0.f; sh.bound = -INFINITY; sh.count = 0; }
   if (tid < a.beams) {
@@ -545,7 +556,7 @@ __global__ void __launch_bounds__(kPickThreads, 1) beam_pick_kernel(const __grid
     a.tokens[to] = -1;
   }
   __syncthreads();
-  pdl_wait();
+  scanned();
   const float* maxima = a.maxima + (size_t)r * a.beams * a.chunks;
   const int keys = a.beams * a.chunks;
   float x[kPer];                                               // a thread's first keys stay in registers
@@ -694,6 +705,26 @@ __global__ void __launch_bounds__(kPickThreads, 1) beam_pick_kernel(const __grid
   }
 }
 
+template <typename T>
+__global__ void __launch_bounds__(kPickThreads, 1) beam_pick_kernel(const __grid_constant__ BeamArgs a) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  pick_request<T>(a, *reinterpret_cast<PickShared<T>*>(smem), blockIdx.x, [] { pdl_wait(); });
+}
+
+// Both in one launch, a cluster of CTAs a request: all of them scan, the first one ranks.
+template <typename T>
+__global__ void __launch_bounds__(kPickThreads, 1) beam_step_kernel(const __grid_constant__ BeamArgs a) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  const int r = blockIdx.x / kBeamCluster, cta = blockIdx.x % kBeamCluster, warp = threadIdx.x >> 5;
+  const int wid = cta * kPickWarps + warp, w = wid / a.parts;
+  auto scan = [&] {
+    if (w < a.beams) scan_part<T>(a, smem + sizeof(PickShared<T>) + warp * kRing, r, w, wid - w * a.parts, [] {});
+    cluster_sync();
+  };
+  if (cta == 0) pick_request<T>(a, *reinterpret_cast<PickShared<T>*>(smem), r, scan);
+  else scan();
+}
+
 // ------------------------------------------------------------------ paths
 // The way back from the last beams is a chain of maps, which may be put together in any grouping.  A cluster of
 // CTAs a request takes a tile of steps from the end, each of its threads a share of them for one beam: they walk
@@ -706,9 +737,6 @@ constexpr int kPathThreads = 1024;
 constexpr int kPathShared = 200 * 1024;
 constexpr int kNoBeam = 255;
 
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release;\n barrier.cluster.wait.acquire;" ::: "memory");
-}
 // A byte of CTA `rank`'s shared memory, at the same place as p in this one.
 __device__ __forceinline__ int of_cta(const uint8_t* p, int rank) {
   uint32_t at, v;
@@ -800,12 +828,32 @@ __global__ void __launch_bounds__(kPathThreads, 1) beam_paths_kernel(const __gri
 }
 
 template <typename T>
-cudaError_t select_t(const BeamArgs& a, cudaStream_t st) {
-  const long long warps = (long long)a.requests * a.beams * a.parts;
-  beam_scan_kernel<T><<<(unsigned)((warps + kScanWarps - 1) / kScanWarps), kScanWarps * 32, 0, st>>>(a);
-  cudaError_t e = cudaGetLastError();
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(beam_pick_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(PickShared<T>));
+cudaError_t step_t(const BeamArgs& a, cudaStream_t st) {
+  constexpr int kBytes = sizeof(PickShared<T>) + kPickWarps * kRing;
+  cudaError_t e = cudaFuncSetAttribute(beam_step_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
   if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.requests * kBeamCluster);
+  cfg.blockDim = dim3(kPickThreads);
+  cfg.dynamicSmemBytes = kBytes;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = kBeamCluster;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, beam_step_kernel<T>, a);
+}
+
+template <typename T>
+cudaError_t select_t(const BeamArgs& a, cudaStream_t st) {
+  if (a.clustered) return step_t<T>(a, st);
+  const long long warps = (long long)a.requests * a.beams * a.parts;
+  cudaError_t e = cudaFuncSetAttribute(beam_pick_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(PickShared<T>));
+  if (e != cudaSuccess) return e;
+  beam_scan_kernel<T><<<(unsigned)((warps + kScanWarps - 1) / kScanWarps), kScanWarps * 32, 0, st>>>(a);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.requests);
   cfg.blockDim = dim3(kPickThreads);

@@ -281,6 +281,7 @@ cudaError_t launch_copy_pages(const CopyPages& a, int layers, cudaStream_t st);
 // from the 32-byte boundary at or before its start; part p of a row is its chunks p, p + parts, ...
 constexpr int kBeamChunk = 512;
 constexpr int kBeamScanWarps = 48;               // warps of the scan on an SM
+constexpr int kBeamCluster = 8, kBeamClusterWarps = kBeamCluster * 32;     // of a step in one launch
 constexpr int kBeamMaxBeams = 128, kBeamMaxOut = 256;
 struct BeamArgs {
   const void* logits;
@@ -289,6 +290,7 @@ struct BeamArgs {
   const uint8_t* finished;   // [requests][beams], or null
   int requests, beams, vocab, n_out, eos, is_bf16;
   int chunks, parts;
+  int clustered;             // one launch: a cluster of CTAs a request
   uint32_t chunks_inv;       // floor((2^32 - 1) / chunks)
   float2* records;           // [requests][beams][parts]: largest logit, sum of exp(x - it)
   float* maxima;             // [requests][beams][chunks]

@@ -1529,6 +1529,14 @@ witcert_status witcert_gate_select(const float* risk, const uint8_t* repaired, i
 }
 
 // ------------------------------------------------------------------ beam search
+// A step whose requests have a cluster each and whose clusters' warps have this many chunks at most is one launch,
+// which costs the host 5.5 us less and the GPU a little more.  One launch / two, us, through the binding and in a
+// graph: 1 request of 4 beams, 32000 tokens (1 chunk a warp) 19.1 / 24.7, 7.9 / 7.6; 10 of 8 beams (2) 18.9 / 24.1, 8.9 /
+// 8.6; 1 of 4, 152001 tokens (4.6) 18.8 / 24.5, 11.2 / 8.4; 1 of 8, 131072 (8) 18.7 / 24.4, 13.1 / 9.5; 2 of 32, 50001 fp32
+// (12) 26.7 / 24.3, 24.8 / 14.5.  Clusters may take two thirds of the SMs: those of 16 requests do not all find their
+// place at once (first steps of 4 beams, 131072 tokens: 16.6 / 9.2 in a graph).
+constexpr int kClusterChunks = 5;
+
 // Checks a step and lays out its scan.
 static witcert_status beam_args(const witcert_beam_step* s, BeamArgs& a, size_t& bytes) {
   if (!s) return fail(WITCERT_EINVAL, "step must not be NULL");
@@ -1548,9 +1556,15 @@ static witcert_status beam_args(const witcert_beam_step* s, BeamArgs& a, size_t&
   const bool even = at % 32 == 0 && (s->n_requests < 2 || s->request_stride * elem % 32 == 0) &&
                     (s->n_beams < 2 || s->beam_stride * elem % 32 == 0);
   a.chunks = (int)((s->vocab + (even ? 0 : 32 / elem - 1) + (long long)kBeamChunk - 1) / kBeamChunk);
-  // a warp a chunk where the rows are few; one wave of warps, then more waves of at most nine chunks a warp
-  const long long warps = (long long)sm_count_now() * kBeamScanWarps;
-  a.parts = (int)std::min<long long>(a.chunks, std::max(warps / std::max(rows, 1ll), (a.chunks + 8ll) / 9));
+  const int sms = sm_count_now();
+  a.clustered = (long long)s->n_requests * kBeamCluster * 3 / 2 <= sms && (long long)s->n_beams * a.chunks <= kClusterChunks * kBeamClusterWarps;
+  if (a.clustered) {
+    a.parts = std::min(a.chunks, kBeamClusterWarps / s->n_beams);
+  } else {
+    // a warp a chunk where the rows are few; one wave of warps, then more waves of at most nine chunks a warp
+    const long long warps = (long long)sms * kBeamScanWarps;
+    a.parts = (int)std::min<long long>(a.chunks, std::max(warps / std::max(rows, 1ll), (a.chunks + 8ll) / 9));
+  }
   a.chunks_inv = UINT32_MAX / (uint32_t)a.chunks;
   if (rows * a.parts > INT_MAX) return fail(WITCERT_EINVAL, "too many logits (%lld rows of %d)", rows, s->vocab);
   bytes = (size_t)rows * (a.parts * sizeof(float2) + a.chunks * sizeof(float));
