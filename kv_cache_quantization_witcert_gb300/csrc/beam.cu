@@ -57,9 +57,7 @@ struct Row {
   }
   // Token of element e of chunk c (may lie outside the row at either end).
   __device__ int token(int c, int e) const { return c * kChunk + e - lead; }
-  // N words of elements from e of chunk c on, as they lie; -inf outside the row.
-  template <int N>
-  __device__ void load(int c, int e, uint32_t (&w)[N]) const { load_at(x, vocab, token(c, e), w); }
+  // N words of elements from token t on, as they lie (t's place is aligned to them); -inf outside the row.
   template <int N>
   static __device__ __forceinline__ void load_at(const T* x, int vocab, int t, uint32_t (&w)[N]) {
     constexpr int n = N * 4 / sizeof(T);
