@@ -496,12 +496,14 @@ def witcert_gate_select(risk, n_kv_heads, tau, repaired=None, selected=None, str
     return selected
 
 
-def _here(name, t):
-    """Check that a tensor lies on the current CUDA device, where the library launches."""
+def _here(name, t, *others):
+    """Check that a call's tensors lie on the current CUDA device, where the library launches."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.get_device() != torch._C._cuda_getDevice():
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    dev = torch._C._cuda_getDevice()
+    for x in (t, *others):
+        if x is not None and x.get_device() != dev:
+            raise ValueError(f"{name} and what goes with it must be on the current device (cuda:{dev}), got {x.device}")
 
 
 def witcert_beam_select(logits, scores, n_out=None, finished=None, eos=-1, out=None, stream=None):
@@ -520,7 +522,7 @@ def witcert_beam_select(logits, scores, n_out=None, finished=None, eos=-1, out=N
     if V != 1 and xs[2] != 1:
         raise ValueError(f"logits must have adjacent tokens (stride 1), got stride {xs[2]}")
     _need(("scores", scores, torch.float32, (R, W)), ("finished", finished, torch.bool, (R, W), True))
-    _here("logits", logits)
+    _here("logits", logits, scores, finished, *(out or ()))
     if out is None:
         shape = (R, max(n, 0))
         out = (_empty(stream, shape, torch.float32, dev), _empty(stream, shape, torch.int32, dev),
@@ -546,7 +548,7 @@ def witcert_beam_paths(rows, tokens, length=None, pad=-1, out=None, stream=None)
     T, R, W = (_extent(rows, i) for i in range(3))
     _need(("rows", rows, torch.int32, (T, R, W)), ("tokens", tokens, torch.int32, (T, R, W)),
           ("length", length, torch.int32, (R,), True))
-    _here("rows", rows)
+    _here("rows", rows, tokens, length, out)
     if out is None:
         out = _empty(stream, (R, W, T), torch.int32, rows.device)
     _need(("out", out, torch.int32, (R, W, T)))
