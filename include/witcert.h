@@ -86,8 +86,8 @@ typedef struct {
   int max_pages;           /* > 0: paged block store.  Each layer holds a pool of max_pages pages, a page
                               being one 16-token block of every KV head of one sequence; a per-sequence
                               page table (shared by the layers) maps a sequence's blocks to pages, taken
-                              as writes reach new blocks and given back by witcert_reset_sequence (and
-                              witcert_fork, which also lets sequences share pages), so
+                              as writes reach new blocks and given back by witcert_reset_sequence and by
+                              witcert_fork, which also lets sequences share them, so
                               sequences of different lengths share the pool instead of each reserving
                               max_tokens.  max_tokens stays the per-sequence cap.  bf16 caches only.
                               0: every sequence owns max_tokens of contiguous blocks. */
