@@ -218,7 +218,6 @@ template <typename T, class After>
 __device__ __forceinline__ void scan_part(const BeamArgs& a, uint8_t* held, int r, int w, int part, After&& after) {
   const int lane = threadIdx.x & 31;
   const uint32_t row = (uint32_t)r * a.beams + w;
-  if (!live(a.scores[row]) || (a.finished && a.finished[row])) return;
   const Row<T> x(a, r, w);
   float* maxima = a.maxima + (size_t)row * a.chunks;
   LaneSum l;
@@ -234,8 +233,15 @@ __device__ __forceinline__ void scan_part(const BeamArgs& a, uint8_t* held, int 
     ahead += a.parts;
     from += step;
   };
+  // the first chunk is on its way while the score is: 64 x 8 rows 28.8 -> 28.0 us with the ranking; first steps, where
+  // three of four rows are absent, 9.3 -> 9.5
+  fetch(0);
+  if (!live(a.scores[row]) || (a.finished && a.finished[row])) {
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    return;
+  }
 #pragma unroll
-  for (int u = 0; u < kStages - 1; ++u) fetch(u);
+  for (int u = 1; u < kStages - 1; ++u) fetch(u);
   for (int c = part; c < a.chunks;) {
 #pragma unroll
     for (int stage = 0; stage < kStages; ++stage) {
