@@ -306,7 +306,7 @@ struct PickShared {
   float base32[kBeamMaxBeams], score[kBeamMaxBeams], top[kBeamMaxBeams], log_sum[kBeamMaxBeams];
   int exponent[kBeamMaxBeams], state[kBeamMaxBeams];     // state: 0 no candidates, 1 live, 2 finished
   int count;
-  float bound, size;                             // size: the largest |base|
+  float bound, size;                             // size: the largest |score| + |log sum|
 };
 
 template <typename T>
@@ -316,10 +316,13 @@ struct Pick {
   int r, n;
   int tid, warp, lane;
 
-  // The least key in 32 bits that may belong to a key which reaches the bound: either is off by at most 2^-23 of
-  // |key| + size.
+  // The least key in 32 bits that may belong to a key which reaches the bound.  With L = e log 2 + log f the log sum,
+  // base is score - L rounded four times: e log 2 by 2^-24 (and its constant by 2^-25) of at most 2.1 |L|, the sum by
+  // 2^-24 |L|, the difference by 2^-24 of itself.  That is 2^-24 of 5.2 (|score| + |L|) however far the two cancel, so
+  // size is taken before they do: key + size bounds x - top, whose rounding and the last sum's add 2^-24 (2 |key| + size).
+  // So a key is off by less than 2^-21 (|key| + size); bound and key together by twice that, and as much is to spare.
   __device__ __forceinline__ float from() const {
-    const float f = sh.bound - 0x1p-20f * (fabsf(sh.bound) + sh.size);
+    const float f = sh.bound - 0x1p-19f * (fabsf(sh.bound) + sh.size);
     return f > -INFINITY ? f : -FLT_MAX;                       // also where that is no number
   }
   __device__ __forceinline__ static float key32(float base, float top, float x) { return fmaxf(base + (x - top), -FLT_MAX); }
@@ -592,13 +595,13 @@ __device__ __forceinline__ void pick_request(const BeamArgs& a, PickShared<T>& s
     if (state == 1 && (!(sum > 0.f) || !(fabsf(top) <= FLT_MAX))) state = 0;
     if (lane == 0 && state) {
       const bool done = state == 2;
-      const float base = done ? sh.score[w] : sh.score[w] - ((float)e * 0.693147181f + log_f);
+      const float log_sum = done ? 0.f : (float)e * 0.693147181f + log_f;
       sh.top[w] = done ? 0.f : top;
       sh.exponent[w] = done ? 0 : e;
       sh.log_sum[w] = done ? 0.f : log_f;
-      sh.base32[w] = base;
+      sh.base32[w] = sh.score[w] - log_sum;
       // non-negative floats order like their bits
-      atomicMax(reinterpret_cast<int*>(&sh.size), __float_as_int(fminf(fabsf(base), FLT_MAX)));
+      atomicMax(reinterpret_cast<int*>(&sh.size), __float_as_int(fminf(fabsf(sh.score[w]) + fabsf(log_sum), FLT_MAX)));
     }
     __syncwarp();
     if (lane == 0) sh.state[w] = state;
