@@ -178,15 +178,20 @@ __device__ __forceinline__ float largest(const uint32_t (&w)[N]) {
 
 // A lane's part of the sum of exp(x - m), m the largest logit its warp has seen.  The exponents are x log2 e - R
 // with R = m log2 e rounded once: a fused product loses nothing, and what R lost, below 2^-8 and the same for
-// every term, goes back in at the end.
+// every term, goes back in at the end.  Next to huge logits R would lose more: the exponents are (x - m) log2 e there,
+// and a maximum that passes from one kind to the other takes what R lost in or out.
 struct LaneSum {
   float m = -INFINITY, R = 0.f, sum = 0.f, lost = 0.f;         // sum + lost = sum 2^(x log2 e - R)
   bool far = false;                                            // a huge maximum: differences instead
   __device__ __forceinline__ void raise(float top) {
     const bool now = !(fabsf(top) < 0x1p16f);
-    const float to = now ? 0.f : top * kLog2e;
-    const float f = m == -INFINITY ? 1.f : far || now ? ex2((m - top) * kLog2e) : ex2(R - to);
-    sum *= f; lost *= f;                                       // before any maximum the sum is 0 (or NaN)
+    const float to = now ? 0.f : __fmul_rn(top, kLog2e);       // rounded as stored, not fused into R - to
+    float f = 1.f;                                             // before any maximum the sum is 0 (or NaN)
+    if (m > -INFINITY) {
+      const float out = far ? 0.f : __fmaf_rn(m, kLog2e, -R), in = now ? 0.f : __fmaf_rn(top, kLog2e, -to);
+      f = far || now ? ex2(__fmaf_rn(m - top, kLog2e, in - out)) : ex2(R - to);
+    }
+    sum *= f; lost *= f;
     m = top; R = to; far = now;
   }
   // Pairs of logits at a time: one instruction for two products, and for two sums.
