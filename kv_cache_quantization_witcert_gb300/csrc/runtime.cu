@@ -49,6 +49,13 @@ void ok() { g_err[0] = 0; }
 
 struct ProfPair { cudaEvent_t a, b; };
 
+// What the last call on the cache's stream left to the next one's launches.
+struct Recent {
+  bool lengths_last = false;        // the most recent launch set dlen
+  bool apart = false;               // the next launch starts after its predecessor's end: a fork, or a call that failed
+  int write_layer = -1, write_blk = 0;   // of the most recent launch when it was a write: its layer and first block
+};
+
 }  // namespace
 
 struct witcert_cache {
@@ -81,8 +88,9 @@ struct witcert_cache {
   std::vector<std::vector<int>> slen;   // per layer and sequence
   std::vector<uint64_t> write_gen, risk_gen;   // per layer: writes / resets so far; at the last metered decode
   bool ragged = false;              // sequence lengths may differ: kernels read dlen
-  bool lengths_last = false;        // the most recent launch on the cache's stream set dlen
-  bool forked = false;              // a fork was the last to change blocks: the next launch starts after its end
+  Recent recent;                    // of the calls in `capture`, or launched (0)
+  Recent launched;                  // during a capture: of the calls launched before it
+  unsigned long long capture = 0, last_capture = 0;   // the capture that the last call was part of; the last one of all
   std::vector<cudaEvent_t> gate_done;
   std::vector<char> gate_pending;
   std::vector<char> backing_lost;   // per layer: the backing store misses exact keys (gate -> EPAGEIN)
@@ -93,8 +101,6 @@ struct witcert_cache {
   uint64_t prof_n = 0, tokens_written = 0, decode_calls = 0, gate_calls = 0;
   int last_n_splits = 0;
   bool overlap = true;       // programmatic dependent launch between the cache's kernels
-  // most recent launch on the cache's stream when it was a write: its layer and first block
-  int last_write_layer = -1, last_write_blk = 0;
 };
 
 namespace {
@@ -143,12 +149,30 @@ bool order_after_gate(witcert_cache* c, int layer, cudaStream_t st) {
   return true;
 }
 
+// Begins a call's launches on st.  A captured call launches nothing: what it leaves holds within its capture, for
+// the calls behind it there, and a call outside goes by the last one that was launched.  The first of those behind a
+// capture starts after its predecessor's end, as graphs may have been launched since, and so does the first call
+// that goes on with a capture after others outside.
+void follow(witcert_cache* c, cudaStream_t st) {
+  cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+  unsigned long long id = 0;
+  if (cudaStreamGetCaptureInfo(st, &status, &id) != cudaSuccess) cudaGetLastError();
+  if (status == cudaStreamCaptureStatusNone) id = 0;
+  else if (status != cudaStreamCaptureStatusActive) id = ~0ull;       // one that has failed
+  if (id == c->capture) return;
+  if (c->capture == 0) c->launched = c->recent; else c->recent = c->launched;
+  if (id == 0 || id == c->last_capture) c->recent.apart = true;
+  c->capture = id;
+  if (id) c->last_capture = id;
+}
+
 // Whether the next launch may start before its predecessor's end.  The kernels that overlap read older
-// blocks, lengths and pages before they wait; a fork writes all of those.
+// blocks, lengths and pages before they wait; a fork writes all of those.  What the call launches has not
+// succeeded yet: the call says so with recent.apart = false.
 bool may_overlap(witcert_cache* c, bool waited) {
-  const bool after_fork = c->forked;
-  c->forked = false;
-  return c->overlap && !waited && !after_fork;
+  const bool apart = c->recent.apart;
+  c->recent.apart = true;
+  return c->overlap && !waited && !apart;
 }
 
 // Turns per position of a frequency (see rope.cuh): f / (2 pi) mod 1 in units of 2^-64, to the nearest.
@@ -511,6 +535,7 @@ static witcert_status write_impl(witcert_cache* c, int layer, const void* K, con
   std::vector<PageTaken> pages;
   if (witcert_status ps = take_pages(c, layer, n, pages)) return ps;
   auto st = static_cast<cudaStream_t>(stream);
+  follow(c, st);
   const bool waited = order_after_gate(c, layer, st);
   bool pdl = may_overlap(c, waited);
   cudaError_t e = push_pages(c, pages, st, pdl);
@@ -522,7 +547,7 @@ static witcert_status write_impl(witcert_cache* c, int layer, const void* K, con
     // a page-table update launched just before must be complete before the writers read it
     // (and a write right after another one waits for it first: a decode that follows takes only
     // the last write's blocks for unfinished, and a truncation between them makes their rows meet)
-    a.late_wait = pages.empty() && c->last_write_layer < 0;
+    a.late_wait = pages.empty() && c->recent.write_layer < 0;
     // rotated keys exist only in the writers' registers: the writers store their exact copies
     if (c->backing_host && n_tok >= kBulkBackingTokens && !rope) {
       // bulk writes copy their exact keys to the pinned backing store with the copy engines
@@ -587,9 +612,9 @@ static witcert_status write_impl(witcert_cache* c, int layer, const void* K, con
     if (e == cudaSuccess) e = flush();
     if (e != cudaSuccess) return cuda_fail(e, "ragged write launch");
   }
-  c->last_write_layer = layer;
-  c->last_write_blk = first_blk;
-  c->lengths_last = false;
+  c->recent = Recent{};
+  c->recent.write_layer = layer;
+  c->recent.write_blk = first_blk;
   for (int i = 0; i < B; ++i) c->slen[layer][i] += n[i];
   int mx = 0;
   for (int i = 0; i < B; ++i) mx = c->slen[layer][i] > mx ? c->slen[layer][i] : mx;
@@ -674,6 +699,7 @@ witcert_status witcert_reset_sequence(witcert_cache* c, int seq, void* stream) t
   if (!c) return fail(WITCERT_EINVAL, "cache is NULL");
   if (seq < 0 || seq >= c->cfg.batch) return fail(WITCERT_EINVAL, "sequence %d out of range [0, %d)", seq, c->cfg.batch);
   auto st = static_cast<cudaStream_t>(stream);
+  follow(c, st);
   // host memory first: nothing may fail between what the device and what the host is told
   std::vector<std::pair<int, int>> upd, freed;
   for (int l = 0; l < c->cfg.n_layers; ++l) upd.emplace_back(l * c->cfg.batch + seq, 0);
@@ -709,8 +735,8 @@ witcert_status witcert_reset_sequence(witcert_cache* c, int seq, void* stream) t
     c->len[l] = mx;
     ++c->write_gen[l];
   }
-  c->last_write_layer = -1;
-  c->lengths_last = true;
+  c->recent = Recent{};
+  c->recent.lengths_last = true;
   ok();
   return WITCERT_OK;
 } WITCERT_NO_THROW
@@ -733,6 +759,7 @@ witcert_status witcert_truncate(witcert_cache* c, int layer, const int32_t* leng
     }
   if (!any) { ok(); return WITCERT_OK; }
   auto st = static_cast<cudaStream_t>(stream);
+  follow(c, st);
   bool waited = false;
   for (int l = l0; l < l1; ++l) waited |= order_after_gate(c, l, st);
   // lengths that stay equal need no copy on the device
@@ -750,7 +777,8 @@ witcert_status witcert_truncate(witcert_cache* c, int layer, const int32_t* leng
         if (lengths[i] < c->slen[l][i]) upd.emplace_back(l * B + i, lengths[i]);
     if (e == cudaSuccess) e = push_lengths(c, upd, st, pdl);
     if (e != cudaSuccess) return cuda_fail(e, "sequence lengths");
-    c->lengths_last = true;
+    c->recent.lengths_last = true;
+    c->recent.apart = false;
   }
   for (int l = l0; l < l1; ++l) {
     int mx = 0;
@@ -945,9 +973,8 @@ witcert_status witcert_fork(witcert_cache* c, const int32_t* parents, const int3
   }
   if (!any) { ok(); return WITCERT_OK; }
   auto st = static_cast<cudaStream_t>(stream);
-  cudaStreamCaptureStatus capturing = cudaStreamCaptureStatusNone;
-  if (cudaStreamIsCapturing(st, &capturing) != cudaSuccess) cudaGetLastError();
-  if (capturing != cudaStreamCaptureStatusNone)
+  follow(c, st);
+  if (c->capture)
     return fail(WITCERT_ESTATE, "a fork cannot be captured: the lengths and pages on the host would not follow a replay");
   fork_moves(f);
   // host memory first: nothing may fail between what the device and what the host is told
@@ -1012,8 +1039,8 @@ witcert_status witcert_fork(witcert_cache* c, const int32_t* parents, const int3
     c->len[l] = *std::max_element(c->slen[l].begin(), c->slen[l].end());
     ++c->write_gen[l];
   }
-  c->last_write_layer = -1;
-  c->lengths_last = c->forked = true;
+  c->recent.write_layer = -1;
+  c->recent.lengths_last = c->recent.apart = true;
   ok();
   return WITCERT_OK;
 } WITCERT_NO_THROW
@@ -1049,6 +1076,7 @@ witcert_status witcert_read(witcert_cache* c, int layer, const int32_t* t0, cons
   if (!K || !V) return fail(WITCERT_EINVAL, "K and V must not be NULL");
   if (((uintptr_t)K | (uintptr_t)V) % 16) return fail(WITCERT_EINVAL, "K and V must be 16-byte aligned");
   auto st = static_cast<cudaStream_t>(stream);
+  follow(c, st);
   order_after_gate(c, layer, st);
   ReadArgs a{};
   a.s = store_args(c, layer);
@@ -1070,8 +1098,8 @@ witcert_status witcert_read(witcert_cache* c, int layer, const int32_t* t0, cons
     }
   }
   if (e != cudaSuccess) return cuda_fail(e, "read launch");
-  c->last_write_layer = -1;
-  c->lengths_last = false;
+  c->recent.write_layer = -1;
+  c->recent.lengths_last = false;
   ok();
   return WITCERT_OK;
 }
@@ -1266,6 +1294,7 @@ witcert_status witcert_attend(witcert_cache* c, int layer, const void* q, const 
   if (plan.bytes() > workspace_bytes || !workspace)
     return fail(WITCERT_EINVAL, "the workspace needs %zu bytes, got %zu", plan.bytes(), workspace ? workspace_bytes : 0);
   auto st = static_cast<cudaStream_t>(stream);
+  follow(c, st);
   order_after_gate(c, layer, st);
   uint8_t* images = static_cast<uint8_t*>(workspace);
   uint4* dither = plan.dither_tiles ? reinterpret_cast<uint4*>(images + plan.image_bytes + plan.rec_bytes) : nullptr;
@@ -1282,8 +1311,8 @@ witcert_status witcert_attend(witcert_cache* c, int layer, const void* q, const 
     cudaError_t e = attend_group(c->scheme, a, st);
     if (e != cudaSuccess) return cuda_fail(e, "attend launch");
   }
-  c->last_write_layer = -1;
-  c->lengths_last = false;
+  c->recent.write_layer = -1;
+  c->recent.lengths_last = false;
   ok();
   return WITCERT_OK;
 } WITCERT_NO_THROW
@@ -1324,7 +1353,7 @@ static void fill_decode(witcert_cache* c, int layer, const void* q, double delta
   philox_round_keys(a.seed, a.rk0, a.rk1);
   a.layer = layer;
   a.pos0 = c->cfg.pos_offset;
-  a.dirty_blk = c->last_write_layer == layer ? c->last_write_blk : INT_MAX;
+  a.dirty_blk = c->recent.write_layer == layer ? c->recent.write_blk : INT_MAX;
   float kappa = 0.f;
   const long long Sk = s_kappa > 0 ? s_kappa : S;
   if (meter && Sk > 0) {
@@ -1350,6 +1379,7 @@ witcert_status witcert_decode(witcert_cache* c, int layer, const void* q, double
   const bool meter = meter_a || meter_b || raw_a || raw_b || meter_v;
   if (meter && !(delta_req > 0.0 && delta_req <= 1.0)) return fail(WITCERT_EINVAL, "delta_req must be in (0, 1]");
   auto st = static_cast<cudaStream_t>(stream);
+  follow(c, st);
   const bool waited = order_after_gate(c, layer, st);
   DecodeArgs a{};
   fill_decode(c, layer, q, delta_req, meter, 0, a);
@@ -1372,12 +1402,11 @@ witcert_status witcert_decode(witcert_cache* c, int layer, const void* q, double
     c->prof_free.pop_back();
   }
   // the split kernel reads the sequence lengths before it waits for its predecessor
-  cudaError_t e = launch_decode(c->scheme, a, c->sm_count, st, pp.a, pp.b, may_overlap(c, waited) && !c->lengths_last);
+  cudaError_t e = launch_decode(c->scheme, a, c->sm_count, st, pp.a, pp.b, may_overlap(c, waited) && !c->recent.lengths_last);
   if (pp.a) c->prof_pending.push_back(pp);
   if (e != cudaSuccess) return cuda_fail(e, "decode launch");
-  c->lengths_last = false;
+  c->recent = Recent{};
   if (gate && meter) c->risk_gen[layer] = c->write_gen[layer];
-  c->last_write_layer = -1;
   c->last_n_splits = a.n_splits;
   ++c->decode_calls;
   ok();
@@ -1395,6 +1424,8 @@ witcert_status witcert_decode_noalloc(witcert_cache* c, int layer, const void* q
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess || dev != c->device)
     return fail(WITCERT_EINVAL, "the cache lives on device %d; make it current before this call", c->device);
+  auto st = static_cast<cudaStream_t>(stream);
+  follow(c, st);
   DecodeArgs a{};
   fill_decode(c, layer, q, delta_req, meter, 0, a);
   float* scratch = nullptr;
@@ -1405,9 +1436,8 @@ witcert_status witcert_decode_noalloc(witcert_cache* c, int layer, const void* q
   if (need > scratch_bytes)
     return fail(WITCERT_EINVAL, "batch %d x %d query heads x %d splits needs %zu bytes of split scratch; "
                 "the static array holds %zu", a.B, a.Hq, a.n_splits, need, scratch_bytes);
-  auto st = static_cast<cudaStream_t>(stream);
   const bool waited = order_after_gate(c, layer, st);
-  a.dirty_blk = c->last_write_layer == layer ? c->last_write_blk : INT_MAX;
+  a.dirty_blk = c->recent.write_layer == layer ? c->recent.write_blk : INT_MAX;
   a.part = scratch;
   const bool gate = c->cfg.max_repair_blocks > 0;
   if (gate && meter) {
@@ -1415,11 +1445,10 @@ witcert_status witcert_decode_noalloc(witcert_cache* c, int layer, const void* q
     a.risk = c->risk + (size_t)layer * a.B * a.Hq * c->nblk_max;
   }
   a.out = out; a.meter_a = meter_a; a.meter_b = meter_b; a.raw_a = raw_a; a.raw_b = raw_b; a.meter_v = meter_v;
-  e = launch_decode(c->scheme, a, c->sm_count, st, nullptr, nullptr, may_overlap(c, waited) && !c->lengths_last);
+  e = launch_decode(c->scheme, a, c->sm_count, st, nullptr, nullptr, may_overlap(c, waited) && !c->recent.lengths_last);
   if (e != cudaSuccess) return cuda_fail(e, "decode launch");
-  c->lengths_last = false;
+  c->recent = Recent{};
   if (gate && meter) c->risk_gen[layer] = c->write_gen[layer];
-  c->last_write_layer = -1;
   c->last_n_splits = a.n_splits;
   ++c->decode_calls;
   ok();
@@ -1435,6 +1464,7 @@ witcert_status witcert_decode_partial(witcert_cache* c, int layer, const void* q
                                            s_total, c->len[layer]);
   if (c->ragged) return fail(WITCERT_ESTATE, "context-parallel shards hold equal-length sequences");
   auto st = static_cast<cudaStream_t>(stream);
+  follow(c, st);
   const bool waited = order_after_gate(c, layer, st);
   DecodeArgs a{};
   fill_decode(c, layer, q, delta_req, true, s_total, a);
@@ -1443,7 +1473,8 @@ witcert_status witcert_decode_partial(witcert_cache* c, int layer, const void* q
   a.risk_raw = c->risk_raw;      // a gated cache's split kernel writes block risks; the merge keeps none (no a.risk)
   cudaError_t e = launch_decode(c->scheme, a, c->sm_count, st, nullptr, nullptr, may_overlap(c, waited));
   if (e != cudaSuccess) return cuda_fail(e, "decode launch");
-  c->last_write_layer = -1;
+  c->recent.write_layer = -1;
+  c->recent.apart = false;
   c->last_n_splits = a.n_splits;
   ++c->decode_calls;
   ok();
@@ -1736,6 +1767,7 @@ witcert_status witcert_export(witcert_cache* c, int layer, witcert_export_kind w
   if (what == WITCERT_X_V_WITNESS && !c->vwit) return fail(WITCERT_EINVAL, "value witnesses need a cache created with v_witness");
   if (!dst || bytes < need) return fail(WITCERT_EINVAL, "export needs %zu bytes, got %zu", need, bytes);
   auto st = static_cast<cudaStream_t>(stream);
+  follow(c, st);
   order_after_gate(c, layer, st);
   ExportArgs a{};
   a.blocks = c->blocks + layer * c->layer_blocks;
@@ -1748,7 +1780,7 @@ witcert_status witcert_export(witcert_cache* c, int layer, witcert_export_kind w
   a.what = (int)what;
   cudaError_t e = launch_export(a, st);
   if (e != cudaSuccess) return cuda_fail(e, "export launch");
-  c->last_write_layer = -1;
+  c->recent.write_layer = -1;
   ok();
   return WITCERT_OK;
 }
