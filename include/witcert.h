@@ -267,7 +267,9 @@ witcert_status witcert_attend_workspace(const witcert_cache* cache, int layer, c
  * copied.  Block risks become stale.  EINVAL for a bad parent, a negative length, a KIVI2 cut that would reopen a
  * finished block (as for witcert_truncate), and for a gated cache: repairs and the backing store belong to
  * one sequence; ESTATE on a stream that is being captured (a replay would move the device's sequences
- * alone).  Asynchronous on `stream`. */
+ * alone).  Other calls that were captured before keep the lengths of their capture, except decodes of a batch
+ * whose lengths differed then: those read the present ones, up to the longest of their capture.  In a paged cache do
+ * not replay the former where a fork or a reset has taken pages that they read.  Asynchronous on `stream`. */
 witcert_status witcert_fork(witcert_cache* cache, const int32_t* parents, const int32_t* lengths, void* stream);
 
 /* Empty sequence `seq` in every layer so the slot can serve a new request (continuous

@@ -88,6 +88,7 @@ struct witcert_cache {
   std::vector<std::vector<int>> slen;   // per layer and sequence
   std::vector<uint64_t> write_gen, risk_gen;   // per layer: writes / resets so far; at the last metered decode
   bool ragged = false;              // sequence lengths may differ: kernels read dlen
+  bool lengths_held = false;        // a captured decode reads dlen: it follows every change, also while lengths are equal
   Recent recent;                    // of the calls in `capture`, or launched (0)
   Recent launched;                  // during a capture: of the calls launched before it
   unsigned long long capture = 0, last_capture = 0;   // the capture that the last call was part of; the last one of all
@@ -476,7 +477,7 @@ static cudaError_t push_pages(witcert_cache* c, const std::vector<PageTaken>& ta
 
 // From now on the sequences' lengths may differ: the device gets every layer's lengths.
 static cudaError_t enter_ragged(witcert_cache* c, cudaStream_t st, bool& pdl) {
-  if (c->ragged) return cudaSuccess;
+  if (c->ragged || c->lengths_held) { c->ragged = true; return cudaSuccess; }
   std::vector<std::pair<int, int>> upd;
   for (int l = 0; l < c->cfg.n_layers; ++l)
     for (int i = 0; i < c->cfg.batch; ++i) upd.emplace_back(l * c->cfg.batch + i, c->slen[l][i]);
@@ -547,7 +548,7 @@ static witcert_status write_impl(witcert_cache* c, int layer, const void* K, con
     // a page-table update launched just before must be complete before the writers read it
     // (and a write right after another one waits for it first: a decode that follows takes only
     // the last write's blocks for unfinished, and a truncation between them makes their rows meet)
-    a.late_wait = pages.empty() && c->recent.write_layer < 0;
+    a.late_wait = pages.empty() && c->recent.write_layer < 0 && !c->lengths_held;
     // rotated keys exist only in the writers' registers: the writers store their exact copies
     if (c->backing_host && n_tok >= kBulkBackingTokens && !rope) {
       // bulk writes copy their exact keys to the pinned backing store with the copy engines
@@ -559,6 +560,11 @@ static witcert_status write_impl(witcert_cache* c, int layer, const void* K, con
       }
       a.backing = nullptr;
       pdl = false;                     // the copies sit between this write and its predecessor
+    }
+    if (c->lengths_held) {
+      std::vector<std::pair<int, int>> upd;
+      for (int i = 0; i < B; ++i) upd.emplace_back(layer * B + i, t0 + n_tok);
+      if ((e = push_lengths(c, upd, st, pdl)) != cudaSuccess) return cuda_fail(e, "sequence lengths");
     }
     e = rope ? launch_write_rope(c->scheme, a, rp, st, pdl) : launch_write(c->scheme, a, st, pdl);
     if (e != cudaSuccess) return cuda_fail(e, "write launch");
@@ -768,9 +774,9 @@ witcert_status witcert_truncate(witcert_cache* c, int layer, const int32_t* leng
     for (int i = 1; i < B && uniform; ++i)
       uniform = std::min(c->slen[l][i], (int)lengths[i]) == std::min(c->slen[l][0], (int)lengths[0]);
   cudaError_t e = cudaSuccess;
-  if (!uniform) {
+  if (!uniform || c->lengths_held) {
     bool pdl = may_overlap(c, waited);
-    e = enter_ragged(c, st, pdl);
+    if (!uniform) e = enter_ragged(c, st, pdl);
     std::vector<std::pair<int, int>> upd;
     for (int l = l0; l < l1; ++l)
       for (int i = 0; i < B; ++i)
@@ -989,6 +995,7 @@ witcert_status witcert_fork(witcert_cache* c, const int32_t* parents, const int3
   std::vector<int32_t> kept(c->table ? c->nblk_max : 0);
   cudaError_t e = cudaSuccess;
   bool pdl = false;
+  const bool lens = !equal || c->lengths_held;               // lengths that stay equal need no copy on the device
   if (!equal) e = enter_ragged(c, st, pdl);
   MoveRows rows{};
   auto stream_of = [&](void* base, size_t layer_pitch, size_t head_pitch, int unit, int count) {
@@ -1005,9 +1012,9 @@ witcert_status witcert_fork(witcert_cache* c, const int32_t* parents, const int3
     stream_of(c->kivi_tail, layer_rows(c) * kBlk * kD * sizeof(float), kBlk * kD * sizeof(float), kD * sizeof(float), 1);
   MoveInts ints{};
   ints.table = c->table;
-  ints.lens = equal ? nullptr : c->dlen;
+  ints.lens = lens ? c->dlen : nullptr;
   ints.nblk_max = c->table ? c->nblk_max : 0;
-  ints.layers = equal ? 0 : L;
+  ints.layers = lens ? L : 0;
   ints.B = B;
   for (size_t k = 0; k + 1 < f.launches.size() && e == cudaSuccess; ++k) {
     const size_t m0 = f.launches[k], n = f.launches[k + 1] - m0;
@@ -1406,6 +1413,7 @@ witcert_status witcert_decode(witcert_cache* c, int layer, const void* q, double
   if (pp.a) c->prof_pending.push_back(pp);
   if (e != cudaSuccess) return cuda_fail(e, "decode launch");
   c->recent = Recent{};
+  if (c->capture && a.seq_len) c->lengths_held = true;
   if (gate && meter) c->risk_gen[layer] = c->write_gen[layer];
   c->last_n_splits = a.n_splits;
   ++c->decode_calls;
@@ -1448,6 +1456,7 @@ witcert_status witcert_decode_noalloc(witcert_cache* c, int layer, const void* q
   e = launch_decode(c->scheme, a, c->sm_count, st, nullptr, nullptr, may_overlap(c, waited) && !c->recent.lengths_last);
   if (e != cudaSuccess) return cuda_fail(e, "decode launch");
   c->recent = Recent{};
+  if (c->capture && a.seq_len) c->lengths_held = true;
   if (gate && meter) c->risk_gen[layer] = c->write_gen[layer];
   c->last_n_splits = a.n_splits;
   ++c->decode_calls;
