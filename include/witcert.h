@@ -259,7 +259,7 @@ witcert_status witcert_attend_workspace(const witcert_cache* cache, int layer, c
  * them where that is more; lengths NULL: all) of what sequence parents[i] held before the call; -1: empty.
  * parents and lengths are host [batch]; any map, in place.  A sequence that is its own parent is cut to its
  * length, and in a paged cache gives back the pages behind it.  What the next tokens, decodes, attends, reads
- * and exports of i see is what they would see of a sequence written with those tokens.
+ * and exports of i see within its length is what they would see of a sequence written with those tokens.
  * Contiguous caches copy blocks; paged ones share pages: a page belongs to every sequence that refers to
  * it, goes back to the pool when none does, and an append to a page that others hold first gives the
  * sequence a copy of its own, in all layers (the append is ENOMEM if the pool has no page for it, with
@@ -500,7 +500,7 @@ typedef enum {
  *   WITCERT_X_BLOCK_RISK        float [batch][n_q_heads][nblk] (last decode; gate enabled)
  *   WITCERT_X_V_WITNESS         fp16 [batch][len][n_kv_heads] (v_witness caches)
  * nblk = ceil(len/16); len is the longest sequence's.  Rows past a shorter sequence's length are zero
- * where a paged store holds no page for them, unspecified elsewhere.  Asynchronous on `stream`. */
+ * where a paged store holds no page for them and among value witnesses, unspecified elsewhere.  Asynchronous on `stream`. */
 witcert_status witcert_export(witcert_cache* cache, int layer, witcert_export_kind what,
                               void* dst, size_t bytes, void* stream);
 

@@ -96,7 +96,10 @@ __global__ void export_kernel(const ExportArgs a, size_t n) {
     case X_VW: {  // [B][S][Hkv]
       const int h = idx % a.Hkv, t = (idx / a.Hkv) % a.S;
       const int i = idx / ((size_t)a.Hkv * a.S);
-      reinterpret_cast<__half*>(a.dst)[idx] = a.vwit[(((size_t)i * a.Hkv + h) * a.nblk_max + (t >> 4)) * kBlk + (t & 15)];
+      // rows past the sequence's end may be an old occupant's
+      const bool held = !a.seq_len || t < a.seq_len[i];
+      reinterpret_cast<__half*>(a.dst)[idx] =
+          held ? a.vwit[(((size_t)i * a.Hkv + h) * a.nblk_max + (t >> 4)) * kBlk + (t & 15)] : __float2half_rn(0.f);
       break;
     }
   }

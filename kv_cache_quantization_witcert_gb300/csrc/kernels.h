@@ -316,6 +316,7 @@ struct ExportArgs {
   const int32_t* slots;
   const float* risk;
   const __half* vwit;        // layer base [B][Hkv][nblk_max][16], or null
+  const int* seq_len;        // [B], or null: S each
   void* dst;
   int what;
 };

@@ -954,13 +954,13 @@ witcert_status witcert_fork(witcert_cache* c, const int32_t* parents, const int3
   const int B = c->cfg.batch, L = c->cfg.n_layers;
   ForkPlan f;
   f.from.resize(B); f.cap.assign(B, -1); f.blocks.assign(B, 0); f.tail.assign(B, 0);
-  bool any = false, emptied = false;
+  bool any = false;
   for (int i = 0; i < B; ++i) {
     const int p = parents[i];
     if (p < -1 || p >= B) return fail(WITCERT_EINVAL, "the parent of sequence %d must be in [-1, %d) (got %d)", i, B, p);
     if (lengths && p >= 0 && lengths[i] < 0) return fail(WITCERT_EINVAL, "lengths must be >= 0 (sequence %d: %d)", i, lengths[i]);
     f.from[i] = p;
-    if (p < 0) { any = emptied = true; f.cap[i] = 0; continue; }
+    if (p < 0) { any = true; f.cap[i] = 0; continue; }
     const int cap = lengths ? lengths[i] : INT_MAX;
     bool cut = false;
     for (int l = 0; l < L; ++l) {
@@ -1033,11 +1033,6 @@ witcert_status witcert_fork(witcert_cache* c, const int32_t* parents, const int3
     if (rows.n_streams) e = launch_move_rows(rows, L, c->cfg.n_kv_heads, st);
     if (e == cudaSuccess && (ints.table || ints.lens)) e = launch_move_ints(ints, st);
   }
-  // an export is as long as the longest sequence: no value witness of the old occupant shows in it
-  const size_t vrows = (size_t)c->cfg.n_kv_heads * backing_rows(c);
-  for (int i = 0; i < B && emptied && c->vwit; ++i)
-    for (int l = 0; l < L && f.from[i] < 0 && e == cudaSuccess; ++l)
-      e = cudaMemsetAsync(c->vwit + l * vwit_layer(c) + (size_t)i * vrows, 0, vrows * sizeof(__half), st);
   if (e != cudaSuccess) return cuda_fail(e, "fork");
   if (c->table) fork_table(c, f, kept);
   c->slen.swap(slen);
@@ -1784,6 +1779,7 @@ witcert_status witcert_export(witcert_cache* c, int layer, witcert_export_kind w
   a.slots = c->slots ? c->slots + layer * layer_rows(c) * c->nblk_max : nullptr;
   a.risk = c->risk ? c->risk + (size_t)layer * B * Hq * c->nblk_max : nullptr;
   a.vwit = c->vwit ? c->vwit + layer * vwit_layer(c) : nullptr;
+  a.seq_len = c->ragged ? c->dlen + (size_t)layer * B : nullptr;
   a.table = c->table;
   a.dst = dst;
   a.what = (int)what;
