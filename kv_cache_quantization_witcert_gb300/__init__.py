@@ -522,16 +522,16 @@ def witcert_beam_select(logits, scores, n_out=None, finished=None, eos=-1, out=N
     if V != 1 and xs[2] != 1:
         raise ValueError(f"logits must have adjacent tokens (stride 1), got stride {xs[2]}")
     _need(("scores", scores, torch.float32, (R, W)), ("finished", finished, torch.bool, (R, W), True))
+    if out is not None:
+        if not isinstance(out, (tuple, list)) or len(out) != 4:
+            raise ValueError("out needs a tuple of four tensors (scores, rows, tokens, finished)")
+        _need(*((name, t, dt, (R, n)) for name, t, dt in zip(("out scores", "rows", "tokens", "out finished"), out,
+                                                            (torch.float32, torch.int32, torch.int32, torch.bool))))
     _here("logits", logits, scores, finished, *(out or ()))
     if out is None:
         shape = (R, max(n, 0))
         out = (_empty(stream, shape, torch.float32, dev), _empty(stream, shape, torch.int32, dev),
                _empty(stream, shape, torch.int32, dev), _empty(stream, shape, torch.bool, dev))
-    else:
-        if len(out) != 4:
-            raise ValueError(f"out needs four tensors (scores, rows, tokens, finished), got {len(out)}")
-        _need(*((name, t, dt, (R, n)) for name, t, dt in zip(("out scores", "rows", "tokens", "out finished"), out,
-                                                            (torch.float32, torch.int32, torch.int32, torch.bool))))
     step = _lib.witcert_beam_step(BF16 if logits.dtype == torch.bfloat16 else F32, R, W, V, n, int(eos), logits.data_ptr(),
                                   xs[0], xs[1], scores.data_ptr(), _ptr(finished), *[t.data_ptr() for t in out])
     size = 12 * R * W * (V // 512 + 2)                     # what witcert_beam_workspace says is at most this
@@ -547,11 +547,10 @@ def witcert_beam_paths(rows, tokens, length=None, pad=-1, out=None, stream=None)
     witcert_beam_paths in include/witcert.h)."""
     T, R, W = (_extent(rows, i) for i in range(3))
     _need(("rows", rows, torch.int32, (T, R, W)), ("tokens", tokens, torch.int32, (T, R, W)),
-          ("length", length, torch.int32, (R,), True))
+          ("length", length, torch.int32, (R,), True), ("out", out, torch.int32, (R, W, T), True))
     _here("rows", rows, tokens, length, out)
     if out is None:
         out = _empty(stream, (R, W, T), torch.int32, rows.device)
-    _need(("out", out, torch.int32, (R, W, T)))
     check(load().witcert_beam_paths(_ptr(rows), _ptr(tokens), T, R, W, _ptr(length), int(pad), _ptr(out),
                                     _stream_ptr(stream)), "witcert_beam_paths")
     return out
