@@ -774,7 +774,7 @@ __global__ void __launch_bounds__(kPathThreads, 1) beam_paths_kernel(const __gri
   int32_t* out = a.out + (size_t)r * W * a.steps;
   // 32 steps of a beam a warp at a time: fn(beam, step in 0 .. count - 1)
   auto along_time = [&](int count, auto&& fn) {
-    const int tasks = (count + 31) / 32 * W;
+    const int tasks = (int)((count + 31u) / 32) * W;           // count up to 2^31 - 1
 #pragma unroll 4
     for (int k = tid / 32; k < tasks; k += kPathThreads / 32) {
       const int t = k / W * 32 + tid % 32;
@@ -893,7 +893,7 @@ cudaError_t launch_beam_paths(PathArgs& a, int sm_count, cudaStream_t st) {
   // by 4 (256 CTAs); 16 of 4 beams and 512 steps (2 by 1) 5.3, 5.6, 5.6, 11.1
   a.ctas = 1;
   while (a.ctas < 8 && 2 * a.ctas * (long long)a.requests <= sm_count && 2 * a.ctas * 4 * (kPathThreads >> a.log_beams) <= a.steps) a.ctas *= 2;
-  a.tile = std::min(kPathShared / (a.beams * 9) - 1, (a.steps + a.ctas - 1) / a.ctas);
+  a.tile = std::min(kPathShared / (a.beams * 9) - 1, (a.steps - 1) / a.ctas + 1);
   const int bytes = a.tile * a.beams * 5 + a.beams * (a.tile | 1) * 4;
   if (bytes > 44 * 1024) {
     cudaError_t e = cudaFuncSetAttribute(beam_paths_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPathShared);
