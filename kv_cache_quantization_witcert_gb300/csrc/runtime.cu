@@ -167,6 +167,15 @@ void follow(witcert_cache* c, cudaStream_t st) {
   if (id) c->last_capture = id;
 }
 
+// Behind a call on st whose kernels start after their predecessor's end, the next launch has no append or lengths of the
+// call before to mind.
+void launched_apart(witcert_cache* c, cudaStream_t st) {
+  if (c->recent.write_layer < 0 && !c->recent.lengths_last) return;
+  follow(c, st);
+  c->recent.write_layer = -1;
+  c->recent.lengths_last = false;
+}
+
 // Whether the next launch may start before its predecessor's end.  The kernels that overlap read older
 // blocks, lengths and pages before they wait; a fork writes all of those.  What the call launches has not
 // succeeded yet: the call says so with recent.apart = false.
@@ -1083,7 +1092,6 @@ witcert_status witcert_read(witcert_cache* c, int layer, const int32_t* t0, cons
   if (!K || !V) return fail(WITCERT_EINVAL, "K and V must not be NULL");
   if (((uintptr_t)K | (uintptr_t)V) % 16) return fail(WITCERT_EINVAL, "K and V must be 16-byte aligned");
   auto st = static_cast<cudaStream_t>(stream);
-  follow(c, st);
   order_after_gate(c, layer, st);
   ReadArgs a{};
   a.s = store_args(c, layer);
@@ -1105,8 +1113,7 @@ witcert_status witcert_read(witcert_cache* c, int layer, const int32_t* t0, cons
     }
   }
   if (e != cudaSuccess) return cuda_fail(e, "read launch");
-  c->recent.write_layer = -1;
-  c->recent.lengths_last = false;
+  launched_apart(c, st);
   ok();
   return WITCERT_OK;
 }
@@ -1301,7 +1308,6 @@ witcert_status witcert_attend(witcert_cache* c, int layer, const void* q, const 
   if (plan.bytes() > workspace_bytes || !workspace)
     return fail(WITCERT_EINVAL, "the workspace needs %zu bytes, got %zu", plan.bytes(), workspace ? workspace_bytes : 0);
   auto st = static_cast<cudaStream_t>(stream);
-  follow(c, st);
   order_after_gate(c, layer, st);
   uint8_t* images = static_cast<uint8_t*>(workspace);
   uint4* dither = plan.dither_tiles ? reinterpret_cast<uint4*>(images + plan.image_bytes + plan.rec_bytes) : nullptr;
@@ -1318,8 +1324,7 @@ witcert_status witcert_attend(witcert_cache* c, int layer, const void* q, const 
     cudaError_t e = attend_group(c->scheme, a, st);
     if (e != cudaSuccess) return cuda_fail(e, "attend launch");
   }
-  c->recent.write_layer = -1;
-  c->recent.lengths_last = false;
+  launched_apart(c, st);
   ok();
   return WITCERT_OK;
 } WITCERT_NO_THROW
@@ -1776,7 +1781,6 @@ witcert_status witcert_export(witcert_cache* c, int layer, witcert_export_kind w
   if (what == WITCERT_X_V_WITNESS && !c->vwit) return fail(WITCERT_EINVAL, "value witnesses need a cache created with v_witness");
   if (!dst || bytes < need) return fail(WITCERT_EINVAL, "export needs %zu bytes, got %zu", need, bytes);
   auto st = static_cast<cudaStream_t>(stream);
-  follow(c, st);
   order_after_gate(c, layer, st);
   ExportArgs a{};
   a.blocks = c->blocks + layer * c->layer_blocks;
@@ -1790,7 +1794,7 @@ witcert_status witcert_export(witcert_cache* c, int layer, witcert_export_kind w
   a.what = (int)what;
   cudaError_t e = launch_export(a, st);
   if (e != cudaSuccess) return cuda_fail(e, "export launch");
-  c->recent.write_layer = -1;
+  if (need > 0) launched_apart(c, st);                        // nothing was launched for an empty layer
   ok();
   return WITCERT_OK;
 }

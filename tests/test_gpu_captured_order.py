@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import kv_cache_quantization_witcert_gb300 as wc
+from kv_cache_quantization_witcert_gb300 import _lib
 
 pytestmark = pytest.mark.gpu
 
@@ -78,6 +79,26 @@ def test_what_follows_a_fork():
     assert first_edge(decode) == 0
     c.witcert_write_ragged(0, one[0], one[0], [0, 1])
     assert first_edge(decode) == 1
+
+
+def test_an_export_of_nothing_launches_nothing():
+    """What it follows still is the last launch: the resets' lengths, that a decode reads at once."""
+    c = wc.Cache(1, 4, 2, 2, 64, "int8_rtn")
+    k, x = rows(40).view(2, 20, 2, 128), torch.empty(64, device="cuda")
+    q, out, dst = rows(2, 4), torch.empty(2, 4, 128, device="cuda"), torch.empty(64, dtype=torch.uint8, device="cuda")
+
+    def decode():
+        x.fill_(1.0)
+        c.witcert_decode(0, q, 1e-2, out)
+
+    c.witcert_write(0, k, k)
+    c.witcert_export(0, _lib.X_K_CODES, torch.empty(2 * 20 * 2 * 128, dtype=torch.uint8, device="cuda"))
+    assert first_edge(decode) == 1
+    for i in range(2):
+        c.witcert_reset_sequence(i)
+    c.witcert_export(0, _lib.X_K_CODES, dst)
+    assert first_edge(decode) == 0
+    torch.cuda.synchronize()
 
 
 def test_calls_outside_a_capture_in_its_middle():
