@@ -408,7 +408,9 @@ witcert_status witcert_gate_select(const float* risk, const uint8_t* repaired, i
  * the score scores[row] + x_token - log sum exp x; a finished one only itself, as token `eos` with its own
  * score.  No candidates come from a row whose score is not finite (an absent beam), from one that has no
  * softmax (+inf or NaN among its logits, or nothing but -inf), or of a logit of -inf.  Candidates
- * are ordered by score (formed in 64 bits; sums of exponentials in fp32), then row, then logit, then token.
+ * are ordered by score, then row, then logit, then token.  Scores are formed in 64 bits from a log sum whose terms
+ * are fp32: it is off by up to 2^-18 + 2^-23 (log vocab + 1), alike for all candidates of a row.  So candidates of
+ * different rows whose scores are closer than twice that may change places; a row's own never do.
  * rows, tokens, out_scores (device [n_requests][n_out]) take the row a candidate continues, its token and
  * score; places for which there is no candidate get -1, -1 and -inf.  out_finished, if given, says whether a
  * candidate's row had finished or its token is eos.  With n_out = n_beams, rows serve as witcert_fork's

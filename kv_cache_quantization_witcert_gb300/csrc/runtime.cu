@@ -835,10 +835,10 @@ static MoveOp fork_move(const ForkPlan& f, int src, int dst, int like, bool rows
 }
 
 // The moves of a fork in an order in which none reads what an earlier one wrote, one connected set of
-// sequences (a request's beams) after another.  First the sequences that nobody reads any more, source by source, which frees their sources in turn; what is left are
-// cycles, each of which saves one row, moves the others up and hands the saved one out.  A launch holds
-// kMovesPerLaunch moves; a cycle that crosses its end is cut into two that share a sequence, the second
-// of which finds there what the first one saved.
+// sequences (a request's beams) after another.  First the sequences that nobody reads any more, source by
+// source, which frees their sources in turn; what is left are cycles, each of which saves one row, moves
+// the others up and hands the saved one out.  A launch holds kMovesPerLaunch moves; a cycle that crosses
+// its end is cut into two that share a sequence, the second of which finds there what the first one saved.
 static void fork_moves(ForkPlan& f) {
   const int B = (int)f.from.size();
   std::vector<int> readers(B, 0), first(B + 1, 0), kids, ready;
